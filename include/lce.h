@@ -49,7 +49,8 @@ typedef enum {
     LCE_ERR_HIP = 3
 } lce_status;
 
-typedef enum { LCE_F32 = 0, LCE_BF16 = 1 } lce_dtype;
+/* LCE_E4M3 (8-bit floats, 4 exponent and 3 mantissa bits, largest 448): only where a call names it. */
+typedef enum { LCE_F32 = 0, LCE_BF16 = 1, LCE_E4M3 = 2 } lce_dtype;
 
 typedef enum { LCE_RED_NONE = 0, LCE_RED_MEAN = 1, LCE_RED_SUM = 2 } lce_reduction;
 
@@ -339,6 +340,107 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
                              lce_reduction reduction, const float *grad_out, int64_t chunk_tokens, const float *lse,
                              const float *one_minus_py, const int64_t *counts, void *grad_hidden, float *grad_weight,
                              void *workspace, size_t workspace_bytes, hipStream_t stream, hipStream_t aux_stream);
+
+/*
+ * ---- around the cross-entropy: the final norm, the rules on its logits ------
+ *
+ * Row operations next to those above: what forms `hidden` (or the 8-bit operand
+ * of lce_linear) and what a serving step does to logits before lce_ce_argmax or
+ * lce_ce_stats reads them.  Matrices are row-major with a row stride in elements;
+ * columns past the width are neither read nor written.  Any alignment of the
+ * element's size works; rows that start on 16 bytes, with strides of whole 16
+ * bytes, are read and written 16 bytes at a time.  An output may be the same
+ * buffer as an input of its type, at the same place and stride; other overlap is
+ * not allowed.  n == 0 is valid.
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   s_ij   = x_ij + residual_ij, rounded to dtype (s = x without a residual)
+ *   rstd_i = 1 / sqrt(mean_j s_ij^2 + eps)
+ *   y_ij   = s_ij rstd_i (weight_j + weight_offset)
+ * with y taken from the rounded s, the rows a later reader and the backward see.
+ * With y_dtype LCE_E4M3, y holds e4m3(y_ij / scale_i) and scale_i = max_j |y_ij| /
+ * 448 (1 for a row of zeros, at least 2^-126).  Sums are fp32.  A row that holds
+ * an infinity or a NaN gives what that arithmetic gives, in that row alone.
+ *   x, residual   device, dtype F32 or BF16; residual may be NULL.
+ *   weight        device [H] F32 or BF16, or NULL (ones, offset not added).
+ *   sum           device, dtype, or NULL: s.
+ *   y             device, y_dtype: dtype or LCE_E4M3.
+ *   scale         device fp32 [n], required with LCE_E4M3, else ignored.
+ *   rstd          device fp32 [n] or NULL: kept for the backward.
+ * H is 1 to 16384 (LCE_ERR_UNSUPPORTED above).
+ */
+lce_status lce_rms_norm(const void *x, int64_t ldx, lce_dtype dtype, const void *residual, int64_t ldr,
+                        const void *weight, lce_dtype weight_dtype, float weight_offset, float eps, int64_t n,
+                        int64_t H, void *sum, int64_t lds, void *y, int64_t ldy, lce_dtype y_dtype, float *scale,
+                        float *rstd, hipStream_t stream);
+
+/* Bytes of workspace lce_rms_norm_backward needs for grad_weight: 4 H min(n, 1024). */
+size_t lce_rms_norm_workspace_bytes(int64_t n, int64_t H);
+
+/*
+ * Backward of lce_rms_norm (y in dtype).  With a_j = grad_y_ij (weight_j +
+ * weight_offset):
+ *   grad_x_ij     = rstd_i (a_j - s_ij rstd_i^2 mean_k(a_k s_ik)) + grad_sum_ij
+ *   grad_weight_j = sum_i grad_y_ij s_ij rstd_i
+ * grad_x is the gradient of x and of the residual alike.
+ *   grad_y, s     device, dtype: the upstream gradient, and the sum (x without a
+ *                 residual).   rstd  device fp32 [n] of the forward.
+ *   grad_sum      device, dtype, or NULL: upstream gradient of the sum.
+ *   grad_x        device, dtype, required.
+ *   grad_weight   device [H] F32 or BF16 (grad_weight_dtype), or NULL; overwritten.
+ *   workspace     device, 16-byte aligned, lce_rms_norm_workspace_bytes(n, H)
+ *                 bytes; may be NULL without grad_weight.  Clobbered; calls that
+ *                 share it must not run at the same time.
+ * Sums are fp32 in a fixed order: the same inputs give the same bits on a device.
+ */
+lce_status lce_rms_norm_backward(const void *grad_y, int64_t ldg, const void *s, int64_t lds, lce_dtype dtype,
+                                 const void *weight, lce_dtype weight_dtype, float weight_offset, const float *rstd,
+                                 const void *grad_sum, int64_t ldgs, int64_t n, int64_t H, void *grad_x, int64_t ldgx,
+                                 void *grad_weight, lce_dtype grad_weight_dtype, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Rules on logits before a token is drawn, in place or into `out`.  For row i and
+ * token j, with c the times j stands among the generated tokens of row i's
+ * history and `seen` that it stands in the history at all, in this order (fp32,
+ * rounded to dtype once):
+ *   z = softcap > 0 ? softcap tanh(x / softcap) : x
+ *   z = seen ? (z > 0 ? z / repetition_i : z repetition_i) : z
+ *   z = c > 0 ? z - frequency_i c - presence_i : z
+ *   z = z + the last bias_values entry of row i whose id is j, if there is one
+ *   z = temperature_i > 0 ? z / temperature_i : z
+ *   out_ij = j allowed for row i ? z : mask_value
+ *   logits, out     device [n, ldx] / [n, ldo], dtype F32 or BF16; may be the same.
+ *   history         device token ids [n, L], row stride ldh (0: one list for all
+ *                   rows), or NULL.  Ids outside [0, V) are padding.
+ *   history_lens    device int64 [n] or NULL (all L), cut to [0, L]: how many ids
+ *                   of the row count.   prompt_lens  device int64 [n] or NULL (0):
+ *                   the first that many are the prompt, the rest generated.
+ *   bias_ids, bias_values  device [n, B] ids and fp32, row strides ldbi, ldbv
+ *                   (0: one list for all rows), or both NULL.  Ids outside [0, V)
+ *                   are padding.
+ *   ids_are_64      whether history and bias_ids are int64 (else int32).
+ *   repetition, presence, frequency, temperature  device fp32 [n] or NULL (off).
+ *   allowed         device uint32 [mask_count, ldm], or NULL: bit j % 32 of word
+ *                   j / 32 says that token j is allowed.  Bits past V are ignored.
+ *   mask_rows       device int64 [n] or NULL (row i uses mask i): the mask of a
+ *                   row; outside [0, mask_count) the row has none.
+ *   mask_value      what a token that is not allowed gets, whatever its logit was
+ *                   (a NaN included): -infinity as a rule.  A row that allows
+ *                   nothing is mask_value throughout.  lce_ce_argmax takes such
+ *                   rows as they are; lce_ce_stats and the losses need finite
+ *                   logits of moderate size, so where those read the result give
+ *                   -1e4 (e^-1e4 is 0 next to any other logit, and sums stay small).
+ */
+lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, int64_t n, int64_t V,
+                              const void *history, int64_t ldh, int64_t L, const int64_t *history_lens,
+                              const int64_t *prompt_lens, const void *bias_ids, int64_t ldbi, const float *bias_values,
+                              int64_t ldbv, int64_t B, int ids_are_64, const float *repetition, const float *presence,
+                              const float *frequency, const float *temperature, const uint32_t *allowed, int64_t ldm,
+                              int64_t mask_count, const int64_t *mask_rows, float mask_value, float softcap, void *out,
+                              int64_t ldo, hipStream_t stream);
 
 /*
  * Text of the most recent error on the calling thread ("" if none).  Valid

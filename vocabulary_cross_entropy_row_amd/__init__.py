@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblce.so")
 
 LCE_OK, LCE_ERR_INVALID_ARG, LCE_ERR_UNSUPPORTED, LCE_ERR_HIP = 0, 1, 2, 3
-LCE_F32, LCE_BF16 = 0, 1
+LCE_F32, LCE_BF16, LCE_E4M3 = 0, 1, 2
 LCE_RED_NONE, LCE_RED_MEAN, LCE_RED_SUM = 0, 1, 2
 REDUCTIONS = {"none": LCE_RED_NONE, "mean": LCE_RED_MEAN, "sum": LCE_RED_SUM}
 ABI_VERSION = 3
@@ -82,6 +82,16 @@ def lib() -> ctypes.CDLL:
     L.lce_flce_backward.restype = ctypes.c_int
     L.lce_flce_backward.argtypes = [p, p, p, i64, i64, i64, i64, f32, f32, ctypes.c_int, p, i64, p, p, p, p, p, p,
                                     ctypes.c_size_t, p, p]
+    ci, sz = ctypes.c_int, ctypes.c_size_t
+    L.lce_rms_norm.restype = ci
+    L.lce_rms_norm.argtypes = [p, i64, ci, p, i64, p, ci, f32, f32, i64, i64, p, i64, p, i64, ci, p, p, p]
+    L.lce_rms_norm_workspace_bytes.restype = sz
+    L.lce_rms_norm_workspace_bytes.argtypes = [i64, i64]
+    L.lce_rms_norm_backward.restype = ci
+    L.lce_rms_norm_backward.argtypes = [p, i64, p, i64, ci, p, ci, f32, p, p, i64, i64, i64, p, i64, p, ci, p, sz, p]
+    L.lce_logits_process.restype = ci
+    L.lce_logits_process.argtypes = [p, i64, ci, i64, i64, p, i64, i64, p, p, p, i64, p, i64, i64, ci, p, p, p, p, p,
+                                     i64, i64, p, f32, f32, p, i64, p]
     if L.lce_abi_version() != ABI_VERSION:
         raise ImportError("liblce.so ABI version mismatch; rebuild it")
     _lib = L
@@ -673,3 +683,8 @@ def _deferred_flce_class():
 
 
 _DeferredFLCE = _LazyFunction(_deferred_flce_class)
+
+
+# The operators around the cross-entropy (their marshalling is head.py's).
+from .head import (  # noqa: E402
+    NormResult, lce_logits_process, lce_rms_norm, lce_rms_norm_backward, lce_rms_norm_workspace_bytes, rms_norm)

@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "head_internal.h"
 #include "lce_internal.h"
 
 // The workspace of lce_ce_fwd_bwd_noalloc: room for the row kernel's workspace
@@ -503,6 +504,225 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
     f.q = one_minus_py;
     f.aux = aux_stream;
     return hip_status(lce::launch_flce(f, stream), "lce_flce_backward launch");
+}
+
+}  // extern "C"
+
+// ---- around the cross-entropy: the final norm, the rules on its logits -------------------------
+
+namespace {
+
+size_t dtype_bytes(lce_dtype t) { return t == LCE_F32 ? 4 : t == LCE_BF16 ? 2 : 1; }
+
+bool f32_or_bf16(lce_dtype t) { return t == LCE_F32 || t == LCE_BF16; }
+
+// A matrix operand: present if required, row stride >= width, aligned to its element.
+lce_status check_matrix(const char *fn, const char *name, const void *p, int64_t ld, int64_t width, lce_dtype t,
+                        bool required) {
+    if (!p) return required ? fail(LCE_ERR_INVALID_ARG, "%s: %s is required", fn, name) : LCE_OK;
+    if (ld < width)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the row stride of %s (%lld) must be >= %lld", fn, name, (long long)ld,
+                    (long long)width);
+    if (!is_aligned(p, dtype_bytes(t)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: %s must be %zu-byte aligned", fn, name, dtype_bytes(t));
+    return LCE_OK;
+}
+
+lce_status check_norm_sizes(const char *fn, int64_t n, int64_t H, lce_dtype dtype, const void *weight,
+                            lce_dtype weight_dtype, float weight_offset) {
+    if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
+    if (H < 1) return fail(LCE_ERR_INVALID_ARG, "%s: H must be >= 1 (got %lld)", fn, (long long)H);
+    if (!f32_or_bf16(dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    if (weight && !f32_or_bf16(weight_dtype))
+        return fail(LCE_ERR_INVALID_ARG, "%s: unknown weight dtype %d", fn, (int)weight_dtype);
+    if (!isfinite(weight_offset))
+        return fail(LCE_ERR_INVALID_ARG, "%s: weight_offset must be finite (got %g)", fn, (double)weight_offset);
+    if (weight && !is_aligned(weight, dtype_bytes(weight_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: weight must be %zu-byte aligned", fn, dtype_bytes(weight_dtype));
+    if (H > lce::kNormMaxH)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: H must be <= %lld (got %lld)", fn, (long long)lce::kNormMaxH, (long long)H);
+    if (n > 0x7fffffffLL) return fail(LCE_ERR_UNSUPPORTED, "%s: n > 2^31-1", fn);
+    return LCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lce_status lce_rms_norm(const void *x, int64_t ldx, lce_dtype dtype, const void *residual, int64_t ldr,
+                        const void *weight, lce_dtype weight_dtype, float weight_offset, float eps, int64_t n,
+                        int64_t H, void *sum, int64_t lds, void *y, int64_t ldy, lce_dtype y_dtype, float *scale,
+                        float *rstd, hipStream_t stream) {
+    const char *fn = "lce_rms_norm";
+    lce_status st = check_norm_sizes(fn, n, H, dtype, weight, weight_dtype, weight_offset);
+    if (st != LCE_OK) return st;
+    if (!(eps >= 0.0f) || isinf(eps))
+        return fail(LCE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0 (got %g)", fn, (double)eps);
+    if (y_dtype != dtype && y_dtype != LCE_E4M3)
+        return fail(LCE_ERR_INVALID_ARG, "%s: y must have the dtype of x or be e4m3 (got %d)", fn, (int)y_dtype);
+    if (n == 0) return ok();
+    if ((st = check_matrix(fn, "x", x, ldx, H, dtype, true)) != LCE_OK ||
+        (st = check_matrix(fn, "residual", residual, ldr, H, dtype, false)) != LCE_OK ||
+        (st = check_matrix(fn, "sum", sum, lds, H, dtype, false)) != LCE_OK ||
+        (st = check_matrix(fn, "y", y, ldy, H, y_dtype, true)) != LCE_OK)
+        return st;
+    if (y_dtype == LCE_E4M3 && !scale)
+        return fail(LCE_ERR_INVALID_ARG, "%s: scale is required for an e4m3 output", fn);
+    lce::NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.sum = sum;
+    a.y = y;
+    a.rstd = rstd;
+    a.scale = scale;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.lds = lds;
+    a.ldy = ldy;
+    a.n = n;
+    a.H = H;
+    a.eps = eps;
+    a.offset = weight_offset;
+    a.weight_bf16 = weight_dtype == LCE_BF16;
+    a.out8 = y_dtype == LCE_E4M3;
+    return hip_status(lce::launch_rms_norm(a, dtype == LCE_BF16, stream), "lce_rms_norm launch");
+}
+
+size_t lce_rms_norm_workspace_bytes(int64_t n, int64_t H) {
+    if (n < 0 || H < 1 || H > lce::kNormMaxH) return 0;
+    return static_cast<size_t>(n < lce::kNormMaxGroups ? n : lce::kNormMaxGroups) * static_cast<size_t>(H) * 4;
+}
+
+lce_status lce_rms_norm_backward(const void *grad_y, int64_t ldg, const void *s, int64_t lds, lce_dtype dtype,
+                                 const void *weight, lce_dtype weight_dtype, float weight_offset, const float *rstd,
+                                 const void *grad_sum, int64_t ldgs, int64_t n, int64_t H, void *grad_x, int64_t ldgx,
+                                 void *grad_weight, lce_dtype grad_weight_dtype, void *workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    const char *fn = "lce_rms_norm_backward";
+    lce_status st = check_norm_sizes(fn, n, H, dtype, weight, weight_dtype, weight_offset);
+    if (st != LCE_OK) return st;
+    if (grad_weight && !f32_or_bf16(grad_weight_dtype))
+        return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_weight dtype %d", fn, (int)grad_weight_dtype);
+    if (grad_weight && !is_aligned(grad_weight, dtype_bytes(grad_weight_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: grad_weight must be %zu-byte aligned", fn, dtype_bytes(grad_weight_dtype));
+    if (n > 0) {
+        if ((st = check_matrix(fn, "grad_y", grad_y, ldg, H, dtype, true)) != LCE_OK ||
+            (st = check_matrix(fn, "s", s, lds, H, dtype, true)) != LCE_OK ||
+            (st = check_matrix(fn, "grad_sum", grad_sum, ldgs, H, dtype, false)) != LCE_OK ||
+            (st = check_matrix(fn, "grad_x", grad_x, ldgx, H, dtype, true)) != LCE_OK)
+            return st;
+        if (!rstd) return fail(LCE_ERR_INVALID_ARG, "%s: rstd is required", fn);
+        if (grad_weight) {
+            const size_t need = lce_rms_norm_workspace_bytes(n, H);
+            if (!workspace || workspace_bytes < need)
+                return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+            if (!is_aligned(workspace, 16))
+                return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+        }
+    }
+    lce::NormGradArgs a;
+    a.gy = grad_y;
+    a.s = s;
+    a.weight = weight;
+    a.gs = grad_sum;
+    a.rstd = rstd;
+    a.gx = grad_x;
+    a.gw = grad_weight;
+    a.part = static_cast<float *>(workspace);
+    a.ldg = ldg;
+    a.lds = lds;
+    a.ldgs = ldgs;
+    a.ldgx = ldgx;
+    a.n = n;
+    a.H = H;
+    a.offset = weight_offset;
+    a.weight_bf16 = weight_dtype == LCE_BF16;
+    a.gw_bf16 = grad_weight_dtype == LCE_BF16;
+    return hip_status(lce::launch_rms_norm_backward(a, dtype == LCE_BF16, stream), "lce_rms_norm_backward launch");
+}
+
+lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, int64_t n, int64_t V,
+                              const void *history, int64_t ldh, int64_t L, const int64_t *history_lens,
+                              const int64_t *prompt_lens, const void *bias_ids, int64_t ldbi, const float *bias_values,
+                              int64_t ldbv, int64_t B, int ids_are_64, const float *repetition, const float *presence,
+                              const float *frequency, const float *temperature, const uint32_t *allowed, int64_t ldm,
+                              int64_t mask_count, const int64_t *mask_rows, float mask_value, float softcap, void *out,
+                              int64_t ldo, hipStream_t stream) {
+    const char *fn = "lce_logits_process";
+    lce_status st;
+    if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
+    if (V < 1) return fail(LCE_ERR_INVALID_ARG, "%s: V must be >= 1 (got %lld)", fn, (long long)V);
+    if (!f32_or_bf16(dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!(softcap >= 0.0f) || isinf(softcap))
+        return fail(LCE_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0 (got %g)", fn, (double)softcap);
+    if (isnan(mask_value)) return fail(LCE_ERR_INVALID_ARG, "%s: mask_value must not be NaN", fn);
+    const size_t idb = ids_are_64 ? 8 : 4;
+    if (history) {
+        if (L < 0) return fail(LCE_ERR_INVALID_ARG, "%s: L must be >= 0 (got %lld)", fn, (long long)L);
+        if (ldh != 0 && ldh < L)
+            return fail(LCE_ERR_INVALID_ARG, "%s: the row stride of history (%lld) must be 0 or >= %lld", fn,
+                        (long long)ldh, (long long)L);
+        if (!is_aligned(history, idb)) return fail(LCE_ERR_INVALID_ARG, "%s: history must be %zu-byte aligned", fn, idb);
+    }
+    if (!bias_ids != !bias_values)
+        return fail(LCE_ERR_INVALID_ARG, "%s: bias_ids and bias_values go together", fn);
+    if (bias_ids) {
+        if (B < 0) return fail(LCE_ERR_INVALID_ARG, "%s: B must be >= 0 (got %lld)", fn, (long long)B);
+        if ((ldbi != 0 && ldbi < B) || (ldbv != 0 && ldbv < B))
+            return fail(LCE_ERR_INVALID_ARG, "%s: the row strides of the biases must be 0 or >= %lld", fn, (long long)B);
+        if (!is_aligned(bias_ids, idb) || !is_aligned(bias_values, 4))
+            return fail(LCE_ERR_INVALID_ARG, "%s: bias_ids and bias_values must be aligned to their elements", fn);
+    }
+    if (allowed) {
+        const int64_t words = (V + 31) / 32;
+        if (mask_count < 0) return fail(LCE_ERR_INVALID_ARG, "%s: mask_count must be >= 0", fn);
+        if (ldm < words)
+            return fail(LCE_ERR_INVALID_ARG, "%s: the row stride of allowed (%lld) must be >= %lld words", fn,
+                        (long long)ldm, (long long)words);
+        if (!mask_rows && mask_count < n)
+            return fail(LCE_ERR_INVALID_ARG, "%s: without mask_rows every row needs a mask (%lld of %lld)", fn,
+                        (long long)mask_count, (long long)n);
+        if (!is_aligned(allowed, 4)) return fail(LCE_ERR_INVALID_ARG, "%s: allowed must be 4-byte aligned", fn);
+    }
+    // column arithmetic is 32-bit, and a count fits the low 31 bits of its word
+    if (V > 0x7fffffffLL - 65536) return fail(LCE_ERR_UNSUPPORTED, "%s: V must be < 2^31 - 65536", fn);
+    if ((history && L > 0x7fffffffLL) || (bias_ids && B > 0x7fffffffLL))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: L and B must be < 2^31", fn);
+    if (n > 0x7fffffffLL) return fail(LCE_ERR_UNSUPPORTED, "%s: n > 2^31-1", fn);
+    if (n == 0) return ok();
+    if ((st = check_matrix(fn, "logits", logits, ldx, V, dtype, true)) != LCE_OK ||
+        (st = check_matrix(fn, "out", out, ldo, V, dtype, true)) != LCE_OK)
+        return st;
+    lce::RulesArgs a;
+    a.logits = logits;
+    a.out = out;
+    a.ldx = ldx;
+    a.ldo = ldo;
+    a.n = n;
+    a.V = V;
+    a.history = L > 0 ? history : nullptr;
+    a.ldh = ldh;
+    a.L = L;
+    a.history_lens = history_lens;
+    a.prompt_lens = prompt_lens;
+    a.bias_ids = B > 0 ? bias_ids : nullptr;
+    a.bias_values = bias_values;
+    a.ldbi = ldbi;
+    a.ldbv = ldbv;
+    a.B = B;
+    a.id64 = ids_are_64 != 0;
+    a.repetition = repetition;
+    a.presence = presence;
+    a.frequency = frequency;
+    a.temperature = temperature;
+    a.allowed = allowed;
+    a.ldm = ldm;
+    a.R = mask_count;
+    a.mask_rows = mask_rows;
+    a.mask_value = mask_value;
+    a.softcap = softcap;
+    return hip_status(lce::launch_logits_process(a, dtype == LCE_BF16, stream), "lce_logits_process launch");
 }
 
 }  // extern "C"

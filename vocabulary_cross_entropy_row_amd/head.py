@@ -1,0 +1,322 @@
+"""The operators around the cross-entropy: the final norm, the rules on its logits.
+
+Argument marshalling for the C entry points of the same names (include/lce.h), and the autograd
+forms.  Like the rest of the binding, every function runs on ``stream`` (default: the current
+stream of the first argument's device) and allocates what is not passed in with that stream
+current.
+"""
+from __future__ import annotations
+
+import functools
+from dataclasses import dataclass
+
+from . import (LCE_BF16, LCE_E4M3, LCE_F32, _LazyFunction, _buf, _check, _on_gpu, _ptr, _torch_stream, lib)
+
+
+def _call_stream(fn):
+    """Runs a binding function with its call stream and device current; the function receives the
+    stream's handle as ``stream``.  The common call -- no stream named, tensors of the current
+    device -- switches nothing."""
+
+    @functools.wraps(fn)
+    def wrapper(first, *args, stream=None, **kw):
+        import torch
+        if not (torch.is_tensor(first) and first.device.type == "cuda"):
+            return fn(first, *args, stream=0, **kw)   # the function's own checks raise
+        if stream is None and first.device.index == torch.cuda.current_device():
+            return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+        st = _torch_stream(stream, first.device)
+        with torch.cuda.device(first.device), torch.cuda.stream(st):
+            return fn(first, *args, stream=st.cuda_stream, **kw)
+    return wrapper
+
+
+@functools.lru_cache(maxsize=None)
+def _codes():
+    import torch
+    return {torch.float32: LCE_F32, torch.bfloat16: LCE_BF16, torch.float8_e4m3fn: LCE_E4M3}
+
+
+def _float_code(t, name: str) -> int:
+    code = _codes().get(t.dtype)
+    if code is None or code == LCE_E4M3:
+        raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return code
+
+
+def _rows(t, name: str, dtype, n: int, width: int, device, required: bool = False) -> int:
+    """Checks a [n, width] operand with unit column stride; returns its row stride."""
+    import torch
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return width
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{n}, {width}] (got {list(t.shape)})")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.stride(0) if n > 1 else width
+
+
+# ---- root-mean-square norm -------------------------------------------------------------------
+
+@dataclass
+class NormResult:
+    y: object       # [n, H], the rows' type or e4m3
+    sum: object     # [n, H] x + residual, or None without a residual
+    rstd: object    # fp32 [n], or None
+    scale: object   # fp32 [n] with an e4m3 y, or None
+
+
+def _norm_weight(weight, H: int, device):
+    if weight is None:
+        return LCE_F32
+    import torch
+    if not torch.is_tensor(weight):
+        raise TypeError("weight must be a torch tensor")
+    if weight.device != device:
+        raise ValueError(f"weight must be on {device} (got {weight.device})")
+    if weight.dim() != 1 or weight.shape[0] != H or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{H}] tensor")
+    return _float_code(weight, "weight")
+
+
+@_call_stream
+def lce_rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, out_dtype=None,
+                 want_rstd: bool = False, y=None, sum_out=None, rstd=None, scale=None, stream=None) -> NormResult:
+    """y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) of the rows of s = x + residual (in x's
+    type; x without a residual).  ``x`` is a [n, H] view with unit column stride.  With ``out_dtype``
+    torch.float8_e4m3fn, y holds y / scale with one scale per row.  Outputs not passed in are
+    allocated; ``sum_out`` may be ``x`` or ``residual`` itself."""
+    import torch
+    if not torch.is_tensor(x) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    dev = _on_gpu(x, "x")
+    n, H = x.shape
+    code = _float_code(x, "x")
+    ldx = _rows(x, "x", x.dtype, n, H, dev)
+    ldr = _rows(residual, "residual", x.dtype, n, H, dev)
+    wcode = _norm_weight(weight, H, dev)
+    if out_dtype is None:
+        out_dtype = x.dtype if y is None else y.dtype
+    ycode = _codes().get(out_dtype)
+    if out_dtype != x.dtype and ycode != LCE_E4M3:
+        raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn (got {out_dtype})")
+    if y is None:
+        y = torch.empty((n, H), dtype=out_dtype, device=dev)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty((n, H), dtype=x.dtype, device=dev)
+    if rstd is None and want_rstd:
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    if ycode != LCE_E4M3:
+        scale = None
+    elif scale is None:
+        scale = torch.empty(n, dtype=torch.float32, device=dev)
+    ldy = _rows(y, "y", out_dtype, n, H, dev)
+    lds = _rows(sum_out, "sum_out", x.dtype, n, H, dev)
+    _buf(rstd, "rstd", torch.float32, n, dev)
+    _buf(scale, "scale", torch.float32, n, dev)
+    _check(lib().lce_rms_norm(x.data_ptr(), ldx, code, _ptr(residual), ldr, _ptr(weight), wcode, float(weight_offset),
+                              float(eps), n, H, _ptr(sum_out), lds, y.data_ptr(), ldy, ycode, _ptr(scale), _ptr(rstd),
+                              stream))
+    return NormResult(y, sum_out, rstd, scale)
+
+
+def lce_rms_norm_workspace_bytes(n: int, H: int) -> int:
+    return int(lib().lce_rms_norm_workspace_bytes(int(n), int(H)))
+
+
+@_call_stream
+def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offset: float = 0.0, grad_x=None,
+                          grad_weight=None, want_grad_weight: bool = True, workspace=None, stream=None):
+    """(grad_x, grad_weight) of lce_rms_norm from its ``s`` (the sum; x without a residual) and ``rstd``.
+    grad_x is the gradient of x and of the residual alike; grad_weight has the weight's type (None
+    without a weight or with ``want_grad_weight`` false)."""
+    import torch
+    if not torch.is_tensor(s) or s.dim() != 2:
+        raise ValueError("s must be a 2-D tensor")
+    dev = _on_gpu(grad_y, "grad_y")
+    n, H = s.shape
+    code = _float_code(s, "s")
+    ldg = _rows(grad_y, "grad_y", s.dtype, n, H, dev)
+    lds = _rows(s, "s", s.dtype, n, H, dev)
+    ldgs = _rows(grad_sum, "grad_sum", s.dtype, n, H, dev)
+    wcode = _norm_weight(weight, H, dev)
+    _buf(rstd, "rstd", torch.float32, n, dev, required=True)
+    if grad_x is None:
+        grad_x = torch.empty((n, H), dtype=s.dtype, device=dev)
+    ldgx = _rows(grad_x, "grad_x", s.dtype, n, H, dev)
+    gwcode, bytes_ = LCE_F32, 0
+    if weight is None or not want_grad_weight:
+        grad_weight = workspace = None
+    else:
+        if grad_weight is None:
+            grad_weight = torch.empty(H, dtype=weight.dtype, device=dev)
+        gwcode = _float_code(grad_weight, "grad_weight")
+        _buf(grad_weight, "grad_weight", grad_weight.dtype, H, dev)
+        bytes_ = lce_rms_norm_workspace_bytes(n, H)
+        if workspace is None:   # clobbered by the call
+            workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=dev)
+        _buf(workspace, "workspace", torch.uint8, bytes_, dev)
+    _check(lib().lce_rms_norm_backward(grad_y.data_ptr(), ldg, s.data_ptr(), lds, code, _ptr(weight), wcode,
+                                       float(weight_offset), _ptr(rstd), _ptr(grad_sum), ldgs, n, H, grad_x.data_ptr(),
+                                       ldgx, _ptr(grad_weight), gwcode, _ptr(workspace), bytes_, stream))
+    return grad_x, grad_weight
+
+
+def _rows_of(t, H: int):
+    """t with its leading dimensions as rows of H, unit column stride, no two rows overlapping."""
+    t = t.reshape(-1, H)
+    if (H > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < H):
+        t = t.contiguous()
+    return t
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
+    """Autograd form of the norm over the last dimension of ``x``.
+
+    Without a residual returns y; with one (x's shape and type) returns (y, sum), sum = x + residual
+    being the stream that goes on.  Gradients: x, weight and residual; the gradient that reaches
+    ``sum`` is added in the same kernel.
+    """
+    return _RmsNorm.apply(x, weight, residual, float(eps), float(weight_offset))
+
+
+def _rms_norm_class():
+    import torch
+
+    class RmsNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, residual, eps, offset):
+            _on_gpu(x, "x")
+            if x.dim() < 1:
+                raise ValueError("x must have at least one dimension")
+            if residual is not None and residual.shape != x.shape:
+                raise ValueError(f"residual must have the shape of x, {list(x.shape)} (got {list(residual.shape)})")
+            H = x.shape[-1]
+            x2 = _rows_of(x, H)
+            r = lce_rms_norm(x2, weight, residual=None if residual is None else _rows_of(residual, H), eps=eps,
+                             weight_offset=offset, want_rstd=True)
+            ctx.set_materialize_grads(False)
+            ctx.offset = offset
+            y = r.y.view(x.shape)
+            if residual is None:
+                ctx.save_for_backward(x, weight, r.rstd)
+                return y
+            total = r.sum.view(x.shape)
+            ctx.save_for_backward(total, weight, r.rstd)
+            return y, total
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gy, gs=None):
+            s, weight, rstd = ctx.saved_tensors
+            H = s.shape[-1]
+            need_x, need_w, need_r = ctx.needs_input_grad[:3]
+            if gy is None:   # nothing came through the norm
+                return (gs if need_x else None), None, (gs if need_r else None), None, None
+            gx, gw = lce_rms_norm_backward(_rows_of(gy, H), _rows_of(s, H), weight, rstd,
+                                           grad_sum=None if gs is None else _rows_of(gs, H),
+                                           weight_offset=ctx.offset, want_grad_weight=need_w)
+            gx = gx.view(s.shape)
+            return (gx if need_x else None), gw, (gx if need_r else None), None, None
+
+    return RmsNorm
+
+
+_RmsNorm = _LazyFunction(_rms_norm_class)
+
+
+# ---- rules on logits -------------------------------------------------------------------------
+
+def _ids(t, name: str, n: int, device):
+    """Checks a [n, L] list of token ids (int32 or int64); returns (row stride, length).  A row stride
+    of 0 (one list expanded over the rows) is kept."""
+    import torch
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64 (got {t.dtype})")
+    return _list(t, name, n)
+
+
+def _list(t, name: str, n: int):
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}, length] (got {list(t.shape)})")
+    L = t.shape[1]
+    if L > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return (t.stride(0) if n > 1 else L), L
+
+
+@_call_stream
+def lce_logits_process(logits, *, history=None, history_lens=None, prompt_lens=None, repetition=None, presence=None,
+                       frequency=None, bias_ids=None, bias_values=None, temperature=None, allowed=None,
+                       mask_rows=None, mask_value: float = float("-inf"), softcap: float = 0.0, out=None, stream=None):
+    """The rules a serving step puts on ``logits`` ([n, V] view, unit column stride) before a token is
+    drawn, in one pass: softcap, penalties for the tokens of ``history`` ([n, L] ids; the first
+    ``prompt_lens`` of a row's ``history_lens`` are its prompt), ``bias_values`` at ``bias_ids`` ([n, B],
+    the last entry of a token counts), ``temperature`` and the grammar masks ``allowed`` (int32 [masks,
+    ceil(V / 32)], one bit per token; ``mask_rows`` names each row's mask, -1 none).  repetition,
+    presence, frequency and temperature are fp32 [n].  Writes to ``out``, or in place, and returns it;
+    lce_ce_argmax reads it from there, and with ``mask_value`` -1e4 (the losses need finite logits)
+    lce_ce_stats and lce_ce_combine."""
+    import torch
+    if not torch.is_tensor(logits) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D view with unit column stride")
+    dev = _on_gpu(logits, "logits")
+    n, V = logits.shape
+    code = _float_code(logits, "logits")
+    ldx = _rows(logits, "logits", logits.dtype, n, V, dev)
+    if out is None:
+        out = logits
+    ldo = _rows(out, "out", logits.dtype, n, V, dev)
+    ldh = L = ldbi = ldbv = B = ldm = masks = 0
+    wide = True
+    if history is not None:
+        ldh, L = _ids(history, "history", n, dev)
+        wide = history.dtype == torch.int64
+    elif history_lens is not None or prompt_lens is not None:
+        raise ValueError("history_lens and prompt_lens go with history")
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        ldbi, B = _ids(bias_ids, "bias_ids", n, dev)
+        if history is not None and bias_ids.dtype != history.dtype:
+            raise TypeError("history and bias_ids must have the same type")
+        wide = bias_ids.dtype == torch.int64
+        if not torch.is_tensor(bias_values) or bias_values.dtype != torch.float32 or bias_values.device != dev:
+            raise TypeError(f"bias_values must be a float32 tensor on {dev}")
+        ldbv, values = _list(bias_values, "bias_values", n)
+        if values != B:
+            raise ValueError(f"bias_ids has {B} entries a row, bias_values {values}")
+    if allowed is not None:
+        if not torch.is_tensor(allowed) or allowed.dtype != torch.int32 or allowed.device != dev:
+            raise TypeError(f"allowed must be an int32 tensor on {dev}")
+        if allowed.dim() != 2 or allowed.shape[1] < (V + 31) // 32:
+            raise ValueError(f"allowed must be [masks, {(V + 31) // 32}] (got {list(allowed.shape)})")
+        if allowed.shape[1] > 1 and allowed.stride(1) != 1:
+            raise ValueError("allowed must have unit column stride")
+        masks = allowed.shape[0]
+        ldm = allowed.stride(0) if masks > 1 else allowed.shape[1]
+    elif mask_rows is not None:
+        raise ValueError("mask_rows goes with allowed")
+    for t, name in ((history_lens, "history_lens"), (prompt_lens, "prompt_lens"), (mask_rows, "mask_rows")):
+        _buf(t, name, torch.int64, n, dev)
+    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency"),
+                    (temperature, "temperature")):
+        _buf(t, name, torch.float32, n, dev)
+    _check(lib().lce_logits_process(logits.data_ptr(), ldx, code, n, V, _ptr(history), ldh, L, _ptr(history_lens),
+                                    _ptr(prompt_lens), _ptr(bias_ids), ldbi, _ptr(bias_values), ldbv, B, int(wide),
+                                    _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(temperature),
+                                    _ptr(allowed), ldm, masks, _ptr(mask_rows), float(mask_value), float(softcap),
+                                    out.data_ptr(), ldo, stream))
+    return out
