@@ -123,3 +123,61 @@ def test_operand_checks():
     rows = head._rows_of(torch.zeros(2, 3, 8).transpose(0, 1), 8)
     assert rows.shape == (6, 8) and rows.stride() == (8, 1)
     assert head._rows_of(torch.zeros(1, 8).expand(5, 8), 8).stride(0) == 8
+
+
+LINEAR = dict(x=P, ldx=64, weight=P, ldw=64, in_dtype=lce.LCE_BF16, scale_x=None, scale_w=None, bias=None,
+              bias_dtype=lce.LCE_F32, act=0, residual=None, ldr=0, n=4, K=64, M=40, out=P, ldo=40,
+              out_dtype=lce.LCE_BF16, preact=None, ldp=0, workspace=None, bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("over,needle,status", [
+    (dict(n=-1), "n must be", ARG), (dict(K=0), "K must be", ARG), (dict(M=0), "M must be", ARG),
+    (dict(in_dtype=lce.LCE_F32), "must be bf16 or e4m3", ARG), (dict(act=5), "activation", ARG),
+    (dict(act=-1), "activation", ARG), (dict(weight=None), "weight is required", ARG), (dict(x=None), "x is required", ARG),
+    (dict(ldx=56), "row strides of x", ARG), (dict(ldw=56), "row strides of x", ARG),
+    (dict(scale_x=P), "scales go with e4m3", ARG), (dict(out_dtype=lce.LCE_E4M3), "output dtype", ARG),
+    (dict(bias=P, bias_dtype=lce.LCE_E4M3), "bias dtype", ARG), (dict(bias=P + 2), "bias must be", ARG),
+    (dict(out=None), "out is required", ARG), (dict(ldo=39), "row stride of out", ARG),
+    (dict(residual=P, ldr=39), "row stride of residual", ARG), (dict(preact=P, ldp=39), "row stride of preact", ARG),
+    (dict(K=60), "multiples of 8", UNSUPPORTED), (dict(ldx=68), "multiples of 8", UNSUPPORTED),
+    (dict(in_dtype=lce.LCE_E4M3, K=56), "multiples of 16", UNSUPPORTED), (dict(x=P + 8), "16-byte aligned", UNSUPPORTED),
+    (dict(in_dtype=lce.LCE_E4M3, out_dtype=lce.LCE_F32), "bf16 output", UNSUPPORTED),
+    (dict(weight=P + 2), "16-byte aligned", UNSUPPORTED), (dict(ldx=1 << 23), "4 GiB", UNSUPPORTED),
+    (dict(n=1 << 23), "2^23", UNSUPPORTED), (dict(M=1 << 23, ldo=1 << 23), "2^23", UNSUPPORTED),
+    (dict(n=200, K=4096, ldx=4096, ldw=4096, M=256, ldo=256), "workspace_bytes", ARG),
+])
+def test_linear_rejects(over, needle, status):
+    st, msg = _call("lce_linear", LINEAR, over)
+    assert st == status and needle in msg
+
+
+LINEAR_BWD = dict(grad_out=P, ldg=40, grad_dtype=lce.LCE_BF16, x=P, ldx=64, weight=P, ldw=64, preact=P, ldp=40, act=2,
+                  n=4, K=64, M=40, grad_x=P, ldgx=64, grad_weight=P, wdtype=lce.LCE_F32, grad_bias=P,
+                  bdtype=lce.LCE_F32, workspace=P, bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("over,needle,status", [
+    (dict(n=-1), "n must be", ARG), (dict(M=36, ldg=36, ldp=36), "M must be a multiple", UNSUPPORTED),
+    (dict(K=60), "multiples of 8", UNSUPPORTED), (dict(grad_dtype=lce.LCE_E4M3), "grad_out dtype", ARG),
+    (dict(wdtype=9), "grad_weight dtype", ARG), (dict(bdtype=lce.LCE_E4M3), "grad_bias dtype", ARG),
+    (dict(preact=None), "preact is required", ARG), (dict(grad_out=None), "grad_out is required", ARG),
+    (dict(ldg=39), "row stride of grad_out", ARG), (dict(ldgx=56), "row stride of grad_x", ARG),
+    (dict(grad_x=P + 2), "grad_x must be 16-byte", UNSUPPORTED), (dict(ldgx=68), "whole 16 bytes", UNSUPPORTED),
+    (dict(grad_weight=P + 4), "grad_weight must be 16-byte", UNSUPPORTED), (dict(grad_bias=P + 2), "grad_bias", ARG),
+    (dict(workspace=None), "workspace_bytes", ARG), (dict(bytes=100), "workspace_bytes", ARG),
+    (dict(workspace=P + 16), "256-byte aligned", ARG), (dict(x=None), "x is required", ARG),
+])
+def test_linear_backward_rejects(over, needle, status):
+    st, msg = _call("lce_linear_backward", LINEAR_BWD, over)
+    assert st == status and needle in msg
+
+
+def test_linear_sizes_and_host_tensors():
+    assert _call("lce_linear", LINEAR, dict(n=0, x=None, out=None))[0] == OK
+    assert lce.lce_linear_workspace_bytes(4096, 4096, 16384) == 0      # enough tiles without splits
+    assert lce.lce_linear_workspace_bytes(200, 4096, 256) % (200 * 256 * 4) == 0 < lce.lce_linear_workspace_bytes(200, 4096, 256)
+    assert lce.lce_linear_workspace_bytes(4, 0, 8) == lce.lce_linear_backward_workspace_bytes(4, 8, 0) == 0
+    x, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((8, 64), dtype=torch.bfloat16)
+    for call in (lambda: lce.lce_linear(x, w), lambda: lce.linear(x, w), lambda: lce.lce_linear_backward(x[:, :8], x, w)):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()

@@ -92,6 +92,15 @@ def lib() -> ctypes.CDLL:
     L.lce_logits_process.restype = ci
     L.lce_logits_process.argtypes = [p, i64, ci, i64, i64, p, i64, i64, p, p, p, i64, p, i64, i64, ci, p, p, p, p, p,
                                      i64, i64, p, f32, f32, p, i64, p]
+    L.lce_linear.restype = ci
+    L.lce_linear.argtypes = [p, i64, p, i64, ci, p, p, p, ci, ci, p, i64, i64, i64, i64, p, i64, ci, p, i64, p, sz, p]
+    L.lce_linear_workspace_bytes.restype = sz
+    L.lce_linear_workspace_bytes.argtypes = [i64, i64, i64, ci]
+    L.lce_linear_backward.restype = ci
+    L.lce_linear_backward.argtypes = [p, i64, ci, p, i64, p, i64, p, i64, ci, i64, i64, i64, p, i64, p, ci, p, ci, p, sz,
+                                      p]
+    L.lce_linear_backward_workspace_bytes.restype = sz
+    L.lce_linear_backward_workspace_bytes.argtypes = [i64, i64, i64]
     if L.lce_abi_version() != ABI_VERSION:
         raise ImportError("liblce.so ABI version mismatch; rebuild it")
     _lib = L
@@ -687,4 +696,6 @@ _DeferredFLCE = _LazyFunction(_deferred_flce_class)
 
 # The operators around the cross-entropy (their marshalling is head.py's).
 from .head import (  # noqa: E402
-    NormResult, lce_logits_process, lce_rms_norm, lce_rms_norm_backward, lce_rms_norm_workspace_bytes, rms_norm)
+    ACTIVATIONS, LinearGrads, LinearResult, NormResult, lce_linear, lce_linear_backward,
+    lce_linear_backward_workspace_bytes, lce_linear_workspace_bytes, lce_logits_process, lce_rms_norm,
+    lce_rms_norm_backward, lce_rms_norm_workspace_bytes, linear, rms_norm)

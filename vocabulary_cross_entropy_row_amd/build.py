@@ -28,7 +28,7 @@ MR_FAMILIES = [(1, 1), (1, 2), (1, 4), (1, 8), (2, 8), (4, 8), (4, 16)]
 # Half-row kernel families (rounds of 960 vectors per half row), ce_rows_half.hip.
 HALF_FAMILIES = [5, 6, 7, 8, 9, 10]
 UNITS = [("ce_kernels.hip", [], "ce_kernels"), ("flce.hip", [], "flce"), ("ce_split.hip", [], "ce_split"),
-         ("rms_norm.hip", [], "rms_norm"), ("logits_process.hip", [], "logits_process"),
+         ("rms_norm.hip", [], "rms_norm"), ("logits_process.hip", [], "logits_process"), ("linear.hip", [], "linear"),
          ("lce_api.cpp", ["-x", "hip"], "lce_api")] + [
     ("ce_rows_inst.hip", [f"-DLCE_BF16={b}", f"-DLCE_KR={kr}", f"-DLCE_KL={kl}", "-DLCE_UA=0"], f"ce_rows_{b}_{kr}_{kl}")
     for b in (1, 0) for kr, kl in FAMILIES] + [

@@ -71,4 +71,53 @@ struct RulesArgs {
 };
 hipError_t launch_logits_process(const RulesArgs &a, bool is_bf16, hipStream_t st);
 
+// ---- matrix product with an epilogue ----------------------------------------------
+
+enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+struct LinearArgs {
+    const void *x;         // [n, K] bf16 or e4m3, row stride ldx (elements)
+    const void *weight;    // [M, K] of the same type, row stride ldw
+    int64_t ldx, ldw, n, K, M;
+    bool fp8;
+    const float *scale_x;  // [n] or NULL
+    const float *scale_w;  // [M] or NULL
+    const void *bias;      // [M] or NULL
+    bool bias_bf16;
+    int act;
+    const void *residual;  // [n, M] of the output's type, row stride ldr, or NULL
+    int64_t ldr;
+    void *out;             // [n, M] bf16 or fp32, row stride ldo
+    int64_t ldo;
+    bool out_bf16;
+    void *preact;          // [n, M] bf16, row stride ldp, or NULL
+    int64_t ldp;
+    float *part;           // workspace: split partials [splits][n][round8(M)] fp32
+};
+// Bytes of split partials the product needs (0: it is not split).
+size_t linear_workspace_bytes(int64_t n, int64_t K, int64_t M, bool fp8);
+hipError_t launch_linear(const LinearArgs &a, hipStream_t st);
+
+struct LinearGradArgs {
+    const void *grad_out;  // [n, M] bf16 or fp32, row stride ldg
+    int64_t ldg;
+    bool grad_bf16;
+    const void *x;         // [n, K] bf16, row stride ldx
+    const void *weight;    // [M, K] bf16, row stride ldw
+    int64_t ldx, ldw;
+    const void *preact;    // [n, M] bf16, row stride ldp (act other than none)
+    int64_t ldp;
+    int act;
+    int64_t n, K, M;
+    void *grad_x;          // [n, K] bf16, row stride ldgx, or NULL
+    int64_t ldgx;
+    void *grad_weight;     // [M, K] bf16 or fp32, contiguous, or NULL
+    bool grad_weight_bf16;
+    void *grad_bias;       // [M] bf16 or fp32, or NULL
+    bool grad_bias_bf16;
+    void *workspace;
+};
+size_t linear_backward_workspace_bytes(int64_t n, int64_t K, int64_t M);
+hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st);
+
 }  // namespace lce

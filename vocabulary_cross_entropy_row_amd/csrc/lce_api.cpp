@@ -508,7 +508,7 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
 
 }  // extern "C"
 
-// ---- around the cross-entropy: the final norm, the rules on its logits -------------------------
+// ---- around the cross-entropy: the final norm, the rules on logits, the matrix product -----------
 
 namespace {
 
@@ -723,6 +723,158 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
     a.mask_value = mask_value;
     a.softcap = softcap;
     return hip_status(lce::launch_logits_process(a, dtype == LCE_BF16, stream), "lce_logits_process launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and operands both directions of the product share.  es: bytes of an operand's element.
+lce_status check_linear(const char *fn, const void *x, int64_t ldx, const void *weight, int64_t ldw, int64_t n, int64_t K,
+                        int64_t M, int act, int64_t es) {
+    if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
+    if (K < 1) return fail(LCE_ERR_INVALID_ARG, "%s: K must be >= 1 (got %lld)", fn, (long long)K);
+    if (M < 1) return fail(LCE_ERR_INVALID_ARG, "%s: M must be >= 1 (got %lld)", fn, (long long)M);
+    if (act < LCE_ACT_NONE || act > LCE_ACT_SILU) return fail(LCE_ERR_INVALID_ARG, "%s: unknown activation %d", fn, act);
+    if (!weight) return fail(LCE_ERR_INVALID_ARG, "%s: weight is required", fn);
+    if (n > 0 && !x) return fail(LCE_ERR_INVALID_ARG, "%s: x is required", fn);
+    if (ldx < K || ldw < K)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the row strides of x (%lld) and weight (%lld) must be >= %lld", fn,
+                    (long long)ldx, (long long)ldw, (long long)K);
+    const int64_t unit = 16 / es;
+    if (K % unit || ldx % unit || ldw % unit)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: K and the row strides of x and weight must be multiples of %lld (16 bytes)",
+                    fn, (long long)unit);
+    if ((x && !is_aligned(x, 16)) || !is_aligned(weight, 16))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: x and weight must be 16-byte aligned", fn);
+    // 32-bit offsets inside a tile of 256 rows, one step of K read ahead
+    const int64_t most = (int64_t(1) << 32) / 256 - 1024;
+    if (ldx * es > most || ldw * es > most || n > 0x7fffffffLL / 256 || M > 0x7fffffffLL / 256)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: 256 rows of x or weight exceed 4 GiB, or n or M >= 2^23", fn);
+    return LCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_linear_workspace_bytes(int64_t n, int64_t K, int64_t M, lce_dtype in_dtype) {
+    if (n < 0 || K < 1 || M < 1) return 0;
+    return lce::linear_workspace_bytes(n, K, M, in_dtype == LCE_E4M3);
+}
+
+lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ldw, lce_dtype in_dtype,
+                      const float *scale_x, const float *scale_w, const void *bias, lce_dtype bias_dtype,
+                      lce_activation act, const void *residual, int64_t ldr, int64_t n, int64_t K, int64_t M, void *out,
+                      int64_t ldo, lce_dtype out_dtype, void *preact, int64_t ldp, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+    const char *fn = "lce_linear";
+    if (in_dtype != LCE_BF16 && in_dtype != LCE_E4M3)
+        return fail(LCE_ERR_INVALID_ARG, "%s: x and weight must be bf16 or e4m3 (got dtype %d)", fn, (int)in_dtype);
+    lce_status st = check_linear(fn, x, ldx, weight, ldw, n, K, M, act, in_dtype == LCE_E4M3 ? 1 : 2);
+    if (st != LCE_OK) return st;
+    if (in_dtype == LCE_BF16 && (scale_x || scale_w))
+        return fail(LCE_ERR_INVALID_ARG, "%s: scales go with e4m3 operands", fn);
+    if (!f32_or_bf16(out_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown output dtype %d", fn, (int)out_dtype);
+    if (in_dtype == LCE_E4M3 && out_dtype != LCE_BF16)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: e4m3 operands give a bf16 output", fn);
+    if (bias && !f32_or_bf16(bias_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown bias dtype %d", fn, (int)bias_dtype);
+    if (bias && !is_aligned(bias, dtype_bytes(bias_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: bias must be %zu-byte aligned", fn, dtype_bytes(bias_dtype));
+    if (n == 0) return ok();
+    if ((st = check_matrix(fn, "residual", residual, ldr, M, out_dtype, false)) != LCE_OK ||
+        (st = check_matrix(fn, "out", out, ldo, M, out_dtype, true)) != LCE_OK ||
+        (st = check_matrix(fn, "preact", preact, ldp, M, LCE_BF16, false)) != LCE_OK)
+        return st;
+    const size_t need = lce::linear_workspace_bytes(n, K, M, in_dtype == LCE_E4M3);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (need > 0 && !is_aligned(workspace, 16))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    lce::LinearArgs a{};
+    a.x = x;
+    a.weight = weight;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.n = n;
+    a.K = K;
+    a.M = M;
+    a.fp8 = in_dtype == LCE_E4M3;
+    a.scale_x = scale_x;
+    a.scale_w = scale_w;
+    a.bias = bias;
+    a.bias_bf16 = bias_dtype == LCE_BF16;
+    a.act = act;
+    a.residual = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    a.out_bf16 = out_dtype == LCE_BF16;
+    a.preact = preact;
+    a.ldp = ldp;
+    a.part = static_cast<float *>(workspace);
+    return hip_status(lce::launch_linear(a, stream), "lce_linear launch");
+}
+
+size_t lce_linear_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
+    if (n < 0 || K < 1 || M < 1) return 0;
+    return lce::linear_backward_workspace_bytes(n, K, M);
+}
+
+lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *x, int64_t ldx,
+                               const void *weight, int64_t ldw, const void *preact, int64_t ldp, lce_activation act,
+                               int64_t n, int64_t K, int64_t M, void *grad_x, int64_t ldgx, void *grad_weight,
+                               lce_dtype grad_weight_dtype, void *grad_bias, lce_dtype grad_bias_dtype, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+    const char *fn = "lce_linear_backward";
+    lce_status st = check_linear(fn, x, ldx, weight, ldw, n, K, M, act, 2);
+    if (st != LCE_OK) return st;
+    if (M % 8) return fail(LCE_ERR_UNSUPPORTED, "%s: M must be a multiple of 8 (got %lld)", fn, (long long)M);
+    if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
+    if (!f32_or_bf16(grad_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_out dtype %d", fn, (int)grad_dtype);
+    if (grad_weight && !f32_or_bf16(grad_weight_dtype))
+        return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_weight dtype %d", fn, (int)grad_weight_dtype);
+    if (grad_bias && !f32_or_bf16(grad_bias_dtype))
+        return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_bias dtype %d", fn, (int)grad_bias_dtype);
+    if (n > 0) {
+        if ((st = check_matrix(fn, "grad_out", grad_out, ldg, M, grad_dtype, true)) != LCE_OK ||
+            (st = check_matrix(fn, "preact", preact, ldp, M, LCE_BF16, act != LCE_ACT_NONE)) != LCE_OK ||
+            (st = check_matrix(fn, "grad_x", grad_x, ldgx, K, LCE_BF16, false)) != LCE_OK)
+            return st;
+    }
+    if (grad_x && (!is_aligned(grad_x, 16) || ldgx % 8))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: grad_x must be 16-byte aligned with a row stride of whole 16 bytes", fn);
+    if (grad_weight && !is_aligned(grad_weight, 16))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: grad_weight must be 16-byte aligned", fn);
+    if (grad_bias && !is_aligned(grad_bias, dtype_bytes(grad_bias_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: grad_bias must be %zu-byte aligned", fn, dtype_bytes(grad_bias_dtype));
+    const size_t need = lce::linear_backward_workspace_bytes(n, K, M);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (need > 0 && !is_aligned(workspace, 256))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    lce::LinearGradArgs a{};
+    a.grad_out = grad_out;
+    a.ldg = ldg;
+    a.grad_bf16 = grad_dtype == LCE_BF16;
+    a.x = x;
+    a.weight = weight;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.preact = preact;
+    a.ldp = ldp;
+    a.act = act;
+    a.n = n;
+    a.K = K;
+    a.M = M;
+    a.grad_x = grad_x;
+    a.ldgx = ldgx;
+    a.grad_weight = grad_weight;
+    a.grad_weight_bf16 = grad_weight_dtype == LCE_BF16;
+    a.grad_bias = grad_bias;
+    a.grad_bias_bf16 = grad_bias_dtype == LCE_BF16;
+    a.workspace = workspace;
+    return hip_status(lce::launch_linear_backward(a, stream), "lce_linear_backward launch");
 }
 
 }  // extern "C"

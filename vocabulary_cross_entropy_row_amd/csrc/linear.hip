@@ -1,0 +1,370 @@
+// Matrix product with bias, activation and residual in its epilogue, and its
+// backward (linear_mfma.h has the kernel).
+//
+// Forward: one launch, or with K split over workgroups (few tiles) a second one
+// that adds the partial sums in their order and runs the epilogue.
+//
+// Backward, with dz = grad_out act'(z):
+//   grad_x = dz W        the same kernel on dz [n, M] and W^T [K, M]
+//   grad_W = dz^T x      ... on dz^T [M, n] and x^T [K, n]
+//   grad_b = sum dz      column sums, fp32 partials per 128 rows folded in order
+// One pass reads grad_out (and the pre-activation) and writes dz, dz^T and the bias
+// partials; W^T and x^T are transposed by the same kernel.
+#include <hip/hip_runtime.h>
+#include <algorithm>
+#include <stdint.h>
+
+#include "ce_device.h"
+#include "head_internal.h"
+#include "linear_mfma.h"
+
+namespace lce {
+namespace {
+
+using dev::Elt;
+using dev::u32x4;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// ---- tile shapes ------------------------------------------------------------------
+
+using Big = linear::Shape<256, 256, 2, 4, 3, 2>;     // one workgroup of 8 waves per CU
+using Mid = linear::Shape<128, 128, 2, 2, 2, 2>;     // two of 4 waves
+using Low = linear::Shape<128, 64, 2, 2, 3, 3>;
+using Few = linear::Shape<128, 32, 4, 1, 4, 4>;
+
+struct ShapeInfo {
+    int bf, bt, per_cu;
+    double tflops, tflops8;   // of one compute unit with this shape, bf16 and e4m3 (measured, long K)
+};
+constexpr ShapeInfo kShapes[] = {
+    {Big::BF, Big::BT, Big::PER_CU, 5.0, 9.0},
+    {Mid::BF, Mid::BT, Mid::PER_CU, 3.6, 5.5},
+    {Low::BF, Low::BT, Low::PER_CU, 2.6, 3.5},
+    {Few::BF, Few::BT, Few::PER_CU, 1.4, 1.6},
+};
+constexpr int kCus = 256;        // compute units of an MI355X
+constexpr int kMaxSplits = 16;
+
+struct Plan {
+    int shape, splits;
+};
+// The tile shape and K splits with the least estimated time: whole rounds of workgroups over the
+// compute units at the shape's rate, not less than reading the operands and writing the output at
+// 5 TB/s, plus for a split product its partials and second launch.
+Plan plan_of(int64_t n, int64_t K, int64_t M, bool fp8) {
+    const int es = fp8 ? 1 : 2;
+    const int64_t steps = std::max<int64_t>(1, ceil_div(K * es, linear::kStepBytes));
+    const double stream = (static_cast<double>(n + M) * K * es + 2.0 * n * M) / 5.0e6;   // us
+    Plan best{0, 1};
+    double best_us = 1e30;
+    for (int i = 0; i < 4; ++i) {
+        const ShapeInfo &s = kShapes[i];
+        const int64_t tiles = ceil_div(M, s.bf) * ceil_div(n, s.bt);
+        const double step_flops = 2.0 * s.bf * s.bt * (linear::kStepBytes / es);
+        // per workgroup: its share of the unit's rate, and of about 60 GB/s of operands from L2
+        const double rate_us = step_flops * s.per_cu / ((fp8 ? s.tflops8 : s.tflops) * 1e6);
+        const double feed_us = (s.bf + s.bt) * linear::kStepBytes * s.per_cu / 60e3;
+        const double step_us = std::max(rate_us, feed_us);
+        for (int sp = 1; sp <= kMaxSplits && (sp == 1 || steps / sp >= 4); ++sp) {
+            const int64_t rounds = ceil_div(tiles * sp, static_cast<int64_t>(kCus) * s.per_cu);
+            double us = std::max(rounds * (static_cast<double>(ceil_div(steps, sp)) * step_us + 2.0), stream + 2.0);
+            if (sp > 1) us += 4.0 + (sp + 1) * static_cast<double>(n) * round_up(M, 8) * 4 / 4.0e6;
+            if (us < best_us - 1e-9) {
+                best_us = us;
+                best = {i, sp};
+            }
+        }
+    }
+    return best;
+}
+
+template <class S>
+hipError_t launch_shape(const linear::Args &g, bool fp8, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(g.per_xcd) * 8u), block(64 * S::NW);
+    const bool tail = g.kbytes % linear::kStepBytes != 0;
+    if (fp8) {
+        if (tail) hipLaunchKernelGGL((linear::linear_kernel<S, true, true>), grid, block, 0, st, g);
+        else hipLaunchKernelGGL((linear::linear_kernel<S, true, false>), grid, block, 0, st, g);
+    } else {
+        if (tail) hipLaunchKernelGGL((linear::linear_kernel<S, false, true>), grid, block, 0, st, g);
+        else hipLaunchKernelGGL((linear::linear_kernel<S, false, false>), grid, block, 0, st, g);
+    }
+    return hipGetLastError();
+}
+
+// ---- transposes ---------------------------------------------------------------------
+
+constexpr int kTrRows = 128, kTrCols = 64;
+
+// v = in, or in act'(pre); out[r][c] = bf16(v) when out is given; out_t[c][r] = bf16(v), rows
+// [rows, rows_pad) as zeros; part[blockIdx.y][c] = sum over the block's rows of bf16(v).  A tile of
+// 128 x 64 goes through LDS, 16-byte chunk c of row r at c ^ (r / 8 mod 8): the writes of a wave cover
+// 1 KB without conflicts and the eight rows of an output chunk are read from different banks.
+struct TransposeArgs {
+    const void *in;        // [rows, cols] bf16 or fp32
+    int64_t ld_in;
+    const uint16_t *pre;   // bf16, or NULL
+    int64_t ld_pre;
+    int act;
+    uint16_t *out;         // [rows, cols] or NULL
+    int64_t ld_out;
+    uint16_t *out_t;       // [cols, rows_pad] or NULL
+    int64_t ld_t;
+    float *part;           // [row blocks][cols] or NULL
+    int rows, rows_pad, cols;
+};
+template <bool BF16_IN>
+__global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
+    constexpr int PER = kTrRows * (kTrCols / 8) / 256;   // 16-byte chunks per thread
+    __shared__ __align__(16) uint16_t tile[kTrRows * kTrCols];
+    const int r0 = blockIdx.y * kTrRows, c0 = blockIdx.x * kTrCols;
+    const int t = threadIdx.x;
+    const bool vin = (a.ld_in * (BF16_IN ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.in) % 16 == 0;
+    const bool vpre = a.ld_pre % 8 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
+#pragma unroll
+    for (int h = 0; h < PER; ++h) {
+        const int idx = t + h * 256, r = idx >> 3, ch = idx & 7;
+        const int gr = r0 + r, gc = c0 + ch * 8;
+        const bool full = gr < a.rows && gc + 8 <= a.cols;
+        float v[8];
+        if (vin && full) {
+            if constexpr (BF16_IN) {
+                const u32x4 q = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.in) + gr * a.ld_in + gc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = Elt<true>::get(q, e);
+            } else {
+                const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(a.in) + gr * a.ld_in + gc);
+                const float4 x = q[0], y = q[1];
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = gr < a.rows && gc + e < a.cols ? Elt<BF16_IN>::load_one(a.in, gr * a.ld_in + gc + e) : 0.0f;
+        }
+        if (a.pre) {
+            float z[8];
+            if (vpre && full) {
+                const u32x4 q = *reinterpret_cast<const u32x4 *>(a.pre + gr * a.ld_pre + gc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = Elt<true>::get(q, e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    z[e] = gr < a.rows && gc + e < a.cols ? Elt<true>::load_one(a.pre, gr * a.ld_pre + gc + e) : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = gr < a.rows && gc + e < a.cols ? v[e] * linear::slope(a.act, z[e]) : 0.0f;
+        }
+        const u32x4 q = Elt<true>::pack(v);
+        if (a.out) {   // ld_out and out are 16-byte whole
+            if (full) {
+                *reinterpret_cast<u32x4 *>(a.out + gr * a.ld_out + gc) = q;
+            } else if (gr < a.rows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (gc + e < a.cols) Elt<true>::store_one(a.out, gr * a.ld_out + gc + e, v[e]);
+            }
+        }
+        *reinterpret_cast<u32x4 *>(tile + r * kTrCols + ((ch ^ (r >> 3)) & 7) * 8) = q;
+    }
+    __syncthreads();
+    if (a.out_t) {
+#pragma unroll
+        for (int h = 0; h < PER; ++h) {
+            const int idx = t + h * 256;
+            const int orow = (idx >> 3) & 63, ch = (idx & 7) + 8 * (idx >> 9);
+            const int gc = c0 + orow, gr = r0 + ch * 8;
+            if (gc >= a.cols || gr >= a.rows_pad) continue;   // rows_pad is a multiple of 8
+            const uint16_t *src = tile + ch * 8 * kTrCols + (((orow >> 3) ^ ch) & 7) * 8 + (orow & 7);
+            u32x4 o;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                o[w] = src[2 * w * kTrCols] | (static_cast<uint32_t>(src[(2 * w + 1) * kTrCols]) << 16);
+            *reinterpret_cast<u32x4 *>(a.out_t + gc * a.ld_t + gr) = o;
+        }
+    }
+    if (a.part && t < kTrCols && c0 + t < a.cols) {
+        float s = 0.0f;
+        for (int r = 0; r < kTrRows; ++r)   // rows past the last are zeros
+            s += Elt<true>::load_one(tile, r * kTrCols + (((t >> 3) ^ (r >> 3)) & 7) * 8 + (t & 7));
+        a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + t] = s;
+    }
+}
+
+hipError_t transpose(const TransposeArgs &a, bool bf16_in, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.cols, kTrCols)),
+                    static_cast<unsigned>(ceil_div(std::max(a.rows, a.rows_pad), kTrRows)));
+    if (grid.x == 0 || grid.y == 0) return hipSuccess;
+    if (bf16_in) hipLaunchKernelGGL(transpose_kernel<true>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(transpose_kernel<false>, grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+// Workspace of the backward: regions in bytes
+struct GradLayout {
+    int64_t np;   // tokens in whole eights
+    size_t off_dz, off_dzt, off_xt, off_wt, off_bias, off_part, bytes;
+};
+GradLayout grad_layout(int64_t n, int64_t K, int64_t M) {
+    GradLayout L;
+    L.np = round_up(n, 8);
+    size_t o = 0;
+    L.off_dz = o;    o += align256(static_cast<size_t>(n) * M * 2);
+    L.off_dzt = o;   o += align256(static_cast<size_t>(L.np) * M * 2);
+    L.off_xt = o;    o += align256(static_cast<size_t>(L.np) * K * 2);
+    L.off_wt = o;    o += align256(static_cast<size_t>(M) * K * 2);
+    L.off_bias = o;  o += align256(static_cast<size_t>(ceil_div(n, kTrRows)) * M * 4);
+    L.off_part = o;
+    o += align256(std::max(linear_workspace_bytes(n, M, K, false), linear_workspace_bytes(M, L.np, K, false)));
+    L.bytes = o;
+    return L;
+}
+
+}  // namespace
+
+size_t linear_workspace_bytes(int64_t n, int64_t K, int64_t M, bool fp8) {
+    if (n <= 0 || M <= 0) return 0;
+    const Plan p = plan_of(n, K, M, fp8);
+    return p.splits > 1 ? static_cast<size_t>(p.splits) * n * round_up(M, 8) * 4 : 0;
+}
+
+hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
+    if (a.n <= 0 || a.M <= 0) return hipSuccess;
+    const int es = a.fp8 ? 1 : 2;
+    const Plan p = plan_of(a.n, a.K, a.M, a.fp8);
+    const ShapeInfo &s = kShapes[p.shape];
+    linear::Args g;
+    g.w = static_cast<const unsigned char *>(a.weight);
+    g.x = static_cast<const unsigned char *>(a.x);
+    g.ldw = a.ldw * es;
+    g.ldx = a.ldx * es;
+    g.kbytes = static_cast<int>(a.K * es);
+    g.n = static_cast<int>(a.n);
+    g.M = static_cast<int>(a.M);
+    const int64_t tf = ceil_div(a.M, s.bf), tt = ceil_div(a.n, s.bt), total = tf * tt * p.splits;
+    if (total > 0x7fffffffLL / 16) return hipErrorInvalidValue;
+    g.tiles_f = static_cast<int>(tf);
+    g.tiles_t = static_cast<int>(tt);
+    g.splits = p.splits;
+    g.per_xcd = static_cast<int>(ceil_div(total, 8));
+    g.part = a.part;
+    g.ldpart = round_up(a.M, 8);
+    linear::Epi &e = g.e;
+    e.scale_x = a.scale_x;
+    e.scale_w = a.scale_w;
+    e.bias = a.bias;
+    e.bias_bf16 = a.bias_bf16;
+    e.act = a.act;
+    e.residual = a.residual;
+    e.ldr = a.ldr;
+    e.out = a.out;
+    e.ldo = a.ldo;
+    e.out_bf16 = a.out_bf16;
+    e.preact = a.preact;
+    e.ldp = a.ldp;
+    e.n = a.n;
+    e.M = a.M;
+    const int unit = a.out_bf16 ? 8 : 4;
+    e.vec_out = on16(a.out) && a.ldo % unit == 0 && (!a.residual || (on16(a.residual) && a.ldr % unit == 0));
+    e.vec_pre = on16(a.preact) && a.ldp % 8 == 0;
+    hipError_t err;
+    switch (p.shape) {
+        case 0: err = launch_shape<Big>(g, a.fp8, st); break;
+        case 1: err = launch_shape<Mid>(g, a.fp8, st); break;
+        case 2: err = launch_shape<Low>(g, a.fp8, st); break;
+        default: err = launch_shape<Few>(g, a.fp8, st); break;
+    }
+    if (err != hipSuccess || p.splits == 1) return err;
+    const int64_t items = a.n * (g.ldpart / 8);
+    hipLaunchKernelGGL(linear::linear_fold_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16384))),
+                       dim3(256), 0, st, a.part, g.ldpart, p.splits, e);
+    return hipGetLastError();
+}
+
+size_t linear_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) { return grad_layout(n, K, M).bytes; }
+
+hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st) {
+    const GradLayout L = grad_layout(a.n, a.K, a.M);
+    char *ws = static_cast<char *>(a.workspace);
+    uint16_t *dz = reinterpret_cast<uint16_t *>(ws + L.off_dz), *dzt = reinterpret_cast<uint16_t *>(ws + L.off_dzt);
+    uint16_t *xt = reinterpret_cast<uint16_t *>(ws + L.off_xt), *wt = reinterpret_cast<uint16_t *>(ws + L.off_wt);
+    float *bias_part = reinterpret_cast<float *>(ws + L.off_bias), *part = reinterpret_cast<float *>(ws + L.off_part);
+    const bool active = a.act != ACT_NONE;
+    // without an activation a bf16 grad_out whose rows the product can read is dz
+    const bool direct = !active && a.grad_bf16 && on16(a.grad_out) && a.ldg % 8 == 0;
+    hipError_t e;
+    TransposeArgs d{};
+    d.in = a.grad_out;
+    d.ld_in = a.ldg;
+    d.pre = active ? static_cast<const uint16_t *>(a.preact) : nullptr;
+    d.ld_pre = a.ldp;
+    d.act = a.act;
+    d.out = a.grad_x && !direct ? dz : nullptr;
+    d.ld_out = a.M;
+    d.out_t = a.grad_weight ? dzt : nullptr;
+    d.ld_t = L.np;
+    d.part = a.grad_bias ? bias_part : nullptr;
+    d.rows = static_cast<int>(a.n);
+    d.rows_pad = static_cast<int>(L.np);
+    d.cols = static_cast<int>(a.M);
+    if ((d.out || d.out_t || d.part) && (e = transpose(d, a.grad_bf16, st)) != hipSuccess) return e;
+    if (a.grad_bias && (e = launch_column_fold(bias_part, ceil_div(a.n, kTrRows), a.M, a.M, a.grad_bias, a.grad_bias_bf16,
+                                               st)) != hipSuccess)
+        return e;
+    if (a.grad_x && a.n > 0) {
+        TransposeArgs t{};
+        t.in = a.weight;
+        t.ld_in = a.ldw;
+        t.out_t = wt;
+        t.ld_t = a.M;
+        t.rows = t.rows_pad = static_cast<int>(a.M);
+        t.cols = static_cast<int>(a.K);
+        if ((e = transpose(t, true, st)) != hipSuccess) return e;
+        LinearArgs g{};
+        g.x = direct ? a.grad_out : dz;
+        g.ldx = direct ? a.ldg : a.M;
+        g.weight = wt;
+        g.ldw = a.M;
+        g.n = a.n;
+        g.K = a.M;
+        g.M = a.K;
+        g.out = a.grad_x;
+        g.ldo = a.ldgx;
+        g.out_bf16 = true;
+        g.part = part;
+        if ((e = launch_linear(g, st)) != hipSuccess) return e;
+    }
+    if (a.grad_weight) {
+        TransposeArgs t{};
+        t.in = a.x;
+        t.ld_in = a.ldx;
+        t.out_t = xt;
+        t.ld_t = L.np;
+        t.rows = static_cast<int>(a.n);
+        t.rows_pad = static_cast<int>(L.np);
+        t.cols = static_cast<int>(a.K);
+        if ((e = transpose(t, true, st)) != hipSuccess) return e;
+        LinearArgs g{};
+        g.x = dzt;
+        g.ldx = L.np;
+        g.weight = xt;
+        g.ldw = L.np;
+        g.n = a.M;
+        g.K = L.np;
+        g.M = a.K;
+        g.out = a.grad_weight;
+        g.ldo = a.K;
+        g.out_bf16 = a.grad_weight_bf16;
+        g.part = part;
+        if ((e = launch_linear(g, st)) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace lce

@@ -1,4 +1,4 @@
-"""The operators around the cross-entropy: the final norm, the rules on its logits.
+"""The operators around the cross-entropy: norm, matrix product with an epilogue, rules on logits.
 
 Argument marshalling for the C entry points of the same names (include/lce.h), and the autograd
 forms.  Like the rest of the binding, every function runs on ``stream`` (default: the current
@@ -231,6 +231,187 @@ def _rms_norm_class():
 
 
 _RmsNorm = _LazyFunction(_rms_norm_class)
+
+
+# ---- matrix product with an epilogue ---------------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+@dataclass
+class LinearResult:
+    out: object      # [n, M]
+    preact: object   # bf16 [n, M], or None
+
+
+@dataclass
+class LinearGrads:
+    grad_x: object        # bf16 [n, K], or None
+    grad_weight: object   # [M, K], or None
+    grad_bias: object     # [M], or None
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {name!r} (one of {', '.join(ACTIVATIONS)})")
+    return ACTIVATIONS[name]
+
+
+def _operand(t, name: str, dtype, width: int | None, device):
+    """Checks a 2-D operand of the product; returns (rows, row stride)."""
+    import torch
+    if not torch.is_tensor(t) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape[0], _rows(t, name, dtype, t.shape[0], t.shape[1] if width is None else width, device)
+
+
+def lce_linear_workspace_bytes(n: int, K: int, M: int, e4m3: bool = False) -> int:
+    return int(lib().lce_linear_workspace_bytes(int(n), int(K), int(M), LCE_E4M3 if e4m3 else LCE_BF16))
+
+
+def lce_linear_backward_workspace_bytes(n: int, K: int, M: int) -> int:
+    return int(lib().lce_linear_backward_workspace_bytes(int(n), int(K), int(M)))
+
+
+@_call_stream
+def lce_linear(x, weight, *, bias=None, activation: str = "none", residual=None, scale_x=None, scale_w=None,
+               out_dtype=None, want_preact: bool = False, out=None, preact=None, workspace=None,
+               stream=None) -> LinearResult:
+    """act(x weight^T + bias) + residual for x [n, K] and weight [M, K], both bfloat16 or both
+    float8_e4m3fn (then with ``scale_x`` [n] and ``scale_w`` [M], as lce_rms_norm's e4m3 output has).
+    The output is bfloat16, or (bfloat16 operands) float32 with ``out_dtype``; a residual has its
+    type.  ``want_preact``
+    keeps the activation's input in bf16 for the backward.  Outputs not passed in are allocated."""
+    import torch
+    if not torch.is_tensor(x) or x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("x must be a bfloat16 or float8_e4m3fn tensor")
+    dev = _on_gpu(x, "x")
+    act = _activation(activation)
+    n, ldx = _operand(x, "x", x.dtype, None, dev)
+    K = x.shape[1]
+    M, ldw = _operand(weight, "weight", x.dtype, K, dev)
+    e4m3 = x.dtype == torch.float8_e4m3fn
+    if not e4m3 and (scale_x is not None or scale_w is not None):
+        raise ValueError("scales go with float8_e4m3fn operands")
+    _buf(scale_x, "scale_x", torch.float32, n, dev)
+    _buf(scale_w, "scale_w", torch.float32, M, dev)
+    bcode = LCE_F32
+    if bias is not None:
+        bcode = _float_code(bias, "bias")
+        _buf(bias, "bias", bias.dtype, M, dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    if out is None:
+        out = torch.empty((n, M), dtype=out_dtype, device=dev)
+    if preact is None and want_preact:
+        preact = torch.empty((n, M), dtype=torch.bfloat16, device=dev)
+    ldo = _rows(out, "out", out_dtype, n, M, dev)
+    ldr = _rows(residual, "residual", out_dtype, n, M, dev)
+    ldp = _rows(preact, "preact", torch.bfloat16, n, M, dev)
+    need = lce_linear_workspace_bytes(n, K, M, e4m3)
+    if need and workspace is None:   # clobbered by the call
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _buf(workspace, "workspace", torch.uint8, need, dev)
+    _check(lib().lce_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, LCE_E4M3 if e4m3 else LCE_BF16, _ptr(scale_x),
+                            _ptr(scale_w), _ptr(bias), bcode, act, _ptr(residual), ldr, n, K, M, out.data_ptr(), ldo,
+                            _codes()[out_dtype], _ptr(preact), ldp, _ptr(workspace),
+                            0 if workspace is None else workspace.numel(), stream))
+    return LinearResult(out, preact)
+
+
+@_call_stream
+def lce_linear_backward(grad_out, x, weight, *, activation: str = "none", preact=None, want_grad_x: bool = True,
+                        want_grad_weight: bool = True, want_grad_bias: bool = False, grad_weight_dtype=None,
+                        grad_bias_dtype=None, grad_x=None, grad_weight=None, grad_bias=None, workspace=None,
+                        stream=None) -> LinearGrads:
+    """Gradients of lce_linear (bfloat16 operands) from grad_out [n, M] and, with an activation, the
+    forward's ``preact``; the residual's gradient is grad_out itself.  grad_x is bf16, grad_weight and
+    grad_bias bf16 unless another type is named."""
+    import torch
+    if not torch.is_tensor(x):
+        raise TypeError("x must be a torch tensor")
+    dev = _on_gpu(grad_out, "grad_out")
+    act = _activation(activation)
+    n, ldx = _operand(x, "x", torch.bfloat16, None, dev)
+    K = x.shape[1]
+    M, ldw = _operand(weight, "weight", torch.bfloat16, K, dev)
+    gcode = _float_code(grad_out, "grad_out")
+    ldg = _rows(grad_out, "grad_out", grad_out.dtype, n, M, dev)
+    ldp = _rows(preact, "preact", torch.bfloat16, n, M, dev, required=act != 0)
+    if grad_x is None and want_grad_x:
+        grad_x = torch.empty((n, K), dtype=torch.bfloat16, device=dev)
+    ldgx = _rows(grad_x, "grad_x", torch.bfloat16, n, K, dev)
+    if grad_weight is None and want_grad_weight:
+        grad_weight = torch.empty((M, K), dtype=grad_weight_dtype or torch.bfloat16, device=dev)
+    wcode = bcode = LCE_F32
+    if grad_weight is not None:
+        wcode = _float_code(grad_weight, "grad_weight")
+        _buf(grad_weight, "grad_weight", grad_weight.dtype, M * K, dev)
+    if grad_bias is None and want_grad_bias:
+        grad_bias = torch.empty(M, dtype=grad_bias_dtype or torch.bfloat16, device=dev)
+    if grad_bias is not None:
+        bcode = _float_code(grad_bias, "grad_bias")
+        _buf(grad_bias, "grad_bias", grad_bias.dtype, M, dev)
+    need = lce_linear_backward_workspace_bytes(n, K, M)
+    if workspace is None:   # clobbered by the call
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _buf(workspace, "workspace", torch.uint8, need, dev)
+    _check(lib().lce_linear_backward(grad_out.data_ptr(), ldg, gcode, x.data_ptr(), ldx, weight.data_ptr(), ldw,
+                                     _ptr(preact) if act else None, ldp, act, n, K, M, _ptr(grad_x), ldgx,
+                                     _ptr(grad_weight), wcode, _ptr(grad_bias), bcode, workspace.data_ptr(),
+                                     workspace.numel(), stream))
+    return LinearGrads(grad_x, grad_weight, grad_bias)
+
+
+def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
+    """Autograd form of the product over the last dimension of ``x``: act(x weight^T + bias) + residual,
+    all of x, weight and residual bfloat16 (bias bfloat16 or float32), the output bfloat16 with x's
+    leading dimensions.  Gradients have their inputs' types; sums are fp32.
+    """
+    return _Linear.apply(x, weight, bias, residual, activation)
+
+
+def _linear_class():
+    import torch
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, residual, activation):
+            _on_gpu(x, "x")
+            if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
+                raise ValueError("x must have at least one dimension, and weight two")
+            M = weight.shape[0]
+            shape = (*x.shape[:-1], M)
+            if residual is not None and residual.shape != shape:
+                raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
+            act = _activation(activation)
+            keep = act != 0 and any(ctx.needs_input_grad[:3])
+            r = lce_linear(_rows_of(x, x.shape[-1]), weight, bias=bias, activation=activation,
+                           residual=None if residual is None else _rows_of(residual, M), want_preact=keep)
+            ctx.save_for_backward(x, weight, r.preact)
+            ctx.activation, ctx.bias_dtype = activation, None if bias is None else bias.dtype
+            return r.out.view(shape)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, g):
+            x, weight, preact = ctx.saved_tensors
+            need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+            r = LinearGrads(None, None, None)
+            if need_x or need_w or need_b:
+                r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
+                                        activation=ctx.activation, preact=preact, want_grad_x=need_x,
+                                        want_grad_weight=need_w, want_grad_bias=need_b,
+                                        grad_weight_dtype=weight.dtype, grad_bias_dtype=ctx.bias_dtype)
+            gx = r.grad_x if r.grad_x is None else r.grad_x.view(x.shape)
+            return gx, r.grad_weight, r.grad_bias, (g if need_r else None), None
+
+    return Linear
+
+
+_Linear = _LazyFunction(_linear_class)
 
 
 # ---- rules on logits -------------------------------------------------------------------------
