@@ -215,6 +215,18 @@ def test_a_long_history_counts_every_token():
     assert int((out != 0).sum()) == 3
 
 
+@pytest.mark.parametrize("L,B", [(32767, 65535), (32768, 9), (50, 65536), (0, 70000), (33000, 0)])
+def test_long_lists(L, B):
+    """Both sides of the sizes at which the counts and entries of a column share a word."""
+    n, V = 2, 9000
+    x = torch.randn(n, V, device=DEV)
+    r = _rules(n, V, L, B, L + B, masks=0)         # most columns are listed: more than a slice's list holds
+    if L:
+        r["history"][0] = 77                       # one token as often as the list is long
+        r["prompt_lens"][0] = 0
+    _check(lce.lce_logits_process(x, out=torch.empty_like(x), **r), x, r)
+
+
 def test_offsets_past_32_bits():
     """A row stride that puts the second row 2^31 elements (4 GiB) away."""
     V, ld = 1000, (1 << 31) + 8

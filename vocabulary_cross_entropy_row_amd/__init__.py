@@ -694,8 +694,20 @@ def _deferred_flce_class():
 _DeferredFLCE = _LazyFunction(_deferred_flce_class)
 
 
-# The operators around the cross-entropy (their marshalling is head.py's).
-from .head import (  # noqa: E402
-    ACTIVATIONS, LinearGrads, LinearResult, NormResult, lce_linear, lce_linear_backward,
-    lce_linear_backward_workspace_bytes, lce_linear_workspace_bytes, lce_logits_process, lce_rms_norm,
-    lce_rms_norm_backward, lce_rms_norm_workspace_bytes, linear, rms_norm)
+# The operators around the cross-entropy.  head.py imports torch, so it is loaded on first use.
+_HEAD = frozenset((
+    "ACTIVATIONS", "LinearGrads", "LinearResult", "NormResult", "lce_linear", "lce_linear_backward",
+    "lce_linear_backward_workspace_bytes", "lce_linear_workspace_bytes", "lce_logits_process", "lce_rms_norm",
+    "lce_rms_norm_backward", "lce_rms_norm_workspace_bytes", "linear", "rms_norm"))
+
+
+def __getattr__(name):
+    if name in _HEAD:
+        from . import head
+        value = globals()[name] = getattr(head, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | _HEAD)

@@ -12,14 +12,19 @@
 //   out = allowed(mask row of i, j) ? z : mask_value
 //
 // Bound by memory: each logit is read once and written once.  A workgroup takes
-// a slice of a row's columns and keeps one LDS word per column of it: bit 31 says
-// that the prompt holds the token, the low bits count it among the generated ones
-// (integer atomics, so the order of the history does not change the result), and
-// with biases a second word holds the last entry's index plus one.  So the
+// a slice of a row's columns and keeps one LDS word per column of it.  First the
+// lists are scanned and the word counts: bit 31 says that the prompt holds the
+// token, the bits below count it among the generated ones (integer atomics, so the
+// order of the history does not change the result); a bias list leaves its last
+// entry's index plus one for the column.  Whoever touches a column first puts it
+// on the slice's list.  Then the listed columns, few, are worked out one per lane
+// and their words replaced by the result's bits; the sweep over all columns only
+// selects between a word and the common case.  (Working the penalties out inside
+// the sweep ran a division in half of its steps for a wave's one or two listed
+// columns: 114 us where this takes 52, 256 x 131072 bf16 with every rule.)  The
 // history is read once per slice, from L2 after the first, no table of counts over
-// the vocabulary exists in memory, and nothing is kept between calls.  The
-// slice's logits are requested before the history is scanned and wait in
-// registers meanwhile.
+// the vocabulary exists in memory, and nothing is kept between calls.  The slice's
+// logits are requested before the history is scanned and wait in registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -32,28 +37,52 @@ namespace {
 using dev::Elt;
 using dev::u32x4;
 
-constexpr int kThreads = 256;
-constexpr int kVecs = 4;                        // 16-byte vectors of logits per thread
-constexpr int kSliceVecs = kThreads * kVecs;    // ... per workgroup
+constexpr int kThreads = 512;
 constexpr uint32_t kPrompt = 0x80000000u;
+constexpr int kAhead = 4;   // history ids per thread requested at once
 
-// T tanh(u), u = x / T: an odd polynomial near zero (its next term is below 2^-28
-// of u at 0.25), else (1 - t) / (1 + t) with t = e^{-2 |u|} <= 1.
+// How biases are kept: none; the last entry's index plus one in the low 16 bits of the column's word,
+// the count above it (histories below 2^15 tokens, lists below 2^16 entries); or in a word of its own.
+// Columns a slice lists; with more (a text without repetition in one slice) the sparse step looks at
+// every column's word instead.
+constexpr uint32_t kListed = 2048;
+enum BiasMode { NO_BIAS = 0, PACKED = 1, OWN_WORD = 2 };
+constexpr int64_t kPackedL = 1 << 15, kPackedB = (1 << 16) - 1;
+
+// 16-byte vectors of logits per thread: 8192 columns per workgroup, half with words for the biases
+// (four workgroups of eight waves per CU either way).
+template <bool BF16, int BIAS>
+constexpr int vecs_of() { return (BF16 ? 2 : 4) / (BIAS == OWN_WORD ? 2 : 1); }
+
+// T tanh(u), u = x / T.  Near zero an odd polynomial, else (1 - t) / (1 + t) with t = e^{-2 |u|} <= 1,
+// whose difference loses 2^-24 / |u| of itself there.  fp32 logits need all of fp32: five terms up to
+// 1/4 (the next is below 2^-28 of u); bf16 ones are rounded 2^15 times coarser: two terms up to 1/64
+// (2^-27), the quotient exact to 2^-18 beyond, and five instructions fewer in a sweep that issues
+// about as long as it waits for memory.
+template <bool BF16>
 __device__ __forceinline__ float softcapped(float x, float T, float inv_t) {
-    const float u = x * inv_t, au = fabsf(u), u2 = u * u;
-    const float t = dev::exp2_fast(au * (-2.0f * dev::kLog2e));
-    const float big = copysignf((1.0f - t) * dev::rcp_fast(1.0f + t), u);
-    const float poly =
-        u * fmaf(u2, fmaf(u2, fmaf(u2, fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-    return T * (au < 0.25f ? poly : big);
+    const float u = x * inv_t, u2 = u * u;
+    const float t = dev::exp2_fast(fabsf(u) * (-2.0f * dev::kLog2e));
+    const float big = copysignf((1.0f - t) * dev::rcp_fast(1.0f + t), u) * T;
+    if constexpr (BF16) {
+        return fabsf(u) < 0.015625f ? fmaf(x * u2, -1.0f / 3.0f, x) : big;
+    } else {
+        const float p =
+            fmaf(u2, fmaf(u2, fmaf(u2, fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+        return fabsf(u) < 0.25f ? x * p : big;
+    }
 }
 
-template <bool BF16, typename Id, bool HIST, bool BIAS>
+template <bool BF16, typename Id, bool HIST, int BIAS>
 __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, unsigned slices) {
-    constexpr int E = Elt<BF16>::E, BYTES = Elt<BF16>::bytes;
-    constexpr int COLS = kSliceVecs * E;
-    __shared__ __attribute__((aligned(16))) uint32_t counts[HIST ? COLS : 4];
-    __shared__ __attribute__((aligned(16))) uint32_t entries[BIAS ? COLS : 4];
+    constexpr int E = Elt<BF16>::E, BYTES = Elt<BF16>::bytes, VECS = vecs_of<BF16, BIAS>();
+    constexpr int COLS = kThreads * VECS * E;
+    constexpr bool SPARSE = HIST || BIAS;
+    constexpr int SHIFT = BIAS == PACKED ? 16 : 0;   // where the count starts
+    __shared__ __attribute__((aligned(16))) uint32_t table[SPARSE ? COLS : 4];
+    __shared__ __attribute__((aligned(16))) uint32_t own[BIAS == OWN_WORD ? COLS : 4];
+    __shared__ uint16_t list[SPARSE ? kListed : 4];
+    __shared__ uint32_t listed;
     // workgroups are dealt round robin over the 8 XCDs: a row's slices go to one XCD, whose L2
     // then holds its history
     const unsigned b = blockIdx.x;
@@ -65,116 +94,175 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
     // the row is taken in 16-byte windows of the address space: `lead` elements of the first lie before it
     const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(xrow) & 15) / BYTES);
     const bool vec_out = (reinterpret_cast<uintptr_t>(orow) & 15) / BYTES == static_cast<uintptr_t>(lead);
-    const int64_t base = slice * COLS - lead;   // column of the slice's first element
     const int V = static_cast<int>(a.V);
+    const int base = static_cast<int>(slice * COLS) - lead;   // column of the slice's first element
+    if (base >= V) return;
+    const int tid = threadIdx.x;
 
-    float x[kVecs][E];
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-        const int64_t c = base + (k * kThreads + static_cast<int>(threadIdx.x)) * E;
-        if (c >= 0 && c + E <= V) {
-            const u32x4 q = *reinterpret_cast<const u32x4 *>(xrow + c * BYTES);
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[k][e] = Elt<BF16>::get(q, e);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[k][e] = (c + e >= 0 && c + e < V) ? Elt<BF16>::load_one(xrow, c + e) : 0.0f;
-        }
+    // Everything whose address is known goes out first: a workgroup's time is the chain of its
+    // dependent loads, not its arithmetic.
+    const Id *h = HIST ? static_cast<const Id *>(a.history) + row * a.ldh : nullptr;
+    const Id *bids = BIAS ? static_cast<const Id *>(a.bias_ids) + row * a.ldbi : nullptr;
+    Id ahead[kAhead], bid = static_cast<Id>(-1);
+    if constexpr (BIAS) {
+        if (tid < a.B) bid = bids[tid];
     }
-
-    int64_t len = 0;
     if constexpr (HIST) {
-        len = a.L;
-        if (a.history_lens) {
-            const int64_t l = a.history_lens[row];
-            len = l < 0 ? 0 : (l < a.L ? l : a.L);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            ahead[u] = tid + u * kThreads < a.L ? h[tid + u * kThreads] : static_cast<Id>(-1);
+    }
+    u32x4 x[VECS];
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) {
+        const int c = base + (k * kThreads + tid) * E;
+        x[k] = (u32x4){0u, 0u, 0u, 0u};
+        if (c >= 0 && c + E <= V) {
+            x[k] = *reinterpret_cast<const u32x4 *>(xrow + static_cast<int64_t>(c) * BYTES);
+        } else if (c < V) {
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = (c + e >= 0 && c + e < V) ? Elt<BF16>::load_one(xrow, c + e) : 0.0f;
+            x[k] = Elt<BF16>::pack(v);
         }
     }
-    if constexpr (HIST || BIAS) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        for (int i = threadIdx.x; i < COLS / 4; i += kThreads) {
-            if constexpr (HIST) reinterpret_cast<u32x4 *>(counts)[i] = zero;
-            if constexpr (BIAS) reinterpret_cast<u32x4 *>(entries)[i] = zero;
-        }
-        __syncthreads();
-        if constexpr (HIST) {
-            const Id *h = static_cast<const Id *>(a.history) + row * a.ldh;
-            const int64_t prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
-            for (int64_t i0 = threadIdx.x; i0 < len; i0 += 4 * kThreads) {
-                Id id[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) id[u] = i0 + u * kThreads < len ? h[i0 + u * kThreads] : static_cast<Id>(-1);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (id[u] < 0 || id[u] >= static_cast<Id>(V)) continue;   // padding
-                    const int64_t at = static_cast<int64_t>(id[u]) - base;
-                    if (at < 0 || at >= COLS) continue;
-                    if (i0 + u * kThreads < prompt) atomicOr(&counts[at], kPrompt);
-                    else atomicAdd(&counts[at], 1u);
-                }
-            }
-        }
-        if constexpr (BIAS) {
-            const Id *ids = static_cast<const Id *>(a.bias_ids) + row * a.ldbi;
-            for (int64_t i = threadIdx.x; i < a.B; i += kThreads) {
-                const Id id = ids[i];
-                if (id < 0 || id >= static_cast<Id>(V)) continue;
-                const int64_t at = static_cast<int64_t>(id) - base;
-                if (at >= 0 && at < COLS) atomicMax(&entries[at], static_cast<uint32_t>(i + 1));
-            }
-        }
-        __syncthreads();
-    }
-
+    const float temp = a.temperature ? a.temperature[row] : 0.0f;
+    const float cap = a.softcap, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
     const float rep = a.repetition ? a.repetition[row] : 1.0f;
     const float pres = a.presence ? a.presence[row] : 0.0f;
     const float freq = a.frequency ? a.frequency[row] : 0.0f;
-    const float temp = a.temperature ? a.temperature[row] : 0.0f;
-    const float inv_temp = temp > 0.0f ? 1.0f / temp : 1.0f;
-    const float cap = a.softcap, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
-    const float *bias = BIAS ? a.bias_values + row * a.ldbv : nullptr;
     const uint32_t *words = nullptr;
     if (a.allowed) {
         const int64_t r = a.mask_rows ? a.mask_rows[row] : row;
         if (r >= 0 && r < a.R) words = a.allowed + r * a.ldm;
     }
+    const float inv_temp = temp > 0.0f ? 1.0f / temp : 1.0f;
+    // mask bits of columns c .. c + E - 1: they lie in one word or two (those before the row or past V do
+    // not matter)
+    uint32_t lo[VECS], hi[VECS];
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-        const int local = (k * kThreads + static_cast<int>(threadIdx.x)) * E;
-        const int64_t c = base + local;
-        if (c >= V) continue;
-        uint32_t bits = ~0u;   // bit e: column c + e is allowed
-        if (words) {
-            // columns c .. c + E - 1 lie in one word or two; those before the row or past V do not matter
-            const int64_t c0 = c < 0 ? 0 : c;
-            const int64_t c1 = c + E - 1 < V ? c + E - 1 : V - 1;
-            const uint64_t lo = words[c0 >> 5], hi = words[c1 >> 5];
-            bits = static_cast<uint32_t>(((hi << 32) | lo) >> (c0 & 31));
-            if ((c0 >> 5) == (c1 >> 5)) bits = static_cast<uint32_t>(lo >> (c0 & 31));
-            if (c < 0) bits <<= -c;
+    for (int k = 0; k < VECS; ++k) {
+        const int c = base + (k * kThreads + tid) * E;
+        lo[k] = hi[k] = 0;
+        if (words && c < V) {
+            lo[k] = words[(c < 0 ? 0 : c) >> 5];
+            hi[k] = words[(c + E - 1 < V ? c + E - 1 : V - 1) >> 5];
         }
+    }
+
+    if constexpr (SPARSE) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        for (int i = tid; i < COLS / 4; i += kThreads) {
+            reinterpret_cast<u32x4 *>(table)[i] = zero;
+            if constexpr (BIAS == OWN_WORD) reinterpret_cast<u32x4 *>(own)[i] = zero;
+        }
+        if (tid == 0) listed = 0;
+        __syncthreads();
+        auto push = [&](int at) {
+            const uint32_t i = atomicAdd(&listed, 1u);
+            if (i < kListed) list[i] = static_cast<uint16_t>(at);
+        };
+        auto column = [&](Id id) {   // of the slice, or -1: padding or another slice's
+            if (id < 0 || id >= static_cast<Id>(V)) return -1;
+            const int at = static_cast<int>(id) - base;
+            return at < COLS ? at : -1;   // below the slice: negative already
+        };
+        if constexpr (BIAS) {
+            uint32_t *entries = BIAS == PACKED ? table : own;
+            for (int64_t i = tid; i < a.B; i += kThreads) {
+                const int at = column(i == tid ? bid : bids[i]);
+                if (at < 0) continue;
+                const uint32_t old = atomicMax(&entries[at], static_cast<uint32_t>(i + 1));
+                if (old == 0) push(at);
+            }
+            // a packed word is an entry until here, then counts: the order of the two must not mix; with
+            // words of their own a listed column must not be listed again
+            if constexpr (HIST) __syncthreads();
+        }
+        if constexpr (HIST) {
+            int64_t len = a.L;
+            if (a.history_lens) {
+                const int64_t l = a.history_lens[row];
+                len = l < 0 ? 0 : (l < a.L ? l : a.L);
+            }
+            const int64_t prompt = a.prompt_lens ? a.prompt_lens[row] : 0;
+            for (int64_t i0 = tid; i0 < len; i0 += kAhead * kThreads) {
+                if (i0 != tid) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u)
+                        ahead[u] = i0 + u * kThreads < len ? h[i0 + u * kThreads] : static_cast<Id>(-1);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (i0 + u * kThreads >= len) continue;
+                    const int at = column(ahead[u]);
+                    if (at < 0) continue;
+                    const uint32_t old =
+                        i0 + u * kThreads < prompt ? atomicOr(&table[at], kPrompt) : atomicAdd(&table[at], 1u << SHIFT);
+                    if (old == 0 && (BIAS != OWN_WORD || own[at] == 0)) push(at);
+                }
+            }
+        }
+        __syncthreads();
+        // the listed columns, one per lane
+        const bool all = listed > kListed;
+        const int n = all ? COLS : static_cast<int>(listed);
+        for (int i = tid; i < n; i += kThreads) {
+            const int at = all ? i : list[i];
+            const uint32_t word = table[at];
+            if (all && word == 0 && (BIAS != OWN_WORD || own[at] == 0)) continue;
+            float z = Elt<BF16>::load_one(xrow, base + at);
+            uint32_t entry = 0;
+            if constexpr (BIAS == PACKED) entry = word & 0xffffu;
+            else if constexpr (BIAS == OWN_WORD) entry = own[at];
+            float bias = 0.0f;
+            if constexpr (BIAS) {
+                if (entry) bias = a.bias_values[row * a.ldbv + entry - 1];
+            }
+            if (cap > 0.0f) z = softcapped<BF16>(z, cap, inv_cap);
+            if constexpr (HIST) {
+                const uint32_t made = (word & ~kPrompt) >> SHIFT;
+                if (made | (word & kPrompt)) z = z > 0.0f ? z / rep : z * rep;
+                if (made) z = z - freq * static_cast<float>(made) - pres;
+            }
+            if constexpr (BIAS) {
+                if (entry) z += bias;
+            }
+            const uint32_t bits = __float_as_uint(z * inv_temp);
+            table[at] = bits ? bits : 0x80000000u;   // 0 says that nothing is listed: -0 for 0
+        }
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) {
+        const int local = (k * kThreads + tid) * E;
+        const int c = base + local;
+        if (c >= V) continue;
         float o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float z = x[k][e];
-            if (cap > 0.0f) z = softcapped(z, cap, inv_cap);
-            if constexpr (HIST) {
-                const uint32_t n = counts[local + e];
-                if (n) {
-                    z = z > 0.0f ? z / rep : z * rep;
-                    const uint32_t made = n & ~kPrompt;
-                    if (made) z = z - freq * static_cast<float>(made) - pres;
-                }
+            float z = Elt<BF16>::get(x[k], e);
+            if (cap > 0.0f) z = softcapped<BF16>(z, cap, inv_cap);
+            o[e] = z * inv_temp;
+        }
+        if constexpr (SPARSE) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint32_t w = table[local + e];
+                o[e] = w ? __uint_as_float(w) : o[e];
             }
-            if constexpr (BIAS) {
-                const uint32_t n = entries[local + e];
-                if (n) z += bias[n - 1];
-            }
-            z *= inv_temp;
-            o[e] = (bits >> e) & 1 ? z : a.mask_value;
+        }
+        if (words) {
+            const int c0 = c < 0 ? 0 : c, c1 = c + E - 1 < V ? c + E - 1 : V - 1;
+            uint32_t bits = static_cast<uint32_t>(((static_cast<uint64_t>(hi[k]) << 32) | lo[k]) >> (c0 & 31));
+            if ((c0 >> 5) == (c1 >> 5)) bits = lo[k] >> (c0 & 31);   // bit e: column c + e is allowed
+            if (c < 0) bits <<= -c;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = (bits & (1u << e)) ? o[e] : a.mask_value;
         }
         if (vec_out && c >= 0 && c + E <= V) {
-            *reinterpret_cast<u32x4 *>(orow + c * BYTES) = Elt<BF16>::pack(o);
+            *reinterpret_cast<u32x4 *>(orow + static_cast<int64_t>(c) * BYTES) = Elt<BF16>::pack(o);
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -183,13 +271,14 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
     }
 }
 
-template <bool BF16, typename Id, bool HIST, bool BIAS>
+template <bool BF16, typename Id, bool HIST, int BIAS>
 hipError_t launch(const RulesArgs &a, hipStream_t st) {
-    constexpr int COLS = kSliceVecs * Elt<BF16>::E;
+    constexpr int COLS = kThreads * vecs_of<BF16, BIAS>() * Elt<BF16>::E;
     // a row that starts inside a 16-byte window covers up to E - 1 elements more
-    const int64_t slices = (a.V + Elt<BF16>::E - 1 + COLS - 1) / COLS;
+    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ldx * Elt<BF16>::bytes % 16 == 0;
+    const int64_t slices = (a.V + (aligned ? 0 : Elt<BF16>::E - 1) + COLS - 1) / COLS;
     // a launch has fewer than 2^32 threads
-    const int64_t rows = ((int64_t(1) << 23) / slices) / 8 * 8;
+    const int64_t rows = ((int64_t(1) << 22) / slices) / 8 * 8;
     for (int64_t r = 0; r < a.n; r += rows) {
         RulesArgs b = a;
         b.n = a.n - r < rows ? a.n - r : rows;
@@ -223,8 +312,9 @@ hipError_t launch(const RulesArgs &a, hipStream_t st) {
 
 template <bool BF16, typename Id>
 hipError_t pick(const RulesArgs &a, hipStream_t st) {
-    if (a.history) return a.bias_ids ? launch<BF16, Id, true, true>(a, st) : launch<BF16, Id, true, false>(a, st);
-    return a.bias_ids ? launch<BF16, Id, false, true>(a, st) : launch<BF16, Id, false, false>(a, st);
+    if (!a.bias_ids) return a.history ? launch<BF16, Id, true, NO_BIAS>(a, st) : launch<BF16, Id, false, NO_BIAS>(a, st);
+    if (!a.history) return a.B <= kPackedB ? launch<BF16, Id, false, PACKED>(a, st) : launch<BF16, Id, false, OWN_WORD>(a, st);
+    return a.L < kPackedL && a.B <= kPackedB ? launch<BF16, Id, true, PACKED>(a, st) : launch<BF16, Id, true, OWN_WORD>(a, st);
 }
 
 }  // namespace

@@ -10,35 +10,35 @@ from __future__ import annotations
 import functools
 from dataclasses import dataclass
 
-from . import (LCE_BF16, LCE_E4M3, LCE_F32, _LazyFunction, _buf, _check, _on_gpu, _ptr, _torch_stream, lib)
+import torch
+
+from . import LCE_BF16, LCE_E4M3, LCE_F32, _check, _on_gpu, _ptr, _torch_stream, lib
+
+_CODES = {torch.float32: LCE_F32, torch.bfloat16: LCE_BF16, torch.float8_e4m3fn: LCE_E4M3}
+# The current stream's handle, without the stream object around it (3 us of a 10 us call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call_stream(fn):
     """Runs a binding function with its call stream and device current; the function receives the
     stream's handle as ``stream``.  The common call -- no stream named, tensors of the current
     device -- switches nothing."""
-
     @functools.wraps(fn)
     def wrapper(first, *args, stream=None, **kw):
-        import torch
-        if not (torch.is_tensor(first) and first.device.type == "cuda"):
+        if not (torch.is_tensor(first) and first.is_cuda):
             return fn(first, *args, stream=0, **kw)   # the function's own checks raise
-        if stream is None and first.device.index == torch.cuda.current_device():
-            return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
-        st = _torch_stream(stream, first.device)
-        with torch.cuda.device(first.device), torch.cuda.stream(st):
+        device = first.device
+        if stream is None and device.index == torch.cuda.current_device():
+            return fn(first, *args, stream=_current_stream(device.index), **kw)
+        st = _torch_stream(stream, device)
+        with torch.cuda.device(device), torch.cuda.stream(st):
             return fn(first, *args, stream=st.cuda_stream, **kw)
     return wrapper
 
 
-@functools.lru_cache(maxsize=None)
-def _codes():
-    import torch
-    return {torch.float32: LCE_F32, torch.bfloat16: LCE_BF16, torch.float8_e4m3fn: LCE_E4M3}
-
-
 def _float_code(t, name: str) -> int:
-    code = _codes().get(t.dtype)
+    code = _CODES.get(t.dtype)
     if code is None or code == LCE_E4M3:
         raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
     return code
@@ -46,22 +46,38 @@ def _float_code(t, name: str) -> int:
 
 def _rows(t, name: str, dtype, n: int, width: int, device, required: bool = False) -> int:
     """Checks a [n, width] operand with unit column stride; returns its row stride."""
-    import torch
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
         return width
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.shape != (n, width):
         raise ValueError(f"{name} must be [{n}, {width}] (got {list(t.shape)})")
-    if width > 1 and t.stride(1) != 1:
+    row, column = t.stride()
+    if column != 1 and width > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.stride(0) if n > 1 else width
+    return row if n > 1 else width
+
+
+def _buf(t, name: str, dtype, numel: int, device, required: bool = False) -> None:
+    """Checks a contiguous buffer of at least ``numel`` values."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name} needs at least {numel} contiguous elements (got {list(t.shape)}, strides {t.stride()})")
 
 
 # ---- root-mean-square norm -------------------------------------------------------------------
@@ -77,7 +93,6 @@ class NormResult:
 def _norm_weight(weight, H: int, device):
     if weight is None:
         return LCE_F32
-    import torch
     if not torch.is_tensor(weight):
         raise TypeError("weight must be a torch tensor")
     if weight.device != device:
@@ -94,7 +109,6 @@ def lce_rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_off
     type; x without a residual).  ``x`` is a [n, H] view with unit column stride.  With ``out_dtype``
     torch.float8_e4m3fn, y holds y / scale with one scale per row.  Outputs not passed in are
     allocated; ``sum_out`` may be ``x`` or ``residual`` itself."""
-    import torch
     if not torch.is_tensor(x) or x.dim() != 2:
         raise ValueError("x must be a 2-D tensor")
     dev = _on_gpu(x, "x")
@@ -105,7 +119,7 @@ def lce_rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_off
     wcode = _norm_weight(weight, H, dev)
     if out_dtype is None:
         out_dtype = x.dtype if y is None else y.dtype
-    ycode = _codes().get(out_dtype)
+    ycode = _CODES.get(out_dtype)
     if out_dtype != x.dtype and ycode != LCE_E4M3:
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn (got {out_dtype})")
     if y is None:
@@ -138,7 +152,6 @@ def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offs
     """(grad_x, grad_weight) of lce_rms_norm from its ``s`` (the sum; x without a residual) and ``rstd``.
     grad_x is the gradient of x and of the residual alike; grad_weight has the weight's type (None
     without a weight or with ``want_grad_weight`` false)."""
-    import torch
     if not torch.is_tensor(s) or s.dim() != 2:
         raise ValueError("s must be a 2-D tensor")
     dev = _on_gpu(grad_y, "grad_y")
@@ -172,10 +185,52 @@ def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offs
 
 def _rows_of(t, H: int):
     """t with its leading dimensions as rows of H, unit column stride, no two rows overlapping."""
-    t = t.reshape(-1, H)
-    if (H > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < H):
+    if t.dim() != 2:
+        t = t.reshape(-1, H)
+    row, column = t.stride()
+    if (H > 1 and column != 1) or (t.shape[0] > 1 and row < H):
         t = t.contiguous()
     return t
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, offset):
+        _on_gpu(x, "x")
+        if x.dim() < 1:
+            raise ValueError("x must have at least one dimension")
+        H = x.shape[-1]
+        x2, r2, total, sum2 = _rows_of(x, H), None, None, None
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if residual is not None:
+            if residual.shape != x.shape:
+                raise ValueError(f"residual must have the shape of x, {list(x.shape)} (got {list(residual.shape)})")
+            r2 = _rows_of(residual, H)
+            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            sum2 = _rows_of(total, H)
+        rstd = lce_rms_norm(x2, weight, residual=r2, eps=eps, weight_offset=offset, want_rstd=True, y=_rows_of(y, H),
+                            sum_out=sum2).rstd
+        ctx.set_materialize_grads(False)
+        ctx.offset = offset
+        if residual is None:
+            ctx.save_for_backward(x, weight, rstd)
+            return y
+        ctx.save_for_backward(total, weight, rstd)
+        return y, total
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy, gs=None):
+        s, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if gy is None:   # nothing came through the norm
+            return (gs if need_x else None), None, (gs if need_r else None), None, None
+        H = s.shape[-1]
+        gx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+        _, gw = lce_rms_norm_backward(_rows_of(gy, H), _rows_of(s, H), weight, rstd,
+                                      grad_sum=None if gs is None else _rows_of(gs, H), weight_offset=ctx.offset,
+                                      grad_x=_rows_of(gx, H), want_grad_weight=need_w)
+        return (gx if need_x else None), gw, (gx if need_r else None), None, None
 
 
 def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
@@ -186,51 +241,6 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     ``sum`` is added in the same kernel.
     """
     return _RmsNorm.apply(x, weight, residual, float(eps), float(weight_offset))
-
-
-def _rms_norm_class():
-    import torch
-
-    class RmsNorm(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, weight, residual, eps, offset):
-            _on_gpu(x, "x")
-            if x.dim() < 1:
-                raise ValueError("x must have at least one dimension")
-            if residual is not None and residual.shape != x.shape:
-                raise ValueError(f"residual must have the shape of x, {list(x.shape)} (got {list(residual.shape)})")
-            H = x.shape[-1]
-            x2 = _rows_of(x, H)
-            r = lce_rms_norm(x2, weight, residual=None if residual is None else _rows_of(residual, H), eps=eps,
-                             weight_offset=offset, want_rstd=True)
-            ctx.set_materialize_grads(False)
-            ctx.offset = offset
-            y = r.y.view(x.shape)
-            if residual is None:
-                ctx.save_for_backward(x, weight, r.rstd)
-                return y
-            total = r.sum.view(x.shape)
-            ctx.save_for_backward(total, weight, r.rstd)
-            return y, total
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, gy, gs=None):
-            s, weight, rstd = ctx.saved_tensors
-            H = s.shape[-1]
-            need_x, need_w, need_r = ctx.needs_input_grad[:3]
-            if gy is None:   # nothing came through the norm
-                return (gs if need_x else None), None, (gs if need_r else None), None, None
-            gx, gw = lce_rms_norm_backward(_rows_of(gy, H), _rows_of(s, H), weight, rstd,
-                                           grad_sum=None if gs is None else _rows_of(gs, H),
-                                           weight_offset=ctx.offset, want_grad_weight=need_w)
-            gx = gx.view(s.shape)
-            return (gx if need_x else None), gw, (gx if need_r else None), None, None
-
-    return RmsNorm
-
-
-_RmsNorm = _LazyFunction(_rms_norm_class)
 
 
 # ---- matrix product with an epilogue ---------------------------------------------------------
@@ -259,7 +269,6 @@ def _activation(name: str) -> int:
 
 def _operand(t, name: str, dtype, width: int | None, device):
     """Checks a 2-D operand of the product; returns (rows, row stride)."""
-    import torch
     if not torch.is_tensor(t) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     return t.shape[0], _rows(t, name, dtype, t.shape[0], t.shape[1] if width is None else width, device)
@@ -282,7 +291,6 @@ def lce_linear(x, weight, *, bias=None, activation: str = "none", residual=None,
     The output is bfloat16, or (bfloat16 operands) float32 with ``out_dtype``; a residual has its
     type.  ``want_preact``
     keeps the activation's input in bf16 for the backward.  Outputs not passed in are allocated."""
-    import torch
     if not torch.is_tensor(x) or x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise TypeError("x must be a bfloat16 or float8_e4m3fn tensor")
     dev = _on_gpu(x, "x")
@@ -316,7 +324,7 @@ def lce_linear(x, weight, *, bias=None, activation: str = "none", residual=None,
     _buf(workspace, "workspace", torch.uint8, need, dev)
     _check(lib().lce_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, LCE_E4M3 if e4m3 else LCE_BF16, _ptr(scale_x),
                             _ptr(scale_w), _ptr(bias), bcode, act, _ptr(residual), ldr, n, K, M, out.data_ptr(), ldo,
-                            _codes()[out_dtype], _ptr(preact), ldp, _ptr(workspace),
+                            _CODES[out_dtype], _ptr(preact), ldp, _ptr(workspace),
                             0 if workspace is None else workspace.numel(), stream))
     return LinearResult(out, preact)
 
@@ -329,7 +337,6 @@ def lce_linear_backward(grad_out, x, weight, *, activation: str = "none", preact
     """Gradients of lce_linear (bfloat16 operands) from grad_out [n, M] and, with an activation, the
     forward's ``preact``; the residual's gradient is grad_out itself.  grad_x is bf16, grad_weight and
     grad_bias bf16 unless another type is named."""
-    import torch
     if not torch.is_tensor(x):
         raise TypeError("x must be a torch tensor")
     dev = _on_gpu(grad_out, "grad_out")
@@ -365,6 +372,42 @@ def lce_linear_backward(grad_out, x, weight, *, activation: str = "none", preact
     return LinearGrads(grad_x, grad_weight, grad_bias)
 
 
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        _on_gpu(x, "x")
+        if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
+            raise ValueError("x must have at least one dimension, and weight two")
+        M = weight.shape[0]
+        shape = (*x.shape[:-1], M)
+        if residual is not None and residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
+        keep = _activation(activation) != 0 and any(ctx.needs_input_grad[:3])
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        preact = lce_linear(_rows_of(x, x.shape[-1]), weight, bias=bias, activation=activation,
+                            residual=None if residual is None else _rows_of(residual, M), want_preact=keep,
+                            out=_rows_of(out, M)).preact
+        ctx.save_for_backward(x, weight, preact)
+        ctx.activation, ctx.bias_dtype = activation, None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        x, weight, preact = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        gx = gw = gb = None
+        if need_x or need_w or need_b:
+            if need_x:
+                gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
+                                    activation=ctx.activation, preact=preact, want_grad_x=need_x,
+                                    want_grad_weight=need_w, want_grad_bias=need_b, grad_weight_dtype=weight.dtype,
+                                    grad_bias_dtype=ctx.bias_dtype, grad_x=gx if gx is None else _rows_of(gx, x.shape[-1]))
+            gw, gb = r.grad_weight, r.grad_bias
+        return gx, gw, gb, (g if need_r else None), None
+
+
 def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
     """Autograd form of the product over the last dimension of ``x``: act(x weight^T + bias) + residual,
     all of x, weight and residual bfloat16 (bias bfloat16 or float32), the output bfloat16 with x's
@@ -373,53 +416,11 @@ def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
     return _Linear.apply(x, weight, bias, residual, activation)
 
 
-def _linear_class():
-    import torch
-
-    class Linear(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, weight, bias, residual, activation):
-            _on_gpu(x, "x")
-            if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
-                raise ValueError("x must have at least one dimension, and weight two")
-            M = weight.shape[0]
-            shape = (*x.shape[:-1], M)
-            if residual is not None and residual.shape != shape:
-                raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
-            act = _activation(activation)
-            keep = act != 0 and any(ctx.needs_input_grad[:3])
-            r = lce_linear(_rows_of(x, x.shape[-1]), weight, bias=bias, activation=activation,
-                           residual=None if residual is None else _rows_of(residual, M), want_preact=keep)
-            ctx.save_for_backward(x, weight, r.preact)
-            ctx.activation, ctx.bias_dtype = activation, None if bias is None else bias.dtype
-            return r.out.view(shape)
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, g):
-            x, weight, preact = ctx.saved_tensors
-            need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-            r = LinearGrads(None, None, None)
-            if need_x or need_w or need_b:
-                r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
-                                        activation=ctx.activation, preact=preact, want_grad_x=need_x,
-                                        want_grad_weight=need_w, want_grad_bias=need_b,
-                                        grad_weight_dtype=weight.dtype, grad_bias_dtype=ctx.bias_dtype)
-            gx = r.grad_x if r.grad_x is None else r.grad_x.view(x.shape)
-            return gx, r.grad_weight, r.grad_bias, (g if need_r else None), None
-
-    return Linear
-
-
-_Linear = _LazyFunction(_linear_class)
-
-
 # ---- rules on logits -------------------------------------------------------------------------
 
 def _ids(t, name: str, n: int, device):
     """Checks a [n, L] list of token ids (int32 or int64); returns (row stride, length).  A row stride
     of 0 (one list expanded over the rows) is kept."""
-    import torch
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
@@ -450,7 +451,6 @@ def lce_logits_process(logits, *, history=None, history_lens=None, prompt_lens=N
     presence, frequency and temperature are fp32 [n].  Writes to ``out``, or in place, and returns it;
     lce_ce_argmax reads it from there, and with ``mask_value`` -1e4 (the losses need finite logits)
     lce_ce_stats and lce_ce_combine."""
-    import torch
     if not torch.is_tensor(logits) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D view with unit column stride")
     dev = _on_gpu(logits, "logits")
