@@ -50,7 +50,8 @@ def _forward64(x, res, w, eps, offset):
 
 
 SHAPES = [(1, 1), (3, 7), (5, 64), (16, 128), (9, 129), (17, 512), (33, 1000), (7, 2048), (4, 4096), (3, 4099),
-          (2, 6656), (3, 8192), (2, 8200), (2, 16384), (2, 16383), (1300, 256), (300, 1003)]
+          (2, 6656), (3, 8192), (2, 8200), (2, 16384), (2, 16383), (1300, 256), (300, 1003),
+          (41, 768), (7, 1536), (2, 3080), (700, 4160), (513, 2056)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])

@@ -230,39 +230,69 @@ __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_kernel(NormArgs a) {
     }
 }
 
+// An access of a row as loaded: 16 bytes, or one widened value
+template <int E>
+struct Raw { typedef u32x4 type; };
+template <>
+struct Raw<1> { typedef float type; };
+template <bool BF16, int E>
+__device__ __forceinline__ typename Raw<E>::type load_raw(const void *p, int64_t i) {
+    if constexpr (E == 1) return Elt<BF16>::load_one(p, i);
+    else return *reinterpret_cast<const u32x4 *>(static_cast<const char *>(p) + i * Elt<BF16>::bytes);
+}
+template <bool BF16, int E>
+__device__ __forceinline__ float raw_get(const typename Raw<E>::type &v, int e) {
+    if constexpr (E == 1) return v;
+    else return Elt<BF16>::get(v, e);
+}
+
 // A workgroup walks rows blockIdx, blockIdx + gridDim, ... (groups of ROWS) and
-// keeps its part of dL/dw in registers, one fp32 sum per column.
+// keeps its part of dL/dw in registers, one fp32 sum per column.  The next row's
+// values are requested before this row is reduced and stored.  They wait as
+// loaded, not widened, so that sixteen waves fit a CU: 8192 x 6656 bf16 takes
+// 136 us with widened rows, no request ahead and twelve waves.
 template <bool BF16, int E, int LPR, int K>
 __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_backward_kernel(NormGradArgs a) {
     constexpr int ROWS = threads_of(LPR) / LPR;
+    typedef typename Raw<E>::type raw;
+    // shapes with more accesses per lane have no registers left for another row
+    constexpr bool AHEAD = E > 1 ? K <= 2 : K <= 4;
+    struct Row {
+        raw s[K], g[K], d[K];
+        float rstd;
+    };
     __shared__ float sh[2][16];
     __shared__ float fold[ROWS > 1 ? ROWS * LPR * K * E : 1];
     const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     const int H = static_cast<int>(a.H);
     const float inv_h = 1.0f / static_cast<float>(H);
+    auto fetch = [&](int64_t row, Row &v) {   // zeros past the last row and past H
+        v.rstd = row < a.n ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * LPR + lane) * E;
+            v.s[k] = v.g[k] = v.d[k] = raw{};
+            if (c < H && row < a.n) {
+                v.s[k] = load_raw<BF16, E>(a.s, row * a.lds + c);
+                v.g[k] = load_raw<BF16, E>(a.gy, row * a.ldg + c);
+                if (AHEAD && a.gs) v.d[k] = load_raw<BF16, E>(a.gs, row * a.ldgs + c);
+            }
+        }
+    };
     float gw[K][E];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) gw[k][e] = 0.0f;
     int turn = 0;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS; row0 < a.n;
-         row0 += static_cast<int64_t>(gridDim.x) * ROWS, turn ^= 1) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+    Row cur, next;
+    if constexpr (AHEAD) fetch(static_cast<int64_t>(blockIdx.x) * ROWS + sub, cur);
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS; row0 < a.n; row0 += step, turn ^= 1) {
         const int64_t row = row0 + sub;
-        const bool there = ROWS == 1 || row < a.n;
-        float s[K][E], g[K][E];
+        fetch(AHEAD ? row + step : row, AHEAD ? next : cur);
+        const float rstd = cur.rstd;
         float dot = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * LPR + lane) * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[k][e] = g[k][e] = 0.0f;
-            if (c < H && there) {
-                load_vals<BF16, E>(a.s, row * a.lds + c, s[k]);
-                load_vals<BF16, E>(a.gy, row * a.ldg + c, g[k]);
-            }
-        }
-        const float rstd = there ? a.rstd[row] : 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * LPR + lane) * E;
@@ -271,10 +301,9 @@ __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_backward_kernel(Norm
             load_weight<E>(a.weight, a.weight_bf16, a.offset, c, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float gv = g[k][e];
-                gw[k][e] = fmaf(gv, s[k][e] * rstd, gw[k][e]);
-                g[k][e] = gv * w[e];
-                dot = fmaf(g[k][e], s[k][e], dot);
+                const float sv = raw_get<BF16, E>(cur.s[k], e), gv = raw_get<BF16, E>(cur.g[k], e);
+                gw[k][e] = fmaf(gv, sv * rstd, gw[k][e]);
+                dot = fmaf(gv * w[e], sv, dot);
             }
         }
         dot = row_sum<LPR>(dot, sh[turn]);
@@ -282,16 +311,17 @@ __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_backward_kernel(Norm
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * LPR + lane) * E;
-            if (c >= H || !there) continue;
-            float gs[E];
+            if (c >= H || row >= a.n) continue;
+            float w[E], o[E];
+            load_weight<E>(a.weight, a.weight_bf16, a.offset, c, w);
+            if (!AHEAD && a.gs) cur.d[k] = load_raw<BF16, E>(a.gs, row * a.ldgs + c);
 #pragma unroll
-            for (int e = 0; e < E; ++e) gs[e] = 0.0f;
-            if (a.gs) load_vals<BF16, E>(a.gs, row * a.ldgs + c, gs);
-            float o[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(rstd, fmaf(-s[k][e], t, g[k][e]), gs[e]);
+            for (int e = 0; e < E; ++e)
+                o[e] = fmaf(rstd, fmaf(-raw_get<BF16, E>(cur.s[k], e), t, raw_get<BF16, E>(cur.g[k], e) * w[e]),
+                            raw_get<BF16, E>(cur.d[k], e));
             store_vals<BF16, E>(a.gx, row * a.ldgx + c, o);
         }
+        if constexpr (AHEAD) cur = next;
     }
     if (!a.gw) return;
     float *part = a.part + static_cast<int64_t>(blockIdx.x) * H;
@@ -349,8 +379,12 @@ __global__ __launch_bounds__(256) void column_fold_kernel(const float *part, int
 struct Plan {
     int e, lpr, k;
 };
-// Lanes by the number of accesses a row has: a 16-lane group for head-sized rows
-// (four rows per wave), a wave up to 256 accesses, then workgroups.
+// Lanes by the number of accesses a row has: a 16-lane group for head-sized rows (four rows per wave),
+// then as many lanes as keep one or two accesses each: a row's time is one load, one reduction and one
+// store, and short ones keep more rows in flight.  Forward, residual, bf16: 16384 x 1536 35 us with 256
+// lanes of one access, 41 with a wave of four; 16384 x 4096 91 us with 512 of one, 99 with 256 of two;
+// 8192 x 6656 83 us with 512 of two, 93 with 256 of four; 16384 x 1024 22 us with a wave of two, 24
+// with 256 of one.
 Plan plan_of(int64_t H, bool vec, int e) {
     if (!vec) {
         if (H <= 256) return {1, 64, 4};
@@ -361,9 +395,10 @@ Plan plan_of(int64_t H, bool vec, int e) {
     const int64_t nv = H / e;
     if (nv <= 16) return {e, 16, 1};
     if (nv <= 64) return {e, 64, 1};
-    if (nv <= 256) return {e, 64, 4};
-    if (nv <= 512) return {e, 256, 2};
-    if (nv <= 1024) return {e, 256, 4};
+    if (nv <= 128) return {e, 64, 2};
+    if (nv <= 256) return {e, 256, 1};
+    if (nv <= 512) return {e, 512, 1};
+    if (nv <= 1024) return {e, 512, 2};
     if (nv <= 2048) return {e, 1024, 2};
     return {e, 1024, 4};
 }
@@ -392,9 +427,10 @@ void pick_fwd(const NormArgs &a, const Plan &p, hipStream_t st) {
     } else {
         if (p.lpr == 16) launch_fwd<BF16, OUT8, E, 16, 1>(a, st);
         else if (p.lpr == 64 && p.k == 1) launch_fwd<BF16, OUT8, E, 64, 1>(a, st);
-        else if (p.lpr == 64) launch_fwd<BF16, OUT8, E, 64, 4>(a, st);
-        else if (p.lpr == 256 && p.k == 2) launch_fwd<BF16, OUT8, E, 256, 2>(a, st);
-        else if (p.lpr == 256) launch_fwd<BF16, OUT8, E, 256, 4>(a, st);
+        else if (p.lpr == 64) launch_fwd<BF16, OUT8, E, 64, 2>(a, st);
+        else if (p.lpr == 256) launch_fwd<BF16, OUT8, E, 256, 1>(a, st);
+        else if (p.lpr == 512 && p.k == 1) launch_fwd<BF16, OUT8, E, 512, 1>(a, st);
+        else if (p.lpr == 512) launch_fwd<BF16, OUT8, E, 512, 2>(a, st);
         else if (E == 8 || p.k == 2) launch_fwd<BF16, OUT8, E, 1024, 2>(a, st);
         else launch_fwd<BF16, OUT8, E, 1024, E == 8 ? 2 : 4>(a, st);   // fp32 only: bf16 rows end at 2048 accesses
     }
@@ -404,8 +440,8 @@ template <bool BF16, int E, int LPR, int K>
 void launch_bwd(const NormGradArgs &a, hipStream_t st, int64_t *groups) {
     constexpr int ROWS = threads_of(LPR) / LPR;
     const int64_t want = (a.n + ROWS - 1) / ROWS;
-    // workgroups a compute unit holds at once
-    const int64_t most = std::min<int64_t>(kNormMaxGroups, static_cast<int64_t>(device_cu_count()) * (LPR > 256 ? 2 : 4));
+    // sixteen waves on every compute unit: all groups run at once, and few partial rows
+    const int64_t most = std::min<int64_t>(kNormMaxGroups, static_cast<int64_t>(device_cu_count()) * (1024 / threads_of(LPR)));
     *groups = std::min(want, most);
     hipLaunchKernelGGL((rms_norm_backward_kernel<BF16, E, LPR, K>), dim3(static_cast<unsigned>(*groups)),
                        dim3(threads_of(LPR)), 0, st, a);
@@ -420,9 +456,10 @@ void pick_bwd(const NormGradArgs &a, const Plan &p, hipStream_t st, int64_t *gro
     } else {
         if (p.lpr == 16) launch_bwd<BF16, E, 16, 1>(a, st, groups);
         else if (p.lpr == 64 && p.k == 1) launch_bwd<BF16, E, 64, 1>(a, st, groups);
-        else if (p.lpr == 64) launch_bwd<BF16, E, 64, 4>(a, st, groups);
-        else if (p.lpr == 256 && p.k == 2) launch_bwd<BF16, E, 256, 2>(a, st, groups);
-        else if (p.lpr == 256) launch_bwd<BF16, E, 256, 4>(a, st, groups);
+        else if (p.lpr == 64) launch_bwd<BF16, E, 64, 2>(a, st, groups);
+        else if (p.lpr == 256) launch_bwd<BF16, E, 256, 1>(a, st, groups);
+        else if (p.lpr == 512 && p.k == 1) launch_bwd<BF16, E, 512, 1>(a, st, groups);
+        else if (p.lpr == 512) launch_bwd<BF16, E, 512, 2>(a, st, groups);
         else if (E == 8 || p.k == 2) launch_bwd<BF16, E, 1024, 2>(a, st, groups);
         else launch_bwd<BF16, E, 1024, E == 8 ? 2 : 4>(a, st, groups);   // fp32 only
     }
