@@ -31,20 +31,32 @@ bool on16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // ---- tile shapes ------------------------------------------------------------------
 
-using Big = linear::Shape<256, 256, 2, 4, 3, 2>;     // one workgroup of 8 waves per CU
-using Mid = linear::Shape<128, 128, 2, 2, 2, 2>;     // two of 4 waves
-using Low = linear::Shape<128, 64, 2, 2, 3, 3>;
-using Few = linear::Shape<128, 32, 4, 1, 4, 4>;
+using Big = linear::Shape<256, 256, 2, 4, 3, 2>;    // one workgroup of eight waves per CU
+using Wide = linear::Shape<256, 128, 4, 2, 3, 3>;   // one
+using Low = linear::Shape<128, 64, 2, 2, 3, 3>;     // two of four waves
+using Tiny = linear::Shape<64, 32, 2, 1, 4, 4>;     // three of two
+enum { BIG, WIDE, LOW, TINY, ROWS16, ROWS32, SHAPES };   // ROWS: linear_rows_kernel, up to 16 and 32 tokens
 
+// What a shape's workgroups cost, in us: a step of K with 1, 2 or 3 of them on a compute unit, a
+// workgroup's start and end, the launch, and what its tile moves at (bytes per us); for a product split
+// along K the second launch and the rate of the partial sums.  Fitted to the times of each shape, with
+// 1 to 16 splits, over 208 random bf16 products (n 1 to 4096, K 256 to 8192, M 256 to 202048) and 112
+// e4m3 ones: off by 10 to 14% (root mean square); the choice that the estimates make is 3% slower than
+// the fastest measured one on geometric average.
+struct Cost {
+    double step[3], tile, launch, rate, fold, fold_rate;
+};
 struct ShapeInfo {
     int bf, bt, per_cu;
-    double tflops, tflops8;   // of one compute unit with this shape, bf16 and e4m3 (measured, long K)
+    Cost bf16, e4m3;
 };
-constexpr ShapeInfo kShapes[] = {
-    {Big::BF, Big::BT, Big::PER_CU, 5.0, 9.0},
-    {Mid::BF, Mid::BT, Mid::PER_CU, 3.6, 5.5},
-    {Low::BF, Low::BT, Low::PER_CU, 2.6, 3.5},
-    {Few::BF, Few::BT, Few::PER_CU, 1.4, 1.6},
+constexpr ShapeInfo kShapes[SHAPES] = {
+    {Big::BF, Big::BT, 1, {{1.22, 0, 0}, 7.5, 0.3, 4.0e6, 2.2, 5.5e6}, {{1.48, 0, 0}, 8.4, 0.8, 2.8e6, 1.1, 4.9e6}},
+    {Wide::BF, Wide::BT, 1, {{0.82, 0, 0}, 5.5, 0.0, 4.3e6, 3.1, 6.1e6}, {{0.86, 0, 0}, 6.2, 0.2, 3.4e6, 2.7, 4.9e6}},
+    {Low::BF, Low::BT, 2, {{0.38, 0.85, 0}, 0.1, 4.3, 4.8e6, 3.2, 6.4e6}, {{0.33, 0.89, 0}, 1.8, 3.2, 4.1e6, 3.1, 4.6e6}},
+    {Tiny::BF, Tiny::BT, 3, {{0.28, 0.38, 0.58}, 0.4, 3.9, 4.7e6, 2.9, 4.8e6}, {{0.23, 0.51, 0.55}, 1.7, 2.6, 4.3e6, 3.0, 4.0e6}},
+    {16, 16, 2, {{0.04, 0.16, 0}, 4.7, 0.7, 4.0e6, 0, 1}, {{0.03, 0.19, 0}, 4.3, 1.1, 8.0e6, 0, 1}},
+    {16, 32, 3, {{0.10, 0.30, 0.55}, 2.4, 2.8, 8.0e6, 0, 1}, {{0.11, 0.24, 0.56}, 4.5, 0.0, 8.0e6, 0, 1}},
 };
 constexpr int kCus = 256;        // compute units of an MI355X
 constexpr int kMaxSplits = 16;
@@ -53,26 +65,26 @@ struct Plan {
     int shape, splits;
 };
 // The tile shape and K splits with the least estimated time: whole rounds of workgroups over the
-// compute units at the shape's rate, not less than reading the operands and writing the output at
-// 5 TB/s, plus for a split product its partials and second launch.
+// compute units, the last one as full as it is, and not less than the bytes take.
 Plan plan_of(int64_t n, int64_t K, int64_t M, bool fp8) {
     const int es = fp8 ? 1 : 2;
     const int64_t steps = std::max<int64_t>(1, ceil_div(K * es, linear::kStepBytes));
-    const double stream = (static_cast<double>(n + M) * K * es + 2.0 * n * M) / 5.0e6;   // us
-    Plan best{0, 1};
+    const double bytes = static_cast<double>(n + M) * K * es + 2.0 * n * M;
+    Plan best{BIG, 1};
     double best_us = 1e30;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < SHAPES; ++i) {
+        const bool rows = i == ROWS16 || i == ROWS32;
+        if (rows && (n > kShapes[i].bt || (i == ROWS32 && n <= kShapes[ROWS16].bt))) continue;
         const ShapeInfo &s = kShapes[i];
-        const int64_t tiles = ceil_div(M, s.bf) * ceil_div(n, s.bt);
-        const double step_flops = 2.0 * s.bf * s.bt * (linear::kStepBytes / es);
-        // per workgroup: its share of the unit's rate, and of about 60 GB/s of operands from L2
-        const double rate_us = step_flops * s.per_cu / ((fp8 ? s.tflops8 : s.tflops) * 1e6);
-        const double feed_us = (s.bf + s.bt) * linear::kStepBytes * s.per_cu / 60e3;
-        const double step_us = std::max(rate_us, feed_us);
-        for (int sp = 1; sp <= kMaxSplits && (sp == 1 || steps / sp >= 4); ++sp) {
-            const int64_t rounds = ceil_div(tiles * sp, static_cast<int64_t>(kCus) * s.per_cu);
-            double us = std::max(rounds * (static_cast<double>(ceil_div(steps, sp)) * step_us + 2.0), stream + 2.0);
-            if (sp > 1) us += 4.0 + (sp + 1) * static_cast<double>(n) * round_up(M, 8) * 4 / 4.0e6;
+        const Cost &c = fp8 ? s.e4m3 : s.bf16;
+        const int64_t tiles = ceil_div(M, s.bf) * ceil_div(n, s.bt), slots = static_cast<int64_t>(kCus) * s.per_cu;
+        for (int sp = 1; sp <= (rows ? 1 : kMaxSplits) && (sp == 1 || steps / sp >= 3); ++sp) {
+            const double depth = static_cast<double>(ceil_div(steps, sp));
+            const int64_t groups = tiles * sp, last = groups % slots;
+            double us = static_cast<double>(groups / slots) * (depth * c.step[s.per_cu - 1] + c.tile);
+            if (last) us += depth * c.step[ceil_div(last, kCus) - 1] + c.tile;
+            us = std::max(us, bytes / c.rate) + c.launch;
+            if (sp > 1) us += c.fold + 8.0 * sp * static_cast<double>(n) * round_up(M, 8) / c.fold_rate;
             if (us < best_us - 1e-9) {
                 best_us = us;
                 best = {i, sp};
@@ -93,6 +105,13 @@ hipError_t launch_shape(const linear::Args &g, bool fp8, hipStream_t st) {
         if (tail) hipLaunchKernelGGL((linear::linear_kernel<S, false, true>), grid, block, 0, st, g);
         else hipLaunchKernelGGL((linear::linear_kernel<S, false, false>), grid, block, 0, st, g);
     }
+    return hipGetLastError();
+}
+template <int TT>
+hipError_t launch_rows(const linear::Args &g, bool fp8, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.M, 16))), block(64 * linear::kRowsWaves);
+    if (fp8) hipLaunchKernelGGL((linear::linear_rows_kernel<true, TT>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((linear::linear_rows_kernel<false, TT>), grid, block, 0, st, g);
     return hipGetLastError();
 }
 
@@ -275,10 +294,12 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
     e.vec_pre = on16(a.preact) && a.ldp % 8 == 0;
     hipError_t err;
     switch (p.shape) {
-        case 0: err = launch_shape<Big>(g, a.fp8, st); break;
-        case 1: err = launch_shape<Mid>(g, a.fp8, st); break;
-        case 2: err = launch_shape<Low>(g, a.fp8, st); break;
-        default: err = launch_shape<Few>(g, a.fp8, st); break;
+        case BIG: err = launch_shape<Big>(g, a.fp8, st); break;
+        case WIDE: err = launch_shape<Wide>(g, a.fp8, st); break;
+        case LOW: err = launch_shape<Low>(g, a.fp8, st); break;
+        case TINY: err = launch_shape<Tiny>(g, a.fp8, st); break;
+        case ROWS16: err = launch_rows<1>(g, a.fp8, st); break;
+        default: err = launch_rows<2>(g, a.fp8, st); break;
     }
     if (err != hipSuccess || p.splits == 1) return err;
     const int64_t items = a.n * (g.ldpart / 8);

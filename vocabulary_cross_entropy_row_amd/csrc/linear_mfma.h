@@ -42,6 +42,7 @@ using dev::u32x4;
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef float f4v __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void *lds_ptr;
@@ -121,25 +122,21 @@ __device__ __forceinline__ float activate(int act, float z) {
         default: return z;
     }
 }
-// eight at a time: the choice once, not per value
-__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+// U x 8 values: the choice once, not per value
+template <int ACT, int U>
+__device__ __forceinline__ void activate_all(float (&v)[U][8]) {
+#pragma unroll
+    for (int p = 0; p < U; ++p)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[p][u] = activate(ACT, v[p][u]);
+}
+template <int U>
+__device__ __forceinline__ void activate_block(int act, float (&v)[U][8]) {
     switch (act) {
-        case ACT_RELU:
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = activate(ACT_RELU, v[u]);
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = activate(ACT_GELU, v[u]);
-            break;
-        case ACT_GELU_TANH:
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = activate(ACT_GELU_TANH, v[u]);
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = activate(ACT_SILU, v[u]);
-            break;
+        case ACT_RELU: activate_all<ACT_RELU>(v); break;
+        case ACT_GELU: activate_all<ACT_GELU>(v); break;
+        case ACT_GELU_TANH: activate_all<ACT_GELU_TANH>(v); break;
+        case ACT_SILU: activate_all<ACT_SILU>(v); break;
         default: break;
     }
 }
@@ -178,54 +175,92 @@ __device__ __forceinline__ Cols load_cols(const Epi &e, int64_t f) {
     }
     return c;
 }
-// The sums v of token t, features f .. f + 7, through the epilogue to memory
-__device__ __forceinline__ void finish8(const Epi &e, const Cols &c, int64_t t, int64_t f, float (&v)[8]) {
-    if (t >= e.n || f >= e.M) return;
-    const bool full = f + 8 <= e.M;
-    const float sx = e.scale_x ? e.scale_x[t] : 1.0f;
+// The sums v of tokens t0, t0 + dt, ... (U of them), features f .. f + 7, through the epilogue to
+// memory.  The residuals are requested before the sums are read (read()), so U tokens wait for memory
+// once.
+template <int U, class Read>
+__device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, int dt, int64_t f, Read read) {
+    const bool vec = e.vec_out && f + 8 <= e.M;
+    u32x4 ra[U], rb[U];   // the residual's 16 bytes (bf16) or 32 (fp32)
+    if (e.residual && vec) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = fmaf(v[u] * sx, c.sw[u], c.b[u]);
-    if (e.preact) {
-        const int64_t o = t * e.ldp + f;
-        if (e.vec_pre && full) {
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.preact) + o) = Elt<true>::pack(v);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (f + u < e.M) Elt<true>::store_one(e.preact, o + u, v[u]);
+        for (int p = 0; p < U; ++p) {
+            const int64_t t = t0 + p * dt;
+            ra[p] = rb[p] = (u32x4){0u, 0u, 0u, 0u};
+            if (t >= e.n) continue;
+            const char *r = static_cast<const char *>(e.residual) + (t * e.ldr + f) * (e.out_bf16 ? 2 : 4);
+            ra[p] = reinterpret_cast<const u32x4 *>(r)[0];
+            if (!e.out_bf16) rb[p] = reinterpret_cast<const u32x4 *>(r)[1];
         }
     }
-    activate8(e.act, v);
-    const int64_t o = t * e.ldo + f;
-    if (e.vec_out && full) {
-        if (e.out_bf16) {
-            if (e.residual) {
-                const u32x4 r = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(e.residual) + t * e.ldr + f);
+    float v[U][8];
+    read(v);
+    if (e.scale_w) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] += Elt<true>::get(r, u);
+        for (int p = 0; p < U; ++p)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[p][u] *= c.sw[u];
+    }
+    if (e.bias) {
+#pragma unroll
+        for (int p = 0; p < U; ++p)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[p][u] += c.b[u];
+    }
+    if (e.preact) {
+#pragma unroll
+        for (int p = 0; p < U; ++p) {
+            const int64_t t = t0 + p * dt, o = t * e.ldp + f;
+            if (t >= e.n) continue;
+            if (e.vec_pre && f + 8 <= e.M) {
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.preact) + o) = Elt<true>::pack(v[p]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (f + u < e.M) Elt<true>::store_one(e.preact, o + u, v[p][u]);
             }
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.out) + o) = Elt<true>::pack(v);
-        } else {
+        }
+    }
+    if (e.act != ACT_NONE) activate_block<U>(e.act, v);
+    if (vec && e.out_bf16) {
+#pragma unroll
+        for (int p = 0; p < U; ++p) {
+            const int64_t t = t0 + p * dt;
+            if (t >= e.n) continue;
             if (e.residual) {
-                const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(e.residual) + t * e.ldr + f);
-                const float4 a = r[0], b = r[1];
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[p][u] += Elt<true>::get(ra[p], u);
             }
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(e.out) + o);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.out) + t * e.ldo + f) = Elt<true>::pack(v[p]);
+        }
+    } else if (vec) {
+#pragma unroll
+        for (int p = 0; p < U; ++p) {
+            const int64_t t = t0 + p * dt;
+            if (t >= e.n) continue;
+            if (e.residual) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[p][u] += Elt<false>::get(u < 4 ? ra[p] : rb[p], u & 3);
+            }
+            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(e.out) + t * e.ldo + f);
+            q[0] = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+            q[1] = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
         }
     } else {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (f + u >= e.M) continue;
-            if (e.out_bf16) {
-                if (e.residual) v[u] += Elt<true>::load_one(e.residual, t * e.ldr + f + u);
-                Elt<true>::store_one(e.out, o + u, v[u]);
-            } else {
-                if (e.residual) v[u] += static_cast<const float *>(e.residual)[t * e.ldr + f + u];
-                static_cast<float *>(e.out)[o + u] = v[u];
+        for (int p = 0; p < U; ++p) {
+            const int64_t t = t0 + p * dt, o = t * e.ldo + f;
+            if (t >= e.n) continue;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (f + u >= e.M) continue;
+                if (e.out_bf16) {
+                    if (e.residual) v[p][u] += Elt<true>::load_one(e.residual, t * e.ldr + f + u);
+                    Elt<true>::store_one(e.out, o + u, v[p][u]);
+                } else {
+                    if (e.residual) v[p][u] += static_cast<const float *>(e.residual)[t * e.ldr + f + u];
+                    static_cast<float *>(e.out)[o + u] = v[p][u];
+                }
             }
         }
     }
@@ -450,35 +485,64 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();   // every wave is done with the operand tiles
     constexpr int LPT = FI * 4, TPP = 64 / LPT;   // lanes per token, tokens per pass
+    constexpr int PASSES = 32 / TPP, U = PASSES < 4 ? PASSES : 4;
     float *reg = reinterpret_cast<float *>(lds) + wave * 32 * S::OUT_LD;
     const int lf = (lane % LPT) * 8;
     const int64_t f = f0 + wf * FI * 32 + lf;
     const bool split = g.splits > 1;
     Cols cols;
     if (!split) cols = load_cols(g.e, f);
+    // a lane's accumulators belong to one token per j: its scale goes in here
+    float sx[TJ];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+        const int64_t t = t0 + (wt * TJ + j) * 32 + (lane & 31);
+        sx[j] = FP8 && g.e.scale_x && t < g.n ? g.e.scale_x[t] : 1.0f;
+    }
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
 #pragma unroll
         for (int i = 0; i < FI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                *reinterpret_cast<float4 *>(reg + (lane & 31) * S::OUT_LD + i * 32 + (r >> 2) * 8 + half * 4) =
-                    make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+            for (int r = 0; r < 16; r += 4) {
+                float4 q = make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+                if constexpr (FP8) {
+                    q.x *= sx[j];
+                    q.y *= sx[j];
+                    q.z *= sx[j];
+                    q.w *= sx[j];
+                }
+                *reinterpret_cast<float4 *>(reg + (lane & 31) * S::OUT_LD + i * 32 + (r >> 2) * 8 + half * 4) = q;
+            }
         __builtin_amdgcn_wave_barrier();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1   // the accumulators are in LDS: one copy of the epilogue per j
-        for (int p = 0; p < 32 / TPP; ++p) {
-            const int tl = p * TPP + lane / LPT;
-            const float4 u = *reinterpret_cast<const float4 *>(reg + tl * S::OUT_LD + lf);
-            const float4 v = *reinterpret_cast<const float4 *>(reg + tl * S::OUT_LD + lf + 4);
+        for (int p0 = 0; p0 < PASSES; p0 += U) {
+            const int tl = p0 * TPP + lane / LPT;
             const int64_t t = t0 + (wt * TJ + j) * 32 + tl;
-            float q[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            auto read = [&](float (&v)[U][8]) {
+#pragma unroll
+                for (int p = 0; p < U; ++p) {
+                    const float4 x = *reinterpret_cast<const float4 *>(reg + (tl + p * TPP) * S::OUT_LD + lf);
+                    const float4 y = *reinterpret_cast<const float4 *>(reg + (tl + p * TPP) * S::OUT_LD + lf + 4);
+                    v[p][0] = x.x; v[p][1] = x.y; v[p][2] = x.z; v[p][3] = x.w;
+                    v[p][4] = y.x; v[p][5] = y.y; v[p][6] = y.z; v[p][7] = y.w;
+                }
+            };
+            if (f >= g.M) continue;
             if (!split) {
-                finish8(g.e, cols, t, f, q);
-            } else if (t < g.n && f < g.M) {   // ldpart is M in whole eights
-                float4 *o = reinterpret_cast<float4 *>(g.part + (static_cast<int64_t>(ks) * g.n + t) * g.ldpart + f);
-                o[0] = u;
-                o[1] = v;
+                finish<U>(g.e, cols, t, TPP, f, read);
+            } else {   // ldpart is M in whole eights
+                float v[U][8];
+                read(v);
+#pragma unroll
+                for (int p = 0; p < U; ++p) {
+                    if (t + p * TPP >= g.n) continue;
+                    float4 *o = reinterpret_cast<float4 *>(
+                        g.part + (static_cast<int64_t>(ks) * g.n + t + p * TPP) * g.ldpart + f);
+                    o[0] = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+                    o[1] = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
+                }
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -499,9 +563,110 @@ __global__ __launch_bounds__(256) inline void linear_fold_kernel(const float *pa
             u.x += a.x; u.y += a.y; u.z += a.z; u.w += a.w;
             v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
         }
-        float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
         const Cols c = load_cols(e, f);
-        finish8(e, c, t, f, s);
+        finish<1>(e, c, t, 0, f, [&](float (&s)[1][8]) {
+            s[0][0] = u.x; s[0][1] = u.y; s[0][2] = u.z; s[0][3] = u.w;
+            s[0][4] = v.x; s[0][5] = v.y; s[0][6] = v.z; s[0][7] = v.w;
+        });
+    }
+}
+
+// ---- few tokens ------------------------------------------------------------------------
+//
+// Up to 32 tokens: the weight is read once and little else happens, so the time is how soon and how
+// widely its reads go out.  A workgroup takes 16 features and its eight waves an eighth of K each, so
+// a 4096 x 4096 weight already keeps 2048 waves reading without splitting K over workgroups (whose
+// partial sums and second launch cost 3 us of 11: 4 x 4640 x 1880 e4m3 takes 6.7 us here, 12.2 split).  Operands go straight from memory to the MFMA's
+// registers: lane l supplies row l % 16 of w (token l % 16 of x) and the 16-byte chunk l / 16 of every
+// 64 bytes of K, eight (or with two token tiles four) such loads ahead of those in use.  The waves'
+// sums meet in LDS, are added in wave order and go through the epilogue one value per lane.
+constexpr int kRowsWaves = 8;
+
+template <bool FP8>
+__device__ __forceinline__ void mfma16(f4v &acc, const u32x4 &a, const u32x4 &b) {
+    if constexpr (FP8) {   // 16 bytes are two 8-byte operands
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(
+            static_cast<long>((static_cast<uint64_t>(a.y) << 32) | a.x),
+            static_cast<long>((static_cast<uint64_t>(b.y) << 32) | b.x), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(
+            static_cast<long>((static_cast<uint64_t>(a.w) << 32) | a.z),
+            static_cast<long>((static_cast<uint64_t>(b.w) << 32) | b.z), acc, 0, 0, 0);
+    } else {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), acc, 0, 0, 0);
+    }
+}
+
+template <bool FP8, int TT>   // token tiles of 16
+__global__ __launch_bounds__(64 * kRowsWaves, 2) void linear_rows_kernel(Args g) {
+    constexpr int U = TT == 1 ? 8 : 4;   // loads of w at once
+    __shared__ __attribute__((aligned(16))) float sums[kRowsWaves][TT * 256];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int f0 = blockIdx.x * 16;
+    const int rows = min(16, g.M - f0);
+    const __amdgpu_buffer_rsrc_t rsW = uniform_rsrc(
+        g.w + static_cast<int64_t>(f0) * g.ldw, static_cast<uint32_t>((rows - 1) * g.ldw + g.kbytes));
+    const __amdgpu_buffer_rsrc_t rsX = uniform_rsrc(g.x, static_cast<uint32_t>((g.n - 1) * g.ldx + g.kbytes));
+    const int chunk = (lane >> 4) * 16;   // byte of the lane's chunk in every 64
+    const uint32_t vw = static_cast<uint32_t>(lane & 15) * static_cast<uint32_t>(g.ldw) + chunk;
+    uint32_t vx[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        vx[t] = static_cast<uint32_t>(t * 16 + (lane & 15)) * static_cast<uint32_t>(g.ldx) + chunk;
+    const int total = (g.kbytes + 63) / 64;
+    const int beg = static_cast<int>(static_cast<int64_t>(total) * wave / kRowsWaves);
+    const int end = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / kRowsWaves);
+    auto fetch = [&](int s, u32x4 (&w)[U], u32x4 (&x)[TT][U]) {   // zeros past this wave's share and past K
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = s + u < end && (s + u) * 64 + chunk < g.kbytes;
+            const uint32_t k = static_cast<uint32_t>(s + u) * 64u;
+            w[u] = __builtin_amdgcn_raw_buffer_load_b128(rsW, in ? vw + k : kOutside, 0, 0);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[t][u] = __builtin_amdgcn_raw_buffer_load_b128(rsX, in ? vx[t] + k : kOutside, 0, 0);
+        }
+    };
+    f4v acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 w0[U], w1[U], x0[TT][U], x1[TT][U];
+    auto use = [&](u32x4 (&w)[U], u32x4 (&x)[TT][U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) mfma16<FP8>(acc[t], w[u], x[t][u]);
+    };
+    fetch(beg, w0, x0);
+    for (int s = beg; s < end; s += 2 * U) {
+        fetch(s + U, w1, x1);
+        use(w0, x0);
+        fetch(s + 2 * U, w0, x0);
+        use(w1, x1);
+    }
+    // result register r of lane l: feature (l / 16) 4 + r, token l % 16
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        *reinterpret_cast<f4v *>(&sums[wave][t * 256 + (lane & 15) * 16 + (lane >> 4) * 4]) = acc[t];
+    __syncthreads();
+    const Epi &e = g.e;
+    const int i = threadIdx.x;
+    if (i >= TT * 256) return;
+    const int64_t t = i >> 4, f = f0 + (i & 15);
+    if (t >= e.n || f >= e.M) return;
+    float v = sums[0][i];
+#pragma unroll
+    for (int k = 1; k < kRowsWaves; ++k) v += sums[k][i];
+    if (FP8 && e.scale_x) v *= e.scale_x[t];
+    if (FP8 && e.scale_w) v *= e.scale_w[f];
+    if (e.bias) v += e.bias_bf16 ? Elt<true>::load_one(e.bias, f) : static_cast<const float *>(e.bias)[f];
+    if (e.preact) Elt<true>::store_one(e.preact, t * e.ldp + f, v);
+    v = activate(e.act, v);
+    if (e.out_bf16) {
+        if (e.residual) v += Elt<true>::load_one(e.residual, t * e.ldr + f);
+        Elt<true>::store_one(e.out, t * e.ldo + f, v);
+    } else {
+        if (e.residual) v += static_cast<const float *>(e.residual)[t * e.ldr + f];
+        static_cast<float *>(e.out)[t * e.ldo + f] = v;
     }
 }
 
