@@ -355,9 +355,8 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
  * Row operations next to those above: what forms `hidden` (or the 8-bit operand
  * of lce_linear) and what a serving step does to logits before lce_ce_argmax or
  * lce_ce_stats reads them.  Matrices are row-major with a row stride in elements;
- * columns past the width are neither read nor written.  Any alignment of the
- * element's size works; rows that start on 16 bytes, with strides of whole 16
- * bytes, are read and written 16 bytes at a time.  An output may be the same
+ * columns past the width are neither read nor written, and any alignment of the
+ * element's size works unless a call says otherwise.  An output may be the same
  * buffer as an input of its type, at the same place and stride; other overlap is
  * not allowed.  n == 0 is valid.
  */
@@ -472,9 +471,8 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
  *                 may be NULL where that is 0.  Clobbered; calls that share it must
  *                 not run at the same time.
  * n and M are any size; K, ldx and ldw must be whole 16 bytes and x and weight
- * 16-byte aligned (LCE_ERR_UNSUPPORTED otherwise).  Outputs whose rows start on 16
- * bytes are written 16 bytes at a time, others value by value.  The same inputs
- * give the same bits.  n == 0 is valid.
+ * 16-byte aligned (LCE_ERR_UNSUPPORTED otherwise); the other operands may lie
+ * anywhere their type may.  The same inputs give the same bits.  n == 0 is valid.
  */
 lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ldw, lce_dtype in_dtype,
                       const float *scale_x, const float *scale_w, const void *bias, lce_dtype bias_dtype,

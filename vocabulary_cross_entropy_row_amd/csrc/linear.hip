@@ -289,9 +289,6 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
     e.ldp = a.ldp;
     e.n = a.n;
     e.M = a.M;
-    const int unit = a.out_bf16 ? 8 : 4;
-    e.vec_out = on16(a.out) && a.ldo % unit == 0 && (!a.residual || (on16(a.residual) && a.ldr % unit == 0));
-    e.vec_pre = on16(a.preact) && a.ldp % 8 == 0;
     hipError_t err;
     switch (p.shape) {
         case BIG: err = launch_shape<Big>(g, a.fp8, st); break;

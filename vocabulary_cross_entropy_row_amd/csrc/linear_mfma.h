@@ -43,6 +43,10 @@ using dev::u32x4;
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef float f4v __attribute__((ext_vector_type(4)));
+// 16 bytes at any address: gfx950 loads and stores them in one instruction, so rows of odd length cost
+// no more than aligned ones (one value per store took 35 us where this takes 26, 77 x 1000 x 50257 with
+// fp32 outputs)
+typedef uint32_t any16 __attribute__((ext_vector_type(4), aligned(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void *lds_ptr;
@@ -63,8 +67,6 @@ struct Epi {
     void *preact;
     int64_t ldp;
     int64_t n, M;
-    // 16 bytes at a time: out and residual, pre-activation
-    bool vec_out, vec_pre;
 };
 
 struct Args {
@@ -122,16 +124,16 @@ __device__ __forceinline__ float activate(int act, float z) {
         default: return z;
     }
 }
-// U x 8 values: the choice once, not per value
-template <int ACT, int U>
-__device__ __forceinline__ void activate_all(float (&v)[U][8]) {
+// U x W values: the choice once, not per value
+template <int ACT, int U, int W>
+__device__ __forceinline__ void activate_all(float (&v)[U][W]) {
 #pragma unroll
     for (int p = 0; p < U; ++p)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[p][u] = activate(ACT, v[p][u]);
+        for (int u = 0; u < W; ++u) v[p][u] = activate(ACT, v[p][u]);
 }
-template <int U>
-__device__ __forceinline__ void activate_block(int act, float (&v)[U][8]) {
+template <int U, int W>
+__device__ __forceinline__ void activate_block(int act, float (&v)[U][W]) {
     switch (act) {
         case ACT_RELU: activate_all<ACT_RELU>(v); break;
         case ACT_GELU: activate_all<ACT_GELU>(v); break;
@@ -180,7 +182,7 @@ __device__ __forceinline__ Cols load_cols(const Epi &e, int64_t f) {
 // once.
 template <int U, class Read>
 __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, int dt, int64_t f, Read read) {
-    const bool vec = e.vec_out && f + 8 <= e.M;
+    const bool vec = f + 8 <= e.M;
     u32x4 ra[U], rb[U];   // the residual's 16 bytes (bf16) or 32 (fp32)
     if (e.residual && vec) {
 #pragma unroll
@@ -189,8 +191,8 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
             ra[p] = rb[p] = (u32x4){0u, 0u, 0u, 0u};
             if (t >= e.n) continue;
             const char *r = static_cast<const char *>(e.residual) + (t * e.ldr + f) * (e.out_bf16 ? 2 : 4);
-            ra[p] = reinterpret_cast<const u32x4 *>(r)[0];
-            if (!e.out_bf16) rb[p] = reinterpret_cast<const u32x4 *>(r)[1];
+            ra[p] = reinterpret_cast<const any16 *>(r)[0];
+            if (!e.out_bf16) rb[p] = reinterpret_cast<const any16 *>(r)[1];
         }
     }
     float v[U][8];
@@ -212,8 +214,8 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
         for (int p = 0; p < U; ++p) {
             const int64_t t = t0 + p * dt, o = t * e.ldp + f;
             if (t >= e.n) continue;
-            if (e.vec_pre && f + 8 <= e.M) {
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.preact) + o) = Elt<true>::pack(v[p]);
+            if (vec) {
+                *reinterpret_cast<any16 *>(static_cast<uint16_t *>(e.preact) + o) = Elt<true>::pack(v[p]);
             } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -221,7 +223,7 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
             }
         }
     }
-    if (e.act != ACT_NONE) activate_block<U>(e.act, v);
+    if (e.act != ACT_NONE) activate_block(e.act, v);
     if (vec && e.out_bf16) {
 #pragma unroll
         for (int p = 0; p < U; ++p) {
@@ -231,7 +233,7 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v[p][u] += Elt<true>::get(ra[p], u);
             }
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(e.out) + t * e.ldo + f) = Elt<true>::pack(v[p]);
+            *reinterpret_cast<any16 *>(static_cast<uint16_t *>(e.out) + t * e.ldo + f) = Elt<true>::pack(v[p]);
         }
     } else if (vec) {
 #pragma unroll
@@ -242,9 +244,9 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v[p][u] += Elt<false>::get(u < 4 ? ra[p] : rb[p], u & 3);
             }
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(e.out) + t * e.ldo + f);
-            q[0] = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
-            q[1] = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
+            any16 *q = reinterpret_cast<any16 *>(static_cast<float *>(e.out) + t * e.ldo + f);
+            q[0] = __builtin_bit_cast(u32x4, make_float4(v[p][0], v[p][1], v[p][2], v[p][3]));
+            q[1] = __builtin_bit_cast(u32x4, make_float4(v[p][4], v[p][5], v[p][6], v[p][7]));
         }
     } else {
 #pragma unroll

@@ -37,6 +37,10 @@ namespace {
 using dev::Elt;
 using dev::u32x4;
 
+// 16 bytes at any address (gfx950 stores them in one instruction): the output's rows need not start
+// where the logits' do
+typedef uint32_t any16 __attribute__((ext_vector_type(4), aligned(2)));
+
 constexpr int kThreads = 512;
 constexpr uint32_t kPrompt = 0x80000000u;
 constexpr int kAhead = 4;   // history ids per thread requested at once
@@ -93,7 +97,6 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
     char *orow = static_cast<char *>(a.out) + row * a.ldo * BYTES;
     // the row is taken in 16-byte windows of the address space: `lead` elements of the first lie before it
     const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(xrow) & 15) / BYTES);
-    const bool vec_out = (reinterpret_cast<uintptr_t>(orow) & 15) / BYTES == static_cast<uintptr_t>(lead);
     const int V = static_cast<int>(a.V);
     const int base = static_cast<int>(slice * COLS) - lead;   // column of the slice's first element
     if (base >= V) return;
@@ -261,8 +264,8 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = (bits & (1u << e)) ? o[e] : a.mask_value;
         }
-        if (vec_out && c >= 0 && c + E <= V) {
-            *reinterpret_cast<u32x4 *>(orow + static_cast<int64_t>(c) * BYTES) = Elt<BF16>::pack(o);
+        if (c >= 0 && c + E <= V) {
+            *reinterpret_cast<any16 *>(orow + static_cast<int64_t>(c) * BYTES) = Elt<BF16>::pack(o);
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
