@@ -205,6 +205,26 @@ def test_autograd_matches_the_formula_and_differences(residual):
         assert float((got[i].double() * v).sum()) == pytest.approx(slope, rel=1e-4, abs=1e-4)
 
 
+def test_autograd_of_strided_and_single_rows_on_another_stream():
+    base = torch.randn(40, 3, 80, device=DEV)
+    w = torch.randn(64, device=DEV, requires_grad=True)
+    g = torch.randn(3, 40, 64, device=DEV)
+    for view in (lambda t: t[:, :, 8:72].transpose(0, 1), lambda t: t[:1, :1, :64].expand(3, 40, 64),
+                 lambda t: t[:1, 1:2, 3:67].transpose(0, 2).reshape(1, 64), lambda t: t[7:8, 0, ::1][:, :64]):
+        x = view(base).detach().requires_grad_()
+        cot = g if x.dim() == 3 else g[0, :1]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y = lce.rms_norm(x, w)
+            gx, gw = torch.autograd.grad(y, (x, w), cot)
+        torch.cuda.synchronize()
+        d, dw = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
+        want = torch.autograd.grad(d / (d.square().mean(-1, keepdim=True) + 1e-6).sqrt() * dw, (d, dw), cot.double())
+        for a, b in zip((gx, gw), want):
+            _within(a, b, 1e-5 * (b.abs() + 1), "grad")
+
+
 def test_autograd_with_only_one_output_used():
     x = torch.randn(4, 64, device=DEV, requires_grad=True)
     res = torch.randn(4, 64, device=DEV, requires_grad=True)

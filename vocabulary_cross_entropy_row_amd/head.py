@@ -146,6 +146,19 @@ def lce_rms_norm_workspace_bytes(n: int, H: int) -> int:
     return int(lib().lce_rms_norm_workspace_bytes(int(n), int(H)))
 
 
+def _norm_backward(gy, ldg, s, lds, code, weight, wcode, offset, rstd, gs, ldgs, gx, ldgx, gw, gwcode, workspace, stream):
+    """The call, its operands checked: allocates the workspace that a weight's gradient needs."""
+    n, H = s.shape
+    bytes_ = 0
+    if gw is not None:
+        bytes_ = lce_rms_norm_workspace_bytes(n, H)
+        if workspace is None:   # clobbered by the call
+            workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=s.device)
+    _check(lib().lce_rms_norm_backward(gy.data_ptr(), ldg, s.data_ptr(), lds, code, _ptr(weight), wcode, offset,
+                                       rstd.data_ptr(), _ptr(gs), ldgs, n, H, gx.data_ptr(), ldgx, _ptr(gw), gwcode,
+                                       _ptr(workspace), bytes_, stream))
+
+
 @_call_stream
 def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offset: float = 0.0, grad_x=None,
                           grad_weight=None, want_grad_weight: bool = True, workspace=None, stream=None):
@@ -165,21 +178,18 @@ def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offs
     if grad_x is None:
         grad_x = torch.empty((n, H), dtype=s.dtype, device=dev)
     ldgx = _rows(grad_x, "grad_x", s.dtype, n, H, dev)
-    gwcode, bytes_ = LCE_F32, 0
+    gwcode = LCE_F32
     if weight is None or not want_grad_weight:
-        grad_weight = workspace = None
+        grad_weight = None
     else:
         if grad_weight is None:
             grad_weight = torch.empty(H, dtype=weight.dtype, device=dev)
         gwcode = _float_code(grad_weight, "grad_weight")
         _buf(grad_weight, "grad_weight", grad_weight.dtype, H, dev)
-        bytes_ = lce_rms_norm_workspace_bytes(n, H)
-        if workspace is None:   # clobbered by the call
-            workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=dev)
-        _buf(workspace, "workspace", torch.uint8, bytes_, dev)
-    _check(lib().lce_rms_norm_backward(grad_y.data_ptr(), ldg, s.data_ptr(), lds, code, _ptr(weight), wcode,
-                                       float(weight_offset), _ptr(rstd), _ptr(grad_sum), ldgs, n, H, grad_x.data_ptr(),
-                                       ldgx, _ptr(grad_weight), gwcode, _ptr(workspace), bytes_, stream))
+        if workspace is not None:
+            _buf(workspace, "workspace", torch.uint8, lce_rms_norm_workspace_bytes(n, H), dev)
+    _norm_backward(grad_y, ldg, s, lds, code, weight, wcode, float(weight_offset), rstd, grad_sum, ldgs, grad_x, ldgx,
+                   grad_weight, gwcode, workspace, stream)
     return grad_x, grad_weight
 
 
@@ -191,6 +201,10 @@ def _rows_of(t, H: int):
     if (H > 1 and column != 1) or (t.shape[0] > 1 and row < H):
         t = t.contiguous()
     return t
+
+
+def _ld(rows) -> int:
+    return rows.stride(0) if rows.shape[0] > 1 else rows.shape[1]
 
 
 class _RmsNorm(torch.autograd.Function):
@@ -225,11 +239,17 @@ class _RmsNorm(torch.autograd.Function):
         need_x, need_w, need_r = ctx.needs_input_grad[:3]
         if gy is None:   # nothing came through the norm
             return (gs if need_x else None), None, (gs if need_r else None), None, None
+        # Autograd hands gradients of the outputs' shape, type and device, on the stream the forward ran
+        # on and with its device current; the saved tensors were checked there.  This runs on autograd's
+        # thread, where every interpreted line costs twice what it does on the caller's.
         H = s.shape[-1]
         gx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-        _, gw = lce_rms_norm_backward(_rows_of(gy, H), _rows_of(s, H), weight, rstd,
-                                      grad_sum=None if gs is None else _rows_of(gs, H), weight_offset=ctx.offset,
-                                      grad_x=_rows_of(gx, H), want_grad_weight=need_w)
+        s2, g2, gs2, gx2 = _rows_of(s, H), _rows_of(gy, H), None if gs is None else _rows_of(gs, H), _rows_of(gx, H)
+        gw = None if weight is None or not need_w else torch.empty(H, dtype=weight.dtype, device=s.device)
+        code = _CODES[s.dtype]
+        wcode = code if weight is None else _CODES[weight.dtype]
+        _norm_backward(g2, _ld(g2), s2, _ld(s2), code, weight, wcode, ctx.offset, rstd, gs2, H if gs2 is None else _ld(gs2),
+                       gx2, H, gw, wcode, None, _current_stream(s.device.index))
         return (gx if need_x else None), gw, (gx if need_r else None), None, None
 
 
