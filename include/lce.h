@@ -485,8 +485,8 @@ lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ld
 size_t lce_linear_workspace_bytes(int64_t n, int64_t K, int64_t M, lce_dtype in_dtype);
 
 /*
- * Backward of lce_linear for BF16 operands.  With dz = grad_out act'(preact) (rounded
- * to BF16, as the products take it):
+ * Backward of lce_linear for BF16 operands.  With dz = grad_out act'(preact), rounded
+ * to BF16 where the products take it and not in the bias's sums:
  *   grad_x = dz weight,  grad_weight = dz^T x,  grad_bias = column sums of dz
  * and the residual's gradient is grad_out itself.
  *   grad_out      device [n, ldg] BF16 or F32 (grad_dtype).

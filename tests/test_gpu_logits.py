@@ -194,6 +194,12 @@ def test_infinities_nans_and_masks_that_leave_nothing(dtype):
     assert bool(torch.isnan(out[0, 5])) and bool((out[2] == -30).all())
 
 
+def test_a_vanishing_temperature_keeps_zeros():
+    x = torch.tensor([[0.0, 1.0, -1.0, 1e-30]], device=DEV)
+    out = lce.lce_logits_process(x, temperature=torch.tensor([1e-39], device=DEV), out=torch.empty_like(x))
+    assert float(out[0, 0]) == 0 and float(out[0, 1]) > 1e38 and float(out[0, 2]) < -1e38 and float(out[0, 3]) > 0
+
+
 def test_no_rule_leaves_the_bits():
     for dtype in (BF16, F32):
         x = torch.randn(3, 999, device=DEV).to(dtype)

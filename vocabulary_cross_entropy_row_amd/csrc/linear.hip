@@ -68,7 +68,7 @@ struct Plan {
 // compute units, the last one as full as it is, and not less than the bytes take.
 Plan plan_of(int64_t n, int64_t K, int64_t M, bool fp8) {
     const int es = fp8 ? 1 : 2;
-    const int64_t steps = std::max<int64_t>(1, ceil_div(K * es, linear::kStepBytes));
+    const int64_t steps = std::max<int64_t>(1, ceil_div(K * es, 128));
     const double bytes = static_cast<double>(n + M) * K * es + 2.0 * n * M;
     Plan best{BIG, 1};
     double best_us = 1e30;
@@ -97,7 +97,7 @@ Plan plan_of(int64_t n, int64_t K, int64_t M, bool fp8) {
 template <class S>
 hipError_t launch_shape(const linear::Args &g, bool fp8, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(g.per_xcd) * 8u), block(64 * S::NW);
-    const bool tail = g.kbytes % linear::kStepBytes != 0;
+    const bool tail = g.kbytes % S::STEP != 0;
     if (fp8) {
         if (tail) hipLaunchKernelGGL((linear::linear_kernel<S, true, true>), grid, block, 0, st, g);
         else hipLaunchKernelGGL((linear::linear_kernel<S, true, false>), grid, block, 0, st, g);
@@ -120,7 +120,7 @@ hipError_t launch_rows(const linear::Args &g, bool fp8, hipStream_t st) {
 constexpr int kTrRows = 128, kTrCols = 64;
 
 // v = in, or in act'(pre); out[r][c] = bf16(v) when out is given; out_t[c][r] = bf16(v), rows
-// [rows, rows_pad) as zeros; part[blockIdx.y][c] = sum over the block's rows of bf16(v).  A tile of
+// [rows, rows_pad) as zeros; part[blockIdx.y][c] = sum over the block's rows of v, not rounded.  A tile of
 // 128 x 64 goes through LDS, 16-byte chunk c of row r at c ^ (r / 8 mod 8): the writes of a wave cover
 // 1 KB without conflicts and the eight rows of an output chunk are read from different banks.
 struct TransposeArgs {
@@ -140,6 +140,8 @@ template <bool BF16_IN>
 __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
     constexpr int PER = kTrRows * (kTrCols / 8) / 256;   // 16-byte chunks per thread
     __shared__ __align__(16) uint16_t tile[kTrRows * kTrCols];
+    __shared__ float sums[32][kTrCols];   // per row of threads
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     const int r0 = blockIdx.y * kTrRows, c0 = blockIdx.x * kTrCols;
     const int t = threadIdx.x;
     const bool vin = (a.ld_in * (BF16_IN ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.in) % 16 == 0;
@@ -180,6 +182,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = gr < a.rows && gc + e < a.cols ? v[e] * linear::slope(a.act, z[e]) : 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];   // a thread's chunks are of the same eight columns
         const u32x4 q = Elt<true>::pack(v);
         if (a.out) {   // ld_out and out are 16-byte whole
             if (full) {
@@ -191,6 +195,10 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
             }
         }
         *reinterpret_cast<u32x4 *>(tile + r * kTrCols + ((ch ^ (r >> 3)) & 7) * 8) = q;
+    }
+    if (a.part) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[t >> 3][(t & 7) * 8 + e] = sum[e];
     }
     __syncthreads();
     if (a.out_t) {
@@ -209,10 +217,9 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
         }
     }
     if (a.part && t < kTrCols && c0 + t < a.cols) {
-        float s = 0.0f;
-        for (int r = 0; r < kTrRows; ++r)   // rows past the last are zeros
-            s += Elt<true>::load_one(tile, r * kTrCols + (((t >> 3) ^ (r >> 3)) & 7) * 8 + (t & 7));
-        a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + t] = s;
+        float v = sums[0][t];
+        for (int r = 1; r < 32; ++r) v += sums[r][t];
+        a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + t] = v;
     }
 }
 

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
         const int64_t r = a.mask_rows ? a.mask_rows[row] : row;
         if (r >= 0 && r < a.R) words = a.allowed + r * a.ldm;
     }
-    const float inv_temp = temp > 0.0f ? 1.0f / temp : 1.0f;
+    const float inv_temp = temp > 0.0f ? fminf(1.0f / temp, FLT_MAX) : 1.0f;   // finite, so that 0 stays 0
     // mask bits of columns c .. c + E - 1: they lie in one word or two (those before the row or past V do
     // not matter)
     uint32_t lo[VECS], hi[VECS];

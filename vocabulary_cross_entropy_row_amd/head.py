@@ -26,7 +26,7 @@ def _call_stream(fn):
     device -- switches nothing."""
     @functools.wraps(fn)
     def wrapper(first, *args, stream=None, **kw):
-        if not (torch.is_tensor(first) and first.is_cuda):
+        if not (isinstance(first, torch.Tensor) and first.is_cuda):
             return fn(first, *args, stream=0, **kw)   # the function's own checks raise
         device = first.device
         if stream is None and device.index == torch.cuda.current_device():
@@ -50,7 +50,7 @@ def _rows(t, name: str, dtype, n: int, width: int, device, required: bool = Fals
         if required:
             raise ValueError(f"{name} is required")
         return width
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
@@ -70,7 +70,7 @@ def _buf(t, name: str, dtype, numel: int, device, required: bool = False) -> Non
         if required:
             raise ValueError(f"{name} is required")
         return
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
@@ -402,7 +402,10 @@ class _Linear(torch.autograd.Function):
         shape = (*x.shape[:-1], M)
         if residual is not None and residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
-        keep = _activation(activation) != 0 and any(ctx.needs_input_grad[:3])
+        wanted = any(ctx.needs_input_grad[:3])
+        if wanted and M % 8:
+            raise ValueError(f"gradients need a weight whose rows are a multiple of 8 (got {M})")
+        keep = wanted and _activation(activation) != 0
         out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
         preact = lce_linear(_rows_of(x, x.shape[-1]), weight, bias=bias, activation=activation,
                             residual=None if residual is None else _rows_of(residual, M), want_preact=keep,
