@@ -239,6 +239,16 @@ def test_autograd_with_only_one_output_used():
     _within(gw, b.double(), 1e-5 * (b.double().abs() + 1), "grad_weight")
 
 
+def test_gradients_of_gradients_are_refused():
+    x = torch.randn(4, 64, device=DEV, requires_grad=True)
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    (gx,) = torch.autograd.grad(lce.rms_norm(x, w).square().sum(), (x,), create_graph=True)
+    (ref,) = torch.autograd.grad(lce.rms_norm(x, w).square().sum(), (x,))
+    assert torch.equal(gx, ref)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        gx.sum().backward()
+
+
 def test_repeats_bit_for_bit_and_on_other_streams():
     x, res, w, gy, gs = _inputs(3000, 768, BF16, 9, wdtype=BF16)
     torch.cuda.synchronize()

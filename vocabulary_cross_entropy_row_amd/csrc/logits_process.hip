@@ -54,26 +54,32 @@ enum BiasMode { NO_BIAS = 0, PACKED = 1, OWN_WORD = 2 };
 constexpr int64_t kPackedL = 1 << 15, kPackedB = (1 << 16) - 1;
 
 // 16-byte vectors of logits per thread: 8192 columns per workgroup, half with words for the biases
-// (four workgroups of eight waves per CU either way).
+// (four workgroups per CU either way).
 template <bool BF16, int BIAS>
-constexpr int vecs_of() { return (BF16 ? 2 : 4) / (BIAS == OWN_WORD ? 2 : 1); }
+constexpr int vecs_of() { return 8192 / (kThreads * Elt<BF16>::E) / (BIAS == OWN_WORD ? 2 : 1); }
 
-// T tanh(u), u = x / T.  Near zero an odd polynomial, else (1 - t) / (1 + t) with t = e^{-2 |u|} <= 1,
-// whose difference loses 2^-24 / |u| of itself there.  fp32 logits need all of fp32: five terms up to
-// 1/4 (the next is below 2^-28 of u); bf16 ones are rounded 2^15 times coarser: two terms up to 1/64
-// (2^-27), the quotient exact to 2^-18 beyond, and five instructions fewer in a sweep that issues
-// about as long as it waits for memory.
+// scale T tanh(x / T).  Near zero an odd polynomial, else (1 - t) / (1 + t) with t = e^{-2 |x| / T} <= 1,
+// whose difference loses 2^-24 T / |x| of itself there.  fp32 logits need all of fp32: five terms up to
+// |x| = T / 4 (the next is below 2^-28 of x); bf16 ones are rounded 2^15 times coarser: two terms up to
+// T / 64 (2^-27), the quotient exact to 2^-18 beyond.  The sweep over the columns issues about as long
+// as it waits for memory, so the scale (1 / temperature) rides in the constants.
+struct Softcap {
+    float c, T, k1, k3, near, u;   // c = -2 log2 e / T
+    __device__ __forceinline__ Softcap(float cap, float scale, bool bf16)
+        : c(-2.0f * dev::kLog2e / cap), T(cap * scale), k1(scale), k3(scale * (-1.0f / 3.0f) / (cap * cap)),
+          near(cap * (bf16 ? 0.015625f : 0.25f)), u(1.0f / cap) {}
+};
 template <bool BF16>
-__device__ __forceinline__ float softcapped(float x, float T, float inv_t) {
-    const float u = x * inv_t, u2 = u * u;
-    const float t = dev::exp2_fast(fabsf(u) * (-2.0f * dev::kLog2e));
-    const float big = copysignf((1.0f - t) * dev::rcp_fast(1.0f + t), u) * T;
+__device__ __forceinline__ float softcapped(float x, const Softcap &s) {
+    const float t = dev::exp2_fast(fabsf(x) * s.c);
+    const float big = copysignf(fmaf(-s.T, t, s.T) * dev::rcp_fast(1.0f + t), x);
     if constexpr (BF16) {
-        return fabsf(u) < 0.015625f ? fmaf(x * u2, -1.0f / 3.0f, x) : big;
+        return fabsf(x) < s.near ? x * fmaf(x * x, s.k3, s.k1) : big;
     } else {
+        const float v = x * s.u, u2 = v * v;
         const float p =
             fmaf(u2, fmaf(u2, fmaf(u2, fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-        return fabsf(u) < 0.25f ? x * p : big;
+        return fabsf(x) < s.near ? x * (p * s.k1) : big;
     }
 }
 
@@ -130,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
         }
     }
     const float temp = a.temperature ? a.temperature[row] : 0.0f;
-    const float cap = a.softcap, inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
+    const float cap = a.softcap;
     const float rep = a.repetition ? a.repetition[row] : 1.0f;
     const float pres = a.presence ? a.presence[row] : 0.0f;
     const float freq = a.frequency ? a.frequency[row] : 0.0f;
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
             if constexpr (BIAS) {
                 if (entry) bias = a.bias_values[row * a.ldbv + entry - 1];
             }
-            if (cap > 0.0f) z = softcapped<BF16>(z, cap, inv_cap);
+            if (cap > 0.0f) z = softcapped<BF16>(z, Softcap(cap, 1.0f, BF16));
             if constexpr (HIST) {
                 const uint32_t made = (word & ~kPrompt) >> SHIFT;
                 if (made | (word & kPrompt)) z = z > 0.0f ? z / rep : z * rep;
@@ -237,17 +243,20 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
         __syncthreads();
     }
 
+    const uint32_t hidden = __float_as_uint(a.mask_value);
+    const Softcap capped(cap > 0.0f ? cap : 1.0f, inv_temp, BF16);
 #pragma unroll
     for (int k = 0; k < VECS; ++k) {
         const int local = (k * kThreads + tid) * E;
         const int c = base + local;
         if (c >= V) continue;
         float o[E];
+        if (cap > 0.0f) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float z = Elt<BF16>::get(x[k], e);
-            if (cap > 0.0f) z = softcapped<BF16>(z, cap, inv_cap);
-            o[e] = z * inv_temp;
+            for (int e = 0; e < E; ++e) o[e] = softcapped<BF16>(Elt<BF16>::get(x[k], e), capped);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = Elt<BF16>::get(x[k], e) * inv_temp;
         }
         if constexpr (SPARSE) {
 #pragma unroll
@@ -262,7 +271,10 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
             if ((c0 >> 5) == (c1 >> 5)) bits = lo[k] >> (c0 & 31);   // bit e: column c + e is allowed
             if (c < 0) bits <<= -c;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = (bits & (1u << e)) ? o[e] : a.mask_value;
+            for (int e = 0; e < E; ++e) {   // all ones or all zeros from bit e, then one bit-field select
+                const uint32_t keep = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(bits), e, 1));
+                o[e] = __uint_as_float((keep & __float_as_uint(o[e])) | (~keep & hidden));
+            }
         }
         if (c >= 0 && c + E <= V) {
             *reinterpret_cast<any16 *>(orow + static_cast<int64_t>(c) * BYTES) = Elt<BF16>::pack(o);
@@ -281,7 +293,7 @@ hipError_t launch(const RulesArgs &a, hipStream_t st) {
     const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ldx * Elt<BF16>::bytes % 16 == 0;
     const int64_t slices = (a.V + (aligned ? 0 : Elt<BF16>::E - 1) + COLS - 1) / COLS;
     // a launch has fewer than 2^32 threads
-    const int64_t rows = ((int64_t(1) << 22) / slices) / 8 * 8;
+    const int64_t rows = ((int64_t(1) << 22) / slices) / 8 * 8;   // slices <= 2^19
     for (int64_t r = 0; r < a.n; r += rows) {
         RulesArgs b = a;
         b.n = a.n - r < rows ? a.n - r : rows;

@@ -233,24 +233,31 @@ class _RmsNorm(torch.autograd.Function):
         return y, total
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, gy, gs=None):
-        s, weight, rstd = ctx.saved_tensors
-        need_x, need_w, need_r = ctx.needs_input_grad[:3]
-        if gy is None:   # nothing came through the norm
-            return (gs if need_x else None), None, (gs if need_r else None), None, None
-        # Autograd hands gradients of the outputs' shape, type and device, on the stream the forward ran
-        # on and with its device current; the saved tensors were checked there.  This runs on autograd's
-        # thread, where every interpreted line costs twice what it does on the caller's.
-        H = s.shape[-1]
-        gx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-        s2, g2, gs2, gx2 = _rows_of(s, H), _rows_of(gy, H), None if gs is None else _rows_of(gs, H), _rows_of(gx, H)
-        gw = None if weight is None or not need_w else torch.empty(H, dtype=weight.dtype, device=s.device)
-        code = _CODES[s.dtype]
-        wcode = code if weight is None else _CODES[weight.dtype]
-        _norm_backward(g2, _ld(g2), s2, _ld(s2), code, weight, wcode, ctx.offset, rstd, gs2, H if gs2 is None else _ld(gs2),
-                       gx2, H, gw, wcode, None, _current_stream(s.device.index))
-        return (gx if need_x else None), gw, (gx if need_r else None), None, None
+        return (_norm_backward_twice if torch.is_grad_enabled() else _norm_backward_once)(ctx, gy, gs)
+
+
+def _norm_backward_once(ctx, gy, gs):
+    """The backward on autograd's own thread, where every interpreted line costs twice what it does on
+    the caller's.  Autograd hands gradients of the outputs' shape, type and device, on the stream the
+    forward ran on and with its device current; the saved tensors were checked in the forward."""
+    s, weight, rstd = ctx.saved_tensors
+    need_x, need_w, need_r = ctx.needs_input_grad[:3]
+    if gy is None:   # nothing came through the norm
+        return (gs if need_x else None), None, (gs if need_r else None), None, None
+    H = s.shape[-1]
+    gx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+    s2, g2, gs2, gx2 = _rows_of(s, H), _rows_of(gy, H), None if gs is None else _rows_of(gs, H), _rows_of(gx, H)
+    gw = None if weight is None or not need_w else torch.empty(H, dtype=weight.dtype, device=s.device)
+    code = _CODES[s.dtype]
+    wcode = code if weight is None else _CODES[weight.dtype]
+    _norm_backward(g2, _ld(g2), s2, _ld(s2), code, weight, wcode, ctx.offset, rstd, gs2, H if gs2 is None else _ld(gs2),
+                   gx2, H, gw, wcode, None, _current_stream(s.device.index))
+    return (gx if need_x else None), gw, (gx if need_r else None), None, None
+
+
+# with create_graph: first-order gradients, and an error for those of higher order
+_norm_backward_twice = torch.autograd.function.once_differentiable(_norm_backward_once)
 
 
 def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
@@ -415,20 +422,26 @@ class _Linear(torch.autograd.Function):
         return out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        x, weight, preact = ctx.saved_tensors
-        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-        gx = gw = gb = None
-        if need_x or need_w or need_b:
-            if need_x:
-                gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
-                                    activation=ctx.activation, preact=preact, want_grad_x=need_x,
-                                    want_grad_weight=need_w, want_grad_bias=need_b, grad_weight_dtype=weight.dtype,
-                                    grad_bias_dtype=ctx.bias_dtype, grad_x=gx if gx is None else _rows_of(gx, x.shape[-1]))
-            gw, gb = r.grad_weight, r.grad_bias
-        return gx, gw, gb, (g if need_r else None), None
+        return (_linear_backward_twice if torch.is_grad_enabled() else _linear_backward_once)(ctx, g)
+
+
+def _linear_backward_once(ctx, g):
+    x, weight, preact = ctx.saved_tensors
+    need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+    gx = gw = gb = None
+    if need_x or need_w or need_b:
+        if need_x:
+            gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
+                                activation=ctx.activation, preact=preact, want_grad_x=need_x,
+                                want_grad_weight=need_w, want_grad_bias=need_b, grad_weight_dtype=weight.dtype,
+                                grad_bias_dtype=ctx.bias_dtype, grad_x=gx if gx is None else _rows_of(gx, x.shape[-1]))
+        gw, gb = r.grad_weight, r.grad_bias
+    return gx, gw, gb, (g if need_r else None), None
+
+
+_linear_backward_twice = torch.autograd.function.once_differentiable(_linear_backward_once)
 
 
 def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
