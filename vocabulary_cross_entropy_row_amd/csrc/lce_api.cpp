@@ -831,6 +831,9 @@ lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad
     if (st != LCE_OK) return st;
     if (M % 8) return fail(LCE_ERR_UNSUPPORTED, "%s: M must be a multiple of 8 (got %lld)", fn, (long long)M);
     if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
+    // the transposes' workgroups, of 128 x 64 values each, are one launch of fewer than 2^32 threads
+    if ((n / 128 + 1) * ((M + K) / 64 + 2) + (M / 128 + 1) * (K / 64 + 1) >= (int64_t(1) << 23))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: n (M + K) + M K must be below 2^36", fn);
     if (!f32_or_bf16(grad_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_out dtype %d", fn, (int)grad_dtype);
     if (grad_weight && !f32_or_bf16(grad_weight_dtype))
         return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_weight dtype %d", fn, (int)grad_weight_dtype);

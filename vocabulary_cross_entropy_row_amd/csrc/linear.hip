@@ -8,8 +8,8 @@
 //   grad_x = dz W        the same kernel on dz [n, M] and W^T [K, M]
 //   grad_W = dz^T x      ... on dz^T [M, n] and x^T [K, n]
 //   grad_b = sum dz      column sums, fp32 partials per 128 rows folded in order
-// One pass reads grad_out (and the pre-activation) and writes dz, dz^T and the bias
-// partials; W^T and x^T are transposed by the same kernel.
+// One launch reads grad_out (and the pre-activation), the weight and x, and writes dz,
+// dz^T, the bias's partial sums, W^T and x^T.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <stdint.h>
@@ -115,15 +115,14 @@ hipError_t launch_rows(const linear::Args &g, bool fp8, hipStream_t st) {
     return hipGetLastError();
 }
 
-// ---- transposes ---------------------------------------------------------------------
+// ---- what the backward's products read ---------------------------------------------------
 
 constexpr int kTrRows = 128, kTrCols = 64;
 
-// v = in, or in act'(pre); out[r][c] = bf16(v) when out is given; out_t[c][r] = bf16(v), rows
-// [rows, rows_pad) as zeros; part[blockIdx.y][c] = sum over the block's rows of v, not rounded.  A tile of
-// 128 x 64 goes through LDS, 16-byte chunk c of row r at c ^ (r / 8 mod 8): the writes of a wave cover
-// 1 KB without conflicts and the eight rows of an output chunk are read from different banks.
-struct TransposeArgs {
+// One matrix to transpose: v = in, or in act'(pre); out[r][c] = bf16(v) when out is given; out_t[c][r] =
+// bf16(v), rows [rows, rows_pad) as zeros; sums of v, not rounded, over the rows of a block of 128, to
+// part[block][c], or to `total` where there is one block only.
+struct Transpose {
     const void *in;        // [rows, cols] bf16 or fp32
     int64_t ld_in;
     const uint16_t *pre;   // bf16, or NULL
@@ -134,44 +133,58 @@ struct TransposeArgs {
     uint16_t *out_t;       // [cols, rows_pad] or NULL
     int64_t ld_t;
     float *part;           // [row blocks][cols] or NULL
+    void *total;           // [cols] bf16 or fp32, or NULL
     int rows, rows_pad, cols;
+    int tiles_c;           // column tiles
+    bool in_bf16, total_bf16;
 };
-template <bool BF16_IN>
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
+constexpr int kMaxJobs = 3;
+struct TransposeJobs {
+    Transpose job[kMaxJobs];
+    unsigned end[kMaxJobs];   // one past the job's last workgroup
+};
+// All the transposes of a backward in one launch.  A tile of 128 x 64 goes through LDS, 16-byte chunk c
+// of row r at c ^ (r / 8 mod 8): the writes of a wave cover 1 KB without conflicts and the eight rows
+// of an output chunk are read from different banks.  Bound by memory (4096 x 16384 with an activation,
+// its weight and its input, 870 MB: 190 us).
+__global__ __launch_bounds__(256) void transpose_kernel(TransposeJobs jobs) {
     constexpr int PER = kTrRows * (kTrCols / 8) / 256;   // 16-byte chunks per thread
     __shared__ __align__(16) uint16_t tile[kTrRows * kTrCols];
     __shared__ float sums[32][kTrCols];   // per row of threads
+    const unsigned b = blockIdx.x;
+    const int j = b < jobs.end[0] ? 0 : (b < jobs.end[1] ? 1 : 2);
+    const Transpose &a = jobs.job[j];
+    const int tile_at = static_cast<int>(b - (j ? jobs.end[j - 1] : 0));
+    const int block = tile_at / a.tiles_c;
     float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    const int r0 = blockIdx.y * kTrRows, c0 = blockIdx.x * kTrCols;
+    const int r0 = block * kTrRows, c0 = (tile_at - block * a.tiles_c) * kTrCols;
     const int t = threadIdx.x;
-    const bool vin = (a.ld_in * (BF16_IN ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.in) % 16 == 0;
-    const bool vpre = a.ld_pre % 8 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
 #pragma unroll
     for (int h = 0; h < PER; ++h) {
         const int idx = t + h * 256, r = idx >> 3, ch = idx & 7;
         const int gr = r0 + r, gc = c0 + ch * 8;
         const bool full = gr < a.rows && gc + 8 <= a.cols;
         float v[8];
-        if (vin && full) {
-            if constexpr (BF16_IN) {
-                const u32x4 q = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.in) + gr * a.ld_in + gc);
+        if (full && a.in_bf16) {
+            const u32x4 q = *reinterpret_cast<const linear::any16 *>(static_cast<const uint16_t *>(a.in) + gr * a.ld_in + gc);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = Elt<true>::get(q, e);
-            } else {
-                const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(a.in) + gr * a.ld_in + gc);
-                const float4 x = q[0], y = q[1];
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-                v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-            }
+            for (int e = 0; e < 8; ++e) v[e] = Elt<true>::get(q, e);
+        } else if (full) {
+            const linear::any16 *q = reinterpret_cast<const linear::any16 *>(static_cast<const float *>(a.in) + gr * a.ld_in + gc);
+            const u32x4 x = q[0], y = q[1];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = Elt<false>::get(e < 4 ? x : y, e & 3);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = gr < a.rows && gc + e < a.cols ? Elt<BF16_IN>::load_one(a.in, gr * a.ld_in + gc + e) : 0.0f;
+                v[e] = gr >= a.rows || gc + e >= a.cols ? 0.0f
+                       : a.in_bf16                      ? Elt<true>::load_one(a.in, gr * a.ld_in + gc + e)
+                                                        : Elt<false>::load_one(a.in, gr * a.ld_in + gc + e);
         }
         if (a.pre) {
             float z[8];
-            if (vpre && full) {
-                const u32x4 q = *reinterpret_cast<const u32x4 *>(a.pre + gr * a.ld_pre + gc);
+            if (full) {
+                const u32x4 q = *reinterpret_cast<const linear::any16 *>(a.pre + gr * a.ld_pre + gc);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[e] = Elt<true>::get(q, e);
             } else {
@@ -196,7 +209,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
         }
         *reinterpret_cast<u32x4 *>(tile + r * kTrCols + ((ch ^ (r >> 3)) & 7) * 8) = q;
     }
-    if (a.part) {
+    const bool summed = a.part || a.total;
+    if (summed) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[t >> 3][(t & 7) * 8 + e] = sum[e];
     }
@@ -216,20 +230,13 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
             *reinterpret_cast<u32x4 *>(a.out_t + gc * a.ld_t + gr) = o;
         }
     }
-    if (a.part && t < kTrCols && c0 + t < a.cols) {
+    if (summed && t < kTrCols && c0 + t < a.cols) {
         float v = sums[0][t];
         for (int r = 1; r < 32; ++r) v += sums[r][t];
-        a.part[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + t] = v;
+        if (a.part) a.part[static_cast<int64_t>(block) * a.cols + c0 + t] = v;
+        else if (a.total_bf16) Elt<true>::store_one(a.total, c0 + t, v);
+        else static_cast<float *>(a.total)[c0 + t] = v;
     }
-}
-
-hipError_t transpose(const TransposeArgs &a, bool bf16_in, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.cols, kTrCols)),
-                    static_cast<unsigned>(ceil_div(std::max(a.rows, a.rows_pad), kTrRows)));
-    if (grid.x == 0 || grid.y == 0) return hipSuccess;
-    if (bf16_in) hipLaunchKernelGGL(transpose_kernel<true>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(transpose_kernel<false>, grid, dim3(256), 0, st, a);
-    return hipGetLastError();
 }
 
 // Workspace of the backward: regions in bytes
@@ -324,9 +331,20 @@ hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st) {
     // without an activation a bf16 grad_out whose rows the product can read is dz
     const bool direct = !active && a.grad_bf16 && on16(a.grad_out) && a.ldg % 8 == 0;
     hipError_t e;
-    TransposeArgs d{};
+    TransposeJobs jobs{};
+    int count = 0;
+    unsigned groups = 0;
+    auto add = [&](const Transpose &t) {
+        jobs.job[count] = t;
+        jobs.job[count].tiles_c = static_cast<int>(ceil_div(t.cols, kTrCols));
+        groups += static_cast<unsigned>(ceil_div(t.cols, kTrCols) * ceil_div(std::max(t.rows, t.rows_pad), kTrRows));
+        jobs.end[count++] = groups;
+    };
+    const bool one_block = a.n > 0 && a.n <= kTrRows;   // its column sums are the bias's gradient
+    Transpose d{};
     d.in = a.grad_out;
     d.ld_in = a.ldg;
+    d.in_bf16 = a.grad_bf16;
     d.pre = active ? static_cast<const uint16_t *>(a.preact) : nullptr;
     d.ld_pre = a.ldp;
     d.act = a.act;
@@ -334,23 +352,45 @@ hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st) {
     d.ld_out = a.M;
     d.out_t = a.grad_weight ? dzt : nullptr;
     d.ld_t = L.np;
-    d.part = a.grad_bias ? bias_part : nullptr;
+    d.part = a.grad_bias && !one_block ? bias_part : nullptr;
+    d.total = one_block ? a.grad_bias : nullptr;
+    d.total_bf16 = a.grad_bias_bf16;
     d.rows = static_cast<int>(a.n);
     d.rows_pad = static_cast<int>(L.np);
     d.cols = static_cast<int>(a.M);
-    if ((d.out || d.out_t || d.part) && (e = transpose(d, a.grad_bf16, st)) != hipSuccess) return e;
-    if (a.grad_bias && (e = launch_column_fold(bias_part, ceil_div(a.n, kTrRows), a.M, a.M, a.grad_bias, a.grad_bias_bf16,
-                                               st)) != hipSuccess)
-        return e;
-    if (a.grad_x && a.n > 0) {
-        TransposeArgs t{};
+    if (a.n > 0 && (d.out || d.out_t || d.part || d.total)) add(d);
+    if (a.grad_x && a.n > 0) {   // W^T
+        Transpose t{};
         t.in = a.weight;
         t.ld_in = a.ldw;
+        t.in_bf16 = true;
         t.out_t = wt;
         t.ld_t = a.M;
         t.rows = t.rows_pad = static_cast<int>(a.M);
         t.cols = static_cast<int>(a.K);
-        if ((e = transpose(t, true, st)) != hipSuccess) return e;
+        add(t);
+    }
+    if (a.grad_weight && a.n > 0) {   // x^T
+        Transpose t{};
+        t.in = a.x;
+        t.ld_in = a.ldx;
+        t.in_bf16 = true;
+        t.out_t = xt;
+        t.ld_t = L.np;
+        t.rows = static_cast<int>(a.n);
+        t.rows_pad = static_cast<int>(L.np);
+        t.cols = static_cast<int>(a.K);
+        add(t);
+    }
+    for (int j = count; j < kMaxJobs; ++j) jobs.end[j] = groups;
+    if (groups) {
+        hipLaunchKernelGGL(transpose_kernel, dim3(groups), dim3(256), 0, st, jobs);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (a.grad_bias && !one_block &&
+        (e = launch_column_fold(bias_part, ceil_div(a.n, kTrRows), a.M, a.M, a.grad_bias, a.grad_bias_bf16, st)) != hipSuccess)
+        return e;
+    if (a.grad_x && a.n > 0) {
         LinearArgs g{};
         g.x = direct ? a.grad_out : dz;
         g.ldx = direct ? a.ldg : a.M;
@@ -366,15 +406,6 @@ hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st) {
         if ((e = launch_linear(g, st)) != hipSuccess) return e;
     }
     if (a.grad_weight) {
-        TransposeArgs t{};
-        t.in = a.x;
-        t.ld_in = a.ldx;
-        t.out_t = xt;
-        t.ld_t = L.np;
-        t.rows = static_cast<int>(a.n);
-        t.rows_pad = static_cast<int>(L.np);
-        t.cols = static_cast<int>(a.K);
-        if ((e = transpose(t, true, st)) != hipSuccess) return e;
         LinearArgs g{};
         g.x = dzt;
         g.ldx = L.np;

@@ -389,14 +389,22 @@ def lce_linear_backward(grad_out, x, weight, *, activation: str = "none", preact
         bcode = _float_code(grad_bias, "grad_bias")
         _buf(grad_bias, "grad_bias", grad_bias.dtype, M, dev)
     need = lce_linear_backward_workspace_bytes(n, K, M)
-    if workspace is None:   # clobbered by the call
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _buf(workspace, "workspace", torch.uint8, need, dev)
-    _check(lib().lce_linear_backward(grad_out.data_ptr(), ldg, gcode, x.data_ptr(), ldx, weight.data_ptr(), ldw,
-                                     _ptr(preact) if act else None, ldp, act, n, K, M, _ptr(grad_x), ldgx,
-                                     _ptr(grad_weight), wcode, _ptr(grad_bias), bcode, workspace.data_ptr(),
-                                     workspace.numel(), stream))
+    if workspace is not None:
+        _buf(workspace, "workspace", torch.uint8, need, dev)
+    _linear_backward(grad_out, ldg, gcode, x, ldx, weight, ldw, preact if act else None, ldp, act, grad_x, ldgx,
+                     grad_weight, wcode, grad_bias, bcode, workspace, stream)
     return LinearGrads(grad_x, grad_weight, grad_bias)
+
+
+def _linear_backward(g, ldg, gcode, x, ldx, weight, ldw, preact, ldp, act, gx, ldgx, gw, wcode, gb, bcode, workspace, stream):
+    """The call, its operands checked: allocates the workspace if there is none."""
+    n, K = x.shape
+    M = weight.shape[0]
+    if workspace is None:   # clobbered by the call
+        workspace = torch.empty(max(lce_linear_backward_workspace_bytes(n, K, M), 1), dtype=torch.uint8, device=x.device)
+    _check(lib().lce_linear_backward(g.data_ptr(), ldg, gcode, x.data_ptr(), ldx, weight.data_ptr(), ldw, _ptr(preact), ldp,
+                                     act, n, K, M, _ptr(gx), ldgx, _ptr(gw), wcode, _ptr(gb), bcode, workspace.data_ptr(),
+                                     workspace.numel(), stream))
 
 
 class _Linear(torch.autograd.Function):
@@ -426,18 +434,24 @@ class _Linear(torch.autograd.Function):
         return (_linear_backward_twice if torch.is_grad_enabled() else _linear_backward_once)(ctx, g)
 
 
-def _linear_backward_once(ctx, g):
+def _linear_backward_once(ctx, g):   # on autograd's thread, as _norm_backward_once
     x, weight, preact = ctx.saved_tensors
     need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
     gx = gw = gb = None
     if need_x or need_w or need_b:
+        M, K = weight.shape
+        dev, bcode = x.device, LCE_F32
         if need_x:
-            gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        r = lce_linear_backward(_rows_of(g, weight.shape[0]), _rows_of(x, x.shape[-1]), weight,
-                                activation=ctx.activation, preact=preact, want_grad_x=need_x,
-                                want_grad_weight=need_w, want_grad_bias=need_b, grad_weight_dtype=weight.dtype,
-                                grad_bias_dtype=ctx.bias_dtype, grad_x=gx if gx is None else _rows_of(gx, x.shape[-1]))
-        gw, gb = r.grad_weight, r.grad_bias
+            gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if need_w:
+            gw = torch.empty((M, K), dtype=weight.dtype, device=dev)
+        if need_b:
+            gb = torch.empty(M, dtype=ctx.bias_dtype, device=dev)
+            bcode = _CODES[ctx.bias_dtype]
+        g2, x2 = _rows_of(g, M), _rows_of(x, K)
+        _linear_backward(g2, _ld(g2), _CODES[g2.dtype], x2, _ld(x2), weight, _ld(weight), preact, M,
+                         ACTIVATIONS[ctx.activation], None if gx is None else _rows_of(gx, K), K, gw, LCE_BF16, gb, bcode,
+                         None, _current_stream(dev.index))
     return gx, gw, gb, (g if need_r else None), None
 
 
