@@ -122,18 +122,24 @@ def lce_rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_off
     ycode = _CODES.get(out_dtype)
     if out_dtype != x.dtype and ycode != LCE_E4M3:
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn (got {out_dtype})")
-    if y is None:
+    ldy = lds = H
+    plain = ldx == H   # x is contiguous: its like is the cheapest allocation
+    if y is not None:
+        ldy = _rows(y, "y", out_dtype, n, H, dev)
+    elif plain and out_dtype == x.dtype:
+        y = torch.empty_like(x)
+    else:
         y = torch.empty((n, H), dtype=out_dtype, device=dev)
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty((n, H), dtype=x.dtype, device=dev)
+    if sum_out is not None:
+        lds = _rows(sum_out, "sum_out", x.dtype, n, H, dev)
+    elif residual is not None:
+        sum_out = torch.empty_like(x) if plain else torch.empty((n, H), dtype=x.dtype, device=dev)
     if rstd is None and want_rstd:
         rstd = torch.empty(n, dtype=torch.float32, device=dev)
     if ycode != LCE_E4M3:
         scale = None
     elif scale is None:
         scale = torch.empty(n, dtype=torch.float32, device=dev)
-    ldy = _rows(y, "y", out_dtype, n, H, dev)
-    lds = _rows(sum_out, "sum_out", x.dtype, n, H, dev)
     _buf(rstd, "rstd", torch.float32, n, dev)
     _buf(scale, "scale", torch.float32, n, dev)
     _check(lib().lce_rms_norm(x.data_ptr(), ldx, code, _ptr(residual), ldr, _ptr(weight), wcode, float(weight_offset),
@@ -338,17 +344,21 @@ def lce_linear(x, weight, *, bias=None, activation: str = "none", residual=None,
         out_dtype = torch.bfloat16 if out is None else out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    if out is None:
+    ldo = ldp = M
+    if out is not None:
+        ldo = _rows(out, "out", out_dtype, n, M, dev)
+    else:
         out = torch.empty((n, M), dtype=out_dtype, device=dev)
-    if preact is None and want_preact:
+    if preact is not None:
+        ldp = _rows(preact, "preact", torch.bfloat16, n, M, dev)
+    elif want_preact:
         preact = torch.empty((n, M), dtype=torch.bfloat16, device=dev)
-    ldo = _rows(out, "out", out_dtype, n, M, dev)
-    ldr = _rows(residual, "residual", out_dtype, n, M, dev)
-    ldp = _rows(preact, "preact", torch.bfloat16, n, M, dev)
+    ldr = M if residual is None else _rows(residual, "residual", out_dtype, n, M, dev)
     need = lce_linear_workspace_bytes(n, K, M, e4m3)
-    if need and workspace is None:   # clobbered by the call
+    if workspace is not None:
+        _buf(workspace, "workspace", torch.uint8, need, dev)
+    elif need:   # clobbered by the call
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _buf(workspace, "workspace", torch.uint8, need, dev)
     _check(lib().lce_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, LCE_E4M3 if e4m3 else LCE_BF16, _ptr(scale_x),
                             _ptr(scale_w), _ptr(bias), bcode, act, _ptr(residual), ldr, n, K, M, out.data_ptr(), ldo,
                             _CODES[out_dtype], _ptr(preact), ldp, _ptr(workspace),
