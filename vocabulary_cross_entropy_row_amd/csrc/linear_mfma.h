@@ -17,6 +17,15 @@
 // consecutive features per lane: bias and scales are read once per lane, and
 // residual, pre-activation and output move 16 bytes at a time.
 //
+// 256 x 256 tiles, 1024 x 6656 x 202048 bf16: 2.2 ms, 1.25 PFLOP/s with the matrix
+// units busy 71% of the time at the 1.5 to 1.7 GHz that their power leaves (all-zero
+// operands run 1.4 times as fast); the library product of 8192 to 16384 cubed reaches
+// 1.42 to 1.55.  A step of K takes 1.5 us and a tile's start and end 8 to 10, half of
+// that stores, which nothing overlaps.  e4m3, 4096 x 8192 x 8192: 245 us, 2.2 PFLOP/s,
+// matrix units busy 47% at 2.1 GHz; the waves wait for operands (a row stride of 8192
+// bytes costs 8% of that; five tiles of 64 bytes in flight instead of 2.5 of 128 gain
+// nothing).
+//
 // MFMA operand layout: lane l supplies row l % 32 of A (column of B) and, of a step
 // of K, the 16-byte chunk 2 s + l / 32 for bf16 sub-step s (32x32x16); an e4m3
 // sub-step (32x32x64) takes the chunks of two bf16 sub-steps.  Which k a byte stands
