@@ -187,6 +187,28 @@ def test_strides_and_what_lies_beside(n, K, M, e4m3):
     assert torch.equal(lce.lce_linear(x, w, residual=own, out=own, activation="silu").out, ref.out)
 
 
+@pytest.mark.parametrize("n,K", [(3, 256), (40, 512), (40, 8192)])
+def test_offsets_past_32_bits(n, K):
+    """Output, residual and pre-activation rows far apart, x and weight with the widest strides: byte
+    offsets past 32 bits, in the kernel for few tokens, in tiles and with K split."""
+    M, ld = 96, (1 << 32) // n // 8 * 8 + 64
+    r = _normal(n)
+    x, w, res = r(n, K).to(BF16), (r(M, K) / 16).to(BF16), r(n, M).to(BF16)
+    want = lce.lce_linear(x, w, residual=res, activation="silu", want_preact=True)
+    flat = [torch.zeros(ld * (n - 1) + M, dtype=BF16, device=DEV) for _ in range(3)]
+    far = [f.as_strided((n, M), (ld, 1)) for f in flat]
+    far[0].copy_(res)
+    got = lce.lce_linear(x, w, residual=far[0], out=far[1], preact=far[2], activation="silu")
+    assert torch.equal(got.out, want.out) and torch.equal(got.preact, want.preact)
+    del flat, far
+    wide = (1 << 23) - 1024                          # elements: just under 16 MiB
+    xs = torch.zeros(wide * (n - 1) + K, dtype=BF16, device=DEV).as_strided((n, K), (wide, 1))
+    ws = torch.zeros(wide * (M - 1) + K, dtype=BF16, device=DEV).as_strided((M, K), (wide, 1))
+    xs.copy_(x), ws.copy_(w)
+    got = lce.lce_linear(xs, ws, residual=res, activation="silu", want_preact=True)
+    assert torch.equal(got.out, want.out) and torch.equal(got.preact, want.preact)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("n,K,M", [(1, 8, 8), (3, 64, 40), (60, 512, 1000), (130, 200, 136), (257, 1024, 512),
                                    (1000, 264, 2048), (2100, 1032, 520)])
@@ -330,6 +352,7 @@ def test_refusals_on_the_gpu():
                  lambda: lce.lce_linear(x, w, activation="tanh"),
                  lambda: lce.lce_linear_backward(torch.zeros(4, 8, device=DEV, dtype=BF16), x, w, activation="silu"),
                  lambda: lce.lce_linear(x, w, bias=torch.ones(7, device=DEV)),
+                 lambda: lce.lce_linear(x, w, bias=torch.ones(9, device=DEV)),
                  lambda: lce.linear(x.clone().requires_grad_(), w[:7]),
                  lambda: lce.linear(x, w, residual=torch.ones(4, 7, device=DEV, dtype=BF16))):
         with pytest.raises(ValueError):

@@ -162,6 +162,24 @@ def test_strides_and_what_lies_beside(H, ld, first, dtype):
     assert torch.equal(again.sum, ref.sum) and torch.equal(again.y, r.y) and torch.equal(rv, ref.sum)
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^31 elements apart: byte offsets past 32 bits in every operand."""
+    H, ld = 1000, (1 << 31) + 8
+
+    def far(t=None):
+        v = torch.zeros(ld + H, dtype=BF16, device=DEV).as_strided((2, H), (ld, 1))
+        return v if t is None else v.copy_(t)
+
+    x, _, w, gy, _ = _inputs(2, H, BF16, 5, residual=False, wdtype=BF16)
+    ref = lce.lce_rms_norm(x, w, want_rstd=True)
+    xs, ys = far(x), far()
+    r = lce.lce_rms_norm(xs, w, y=ys, want_rstd=True)
+    assert torch.equal(r.y, ref.y) and torch.equal(r.rstd, ref.rstd)
+    gx, gw = lce.lce_rms_norm_backward(gy, x, w, ref.rstd)
+    got, gw2 = lce.lce_rms_norm_backward(far(gy), xs, w, r.rstd, grad_x=ys)
+    assert torch.equal(got, gx) and torch.equal(gw2, gw)
+
+
 def test_no_rows():
     x = torch.empty((0, 64), dtype=BF16, device=DEV)
     w = torch.ones(64, dtype=BF16, device=DEV)

@@ -152,12 +152,12 @@ def lce_rms_norm_workspace_bytes(n: int, H: int) -> int:
     return int(lib().lce_rms_norm_workspace_bytes(int(n), int(H)))
 
 
-def _norm_backward(gy, ldg, s, lds, code, weight, wcode, offset, rstd, gs, ldgs, gx, ldgx, gw, gwcode, workspace, stream):
+def _norm_backward(gy, ldg, s, lds, code, n, H, weight, wcode, offset, rstd, gs, ldgs, gx, ldgx, gw, gwcode, workspace,
+                   stream):
     """The call, its operands checked: allocates the workspace that a weight's gradient needs."""
-    n, H = s.shape
     bytes_ = 0
     if gw is not None:
-        bytes_ = lce_rms_norm_workspace_bytes(n, H)
+        bytes_ = lib().lce_rms_norm_workspace_bytes(n, H)
         if workspace is None:   # clobbered by the call
             workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=s.device)
     _check(lib().lce_rms_norm_backward(gy.data_ptr(), ldg, s.data_ptr(), lds, code, _ptr(weight), wcode, offset,
@@ -194,8 +194,8 @@ def lce_rms_norm_backward(grad_y, s, weight, rstd, *, grad_sum=None, weight_offs
         _buf(grad_weight, "grad_weight", grad_weight.dtype, H, dev)
         if workspace is not None:
             _buf(workspace, "workspace", torch.uint8, lce_rms_norm_workspace_bytes(n, H), dev)
-    _norm_backward(grad_y, ldg, s, lds, code, weight, wcode, float(weight_offset), rstd, grad_sum, ldgs, grad_x, ldgx,
-                   grad_weight, gwcode, workspace, stream)
+    _norm_backward(grad_y, ldg, s, lds, code, n, H, weight, wcode, float(weight_offset), rstd, grad_sum, ldgs, grad_x,
+                   ldgx, grad_weight, gwcode, workspace, stream)
     return grad_x, grad_weight
 
 
@@ -221,12 +221,12 @@ class _RmsNorm(torch.autograd.Function):
             raise ValueError("x must have at least one dimension")
         H = x.shape[-1]
         x2, r2, total, sum2 = _rows_of(x, H), None, None, None
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
         if residual is not None:
             if residual.shape != x.shape:
                 raise ValueError(f"residual must have the shape of x, {list(x.shape)} (got {list(residual.shape)})")
             r2 = _rows_of(residual, H)
-            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            total = torch.empty_like(y)
             sum2 = _rows_of(total, H)
         rstd = lce_rms_norm(x2, weight, residual=r2, eps=eps, weight_offset=offset, want_rstd=True, y=_rows_of(y, H),
                             sum_out=sum2).rstd
@@ -252,13 +252,20 @@ def _norm_backward_once(ctx, gy, gs):
     if gy is None:   # nothing came through the norm
         return (gs if need_x else None), None, (gs if need_r else None), None, None
     H = s.shape[-1]
-    gx = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-    s2, g2, gs2, gx2 = _rows_of(s, H), _rows_of(gy, H), None if gs is None else _rows_of(gs, H), _rows_of(gx, H)
-    gw = None if weight is None or not need_w else torch.empty(H, dtype=weight.dtype, device=s.device)
+    lds = ldg = ldgs = H
+    rows = s
+    if not (s.is_contiguous() and gy.is_contiguous() and (gs is None or gs.is_contiguous())):
+        rows, gy = _rows_of(s, H), _rows_of(gy, H)
+        lds, ldg = _ld(rows), _ld(gy)
+        if gs is not None:
+            gs = _rows_of(gs, H)
+            ldgs = _ld(gs)
+    gx = torch.empty_like(s, memory_format=torch.contiguous_format)
+    gw = None if weight is None or not need_w else torch.empty_like(weight)
     code = _CODES[s.dtype]
     wcode = code if weight is None else _CODES[weight.dtype]
-    _norm_backward(g2, _ld(g2), s2, _ld(s2), code, weight, wcode, ctx.offset, rstd, gs2, H if gs2 is None else _ld(gs2),
-                   gx2, H, gw, wcode, None, _current_stream(s.device.index))
+    _norm_backward(gy, ldg, rows, lds, code, s.numel() // H, H, weight, wcode, ctx.offset, rstd, gs, ldgs, gx, H, gw,
+                   wcode, None, _current_stream(s.device.index))
     return (gx if need_x else None), gw, (gx if need_r else None), None, None
 
 
@@ -339,6 +346,8 @@ def lce_linear(x, weight, *, bias=None, activation: str = "none", residual=None,
     bcode = LCE_F32
     if bias is not None:
         bcode = _float_code(bias, "bias")
+        if bias.dim() != 1 or bias.shape[0] != M:
+            raise ValueError(f"bias must be [{M}] (got {list(bias.shape)})")
         _buf(bias, "bias", bias.dtype, M, dev)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
