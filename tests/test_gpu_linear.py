@@ -240,6 +240,23 @@ def test_backward(n, K, M, act, gdtype):
     assert torch.equal(one[2].grad_bias, got.grad_bias.to(BF16))
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_gradients_in_place_of_inputs(act):
+    """Each gradient in the place of an input of its type and shape (K = M)."""
+    n = K = 264
+    r = _normal(6)
+    x, w, g = r(n, K).to(BF16), (r(K, K) / 16).to(BF16), r(n, K).to(BF16)
+    pre = lce.lce_linear(x, w, activation=act, want_preact=True).preact
+    ref = lce.lce_linear_backward(g, x, w, activation=act, preact=pre)
+    for gx in range(4):
+        for gw in range(4):
+            t = [g.clone(), x.clone(), w.clone(), pre.clone()]
+            if gx == gw:
+                continue
+            got = lce.lce_linear_backward(t[0], t[1], t[2], activation=act, preact=t[3], grad_x=t[gx], grad_weight=t[gw])
+            assert torch.equal(got.grad_x, ref.grad_x) and torch.equal(got.grad_weight, ref.grad_weight), (gx, gw)
+
+
 def test_no_rows():
     x, w = torch.empty((0, 64), device=DEV, dtype=BF16), torch.ones((40, 64), device=DEV, dtype=BF16)
     assert lce.lce_linear(x, w).out.shape == (0, 40)

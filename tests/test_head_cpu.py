@@ -181,3 +181,14 @@ def test_linear_sizes_and_host_tensors():
     for call in (lambda: lce.lce_linear(x, w), lambda: lce.linear(x, w), lambda: lce.lce_linear_backward(x[:, :8], x, w)):
         with pytest.raises(ValueError, match="GPU tensor"):
             call()
+
+
+@pytest.mark.parametrize("over,needle", [
+    (dict(out=P), "out and preact must not be x or weight"), (dict(weight=2 * P), "out and preact must not be x"),
+    (dict(x=2 * P), "out and preact must not be x"), (dict(out=2 * P, preact=P, ldp=40), "must not be x or weight"),
+    (dict(out=2 * P, preact=2 * P, ldp=40), "preact must not be residual or out"),
+    (dict(out=2 * P, preact=3 * P, ldp=40, residual=3 * P, ldr=40), "preact must not be residual"),
+])
+def test_linear_rejects_outputs_that_it_still_reads(over, needle):
+    st, msg = _call("lce_linear", LINEAR, over)
+    assert st == ARG and needle in msg

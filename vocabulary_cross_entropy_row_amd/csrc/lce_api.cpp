@@ -791,6 +791,11 @@ lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ld
         return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
     if (need > 0 && !is_aligned(workspace, 16))
         return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    // every tile reads whole rows of x and weight; the residual is read after the pre-activation is written
+    if (out == x || out == weight || (preact && (preact == x || preact == weight)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: out and preact must not be x or weight", fn);
+    if (preact && (preact == residual || preact == out))
+        return fail(LCE_ERR_INVALID_ARG, "%s: preact must not be residual or out", fn);
     lce::LinearArgs a{};
     a.x = x;
     a.weight = weight;
