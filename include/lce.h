@@ -499,7 +499,8 @@ size_t lce_linear_workspace_bytes(int64_t n, int64_t K, int64_t M, lce_dtype in_
  *   workspace     device, 256-byte aligned, lce_linear_backward_workspace_bytes(n, K,
  *                 M) bytes: dz, and dz, x and weight transposed.  Clobbered; calls
  *                 that share it must not run at the same time.
- * K and M must be multiples of 8, and alignments as for lce_linear.  n == 0 writes
+ * K and M must be multiples of 8, n and M at most 2^23 - 512, and alignments as for
+ * lce_linear; grad_x and grad_weight may be in the place of an input.  n == 0 writes
  * zeros to grad_weight and grad_bias.
  */
 lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *x, int64_t ldx,

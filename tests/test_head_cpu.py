@@ -192,3 +192,11 @@ def test_linear_sizes_and_host_tensors():
 def test_linear_rejects_outputs_that_it_still_reads(over, needle):
     st, msg = _call("lce_linear", LINEAR, over)
     assert st == ARG and needle in msg
+
+
+@pytest.mark.parametrize("over", [dict(n=(1 << 23) - 511), dict(n=(1 << 23) - 1),
+                                  dict(M=(1 << 23) - 504, ldg=1 << 23, ldp=1 << 23)])
+def test_linear_backward_rejects_rows_past_its_offsets(over):
+    """n and M are the row lengths of the transposed operands: 256 such rows stay below 4 GiB."""
+    st, msg = _call("lce_linear_backward", LINEAR_BWD, over)
+    assert st == UNSUPPORTED and "2^23 - 512" in msg

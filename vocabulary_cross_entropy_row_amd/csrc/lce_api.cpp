@@ -836,6 +836,9 @@ lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad
     if (st != LCE_OK) return st;
     if (M % 8) return fail(LCE_ERR_UNSUPPORTED, "%s: M must be a multiple of 8 (got %lld)", fn, (long long)M);
     if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
+    // n and M are row lengths of what the products read: the limit check_linear puts on ldx and ldw
+    if (n > (1 << 23) - 512 || M > (1 << 23) - 512)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: n and M must be <= 2^23 - 512 (got %lld, %lld)", fn, (long long)n, (long long)M);
     // the transposes' workgroups, of 128 x 64 values each, are one launch of fewer than 2^32 threads
     if ((n / 128 + 1) * ((M + K) / 64 + 2) + (M / 128 + 1) * (K / 64 + 1) >= (int64_t(1) << 23))
         return fail(LCE_ERR_UNSUPPORTED, "%s: n (M + K) + M K must be below 2^36", fn);
