@@ -155,6 +155,20 @@ def test_activations_far_out():
         assert bool(torch.isnan(out[0]).any()) and bool(torch.isfinite(out[1]).all())
 
 
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_far_out(act):
+    """Far from zero every slope is 0 or 1, up to the largest bf16 value; a NaN stays one (relu's slope there is 0)."""
+    big = torch.finfo(BF16).max
+    pre = torch.tensor([[30, -30, 1e4, -1e4, 1e18, -1e18, 1e20, -1e20, 1e30, -1e30, 1e38, -1e38, big, -big, 0.5,
+                         float("nan")]], device=DEV).to(BF16)
+    g = torch.ones_like(pre)
+    x, w = torch.ones(1, 8, device=DEV, dtype=BF16), torch.ones(16, 8, device=DEV, dtype=BF16)
+    got = lce.lce_linear_backward(g, x, w, activation=act, preact=pre, want_grad_bias=True, grad_bias_dtype=F32).grad_bias
+    want = (pre[0, :14] > 0).double()
+    _within(got[:14], want, 2.0 ** -20, act)   # e^-30 30 < 2^-38
+    assert bool(torch.isnan(got[15])) == (act != "relu")
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("n,K,M", [(5, 96, 70), (70, 160, 200), (260, 4096, 300)])
 def test_strides_and_what_lies_beside(n, K, M, e4m3):

@@ -47,19 +47,20 @@ struct Cost {
     double step[3], tile, launch, rate, fold, fold_rate;
 };
 struct ShapeInfo {
-    int bf, bt, per_cu;
+    int bf, bt, per_cu, threads;
     Cost bf16, e4m3;
 };
 constexpr ShapeInfo kShapes[SHAPES] = {
-    {Big::BF, Big::BT, 1, {{1.22, 0, 0}, 7.5, 0.3, 4.0e6, 2.2, 5.5e6}, {{1.48, 0, 0}, 8.4, 0.8, 2.8e6, 1.1, 4.9e6}},
-    {Wide::BF, Wide::BT, 1, {{0.82, 0, 0}, 5.5, 0.0, 4.3e6, 3.1, 6.1e6}, {{0.86, 0, 0}, 6.2, 0.2, 3.4e6, 2.7, 4.9e6}},
-    {Low::BF, Low::BT, 2, {{0.38, 0.85, 0}, 0.1, 4.3, 4.8e6, 3.2, 6.4e6}, {{0.33, 0.89, 0}, 1.8, 3.2, 4.1e6, 3.1, 4.6e6}},
-    {Tiny::BF, Tiny::BT, 3, {{0.28, 0.38, 0.58}, 0.4, 3.9, 4.7e6, 2.9, 4.8e6}, {{0.23, 0.51, 0.55}, 1.7, 2.6, 4.3e6, 3.0, 4.0e6}},
-    {16, 16, 2, {{0.04, 0.16, 0}, 4.7, 0.7, 4.0e6, 0, 1}, {{0.03, 0.19, 0}, 4.3, 1.1, 8.0e6, 0, 1}},
-    {16, 32, 3, {{0.10, 0.30, 0.55}, 2.4, 2.8, 8.0e6, 0, 1}, {{0.11, 0.24, 0.56}, 4.5, 0.0, 8.0e6, 0, 1}},
+    {Big::BF, Big::BT, 1, 64 * Big::NW, {{1.22, 0, 0}, 7.5, 0.3, 4.0e6, 2.2, 5.5e6}, {{1.48, 0, 0}, 8.4, 0.8, 2.8e6, 1.1, 4.9e6}},
+    {Wide::BF, Wide::BT, 1, 64 * Wide::NW, {{0.82, 0, 0}, 5.5, 0.0, 4.3e6, 3.1, 6.1e6}, {{0.86, 0, 0}, 6.2, 0.2, 3.4e6, 2.7, 4.9e6}},
+    {Low::BF, Low::BT, 2, 64 * Low::NW, {{0.38, 0.85, 0}, 0.1, 4.3, 4.8e6, 3.2, 6.4e6}, {{0.33, 0.89, 0}, 1.8, 3.2, 4.1e6, 3.1, 4.6e6}},
+    {Tiny::BF, Tiny::BT, 3, 64 * Tiny::NW, {{0.28, 0.38, 0.58}, 0.4, 3.9, 4.7e6, 2.9, 4.8e6}, {{0.23, 0.51, 0.55}, 1.7, 2.6, 4.3e6, 3.0, 4.0e6}},
+    {16, 16, 2, 64 * linear::kRowsWaves, {{0.04, 0.16, 0}, 4.7, 0.7, 4.0e6, 0, 1}, {{0.03, 0.19, 0}, 4.3, 1.1, 8.0e6, 0, 1}},
+    {16, 32, 3, 64 * linear::kRowsWaves, {{0.10, 0.30, 0.55}, 2.4, 2.8, 8.0e6, 0, 1}, {{0.11, 0.24, 0.56}, 4.5, 0.0, 8.0e6, 0, 1}},
 };
 constexpr int kCus = 256;        // compute units of an MI355X
 constexpr int kMaxSplits = 16;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of a launch
 
 struct Plan {
     int shape, splits;
@@ -81,6 +82,7 @@ Plan plan_of(int64_t n, int64_t K, int64_t M, bool fp8) {
         for (int sp = 1; sp <= (rows ? 1 : kMaxSplits) && (sp == 1 || steps / sp >= 3); ++sp) {
             const double depth = static_cast<double>(ceil_div(steps, sp));
             const int64_t groups = tiles * sp, last = groups % slots;
+            if (round_up(groups, 8) * s.threads > kMaxThreads) break;
             double us = static_cast<double>(groups / slots) * (depth * c.step[s.per_cu - 1] + c.tile);
             if (last) us += depth * c.step[ceil_div(last, kCus) - 1] + c.tile;
             us = std::max(us, bytes / c.rate) + c.launch;
@@ -281,7 +283,7 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
     g.n = static_cast<int>(a.n);
     g.M = static_cast<int>(a.M);
     const int64_t tf = ceil_div(a.M, s.bf), tt = ceil_div(a.n, s.bt), total = tf * tt * p.splits;
-    if (total > 0x7fffffffLL / 16) return hipErrorInvalidValue;
+    if (round_up(total, 8) * s.threads > kMaxThreads) return hipErrorInvalidValue;   // outputs past the card's memory
     g.tiles_f = static_cast<int>(tf);
     g.tiles_t = static_cast<int>(tt);
     g.splits = p.splits;

@@ -165,7 +165,9 @@ __device__ __forceinline__ float slope(int act, float z) {
         }
         case ACT_GELU_TANH: {
             const float t = tanh_fast(kSqrt2OverPi * fmaf(kCubic * z * z, z, z));
-            return fmaf(0.5f * z * (1.0f - t * t), kSqrt2OverPi * fmaf(3.0f * kCubic, z * z, 1.0f), 0.5f * (1.0f + t));
+            const float q = 1.0f - t * t;   // 0 far out, where z^2 may overflow
+            const float bend = q > 0.0f ? 0.5f * z * q * kSqrt2OverPi * fmaf(3.0f * kCubic, z * z, 1.0f) : 0.0f;
+            return bend + 0.5f * (1.0f + t);
         }
         case ACT_SILU: {
             const float s = sigmoid_fast(z);
