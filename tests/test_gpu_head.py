@@ -131,3 +131,41 @@ def test_training_step():
         assert g.dtype == leaves[k].dtype
         rel = float((g.double() - e).norm() / e.norm())
         assert rel <= 8 * 2.0 ** -8, (k, rel)
+
+
+def test_training_step_captured():
+    """norm -> activated projection with residual and their backward, captured through autograd: every
+    replay gives the eager step's bits.  The leaves have no eager graph when the capture is made: the
+    warm-up and the comparison take clones."""
+    n, H = 130, 264
+    r = _rand(9)
+    static = [r(n, H, t=BF16), r(n, H, t=BF16), 1 + 0.1 * r(H), (r(H, H) / 16).to(BF16), 0.1 * r(H)]
+    g = r(n, H, t=BF16)
+
+    def step(leaves):
+        x, res, w1, proj, b = leaves
+        a, stream = lce.rms_norm(x, w1, residual=res)
+        out = lce.linear(a, proj, b, activation="gelu", residual=stream)
+        return [out.detach(), *torch.autograd.grad(out, leaves, g)]
+
+    def eager():
+        return step([t.detach().clone().requires_grad_() for t in static])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            eager()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step([t.requires_grad_() for t in static])
+    for k in range(4):
+        with torch.no_grad():
+            static[0].copy_(r(n, H))
+            g.copy_(r(n, H) * (k + 1))
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager()))

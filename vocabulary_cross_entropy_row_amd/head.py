@@ -278,7 +278,7 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
 
     Without a residual returns y; with one (x's shape and type) returns (y, sum), sum = x + residual
     being the stream that goes on.  Gradients: x, weight and residual; the gradient that reaches
-    ``sum`` is added in the same kernel.
+    ``sum`` is added in the same kernel.  Under capture, what ``linear`` says of it holds here too.
     """
     return _RmsNorm.apply(x, weight, residual, float(eps), float(weight_offset))
 
@@ -481,6 +481,9 @@ def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
     """Autograd form of the product over the last dimension of ``x``: act(x weight^T + bias) + residual,
     all of x, weight and residual bfloat16 (bias bfloat16 or float32), the output bfloat16 with x's
     leading dimensions.  Gradients have their inputs' types; sums are fp32.
+
+    Captured into a graph, forward and backward belong to one capture, and no graph of the same leaves
+    built outside it may be alive: autograd would wait on the stream that one was built on.
     """
     return _Linear.apply(x, weight, bias, residual, activation)
 
