@@ -223,6 +223,22 @@ def test_offsets_past_32_bits(n, K):
     assert torch.equal(got.out, want.out) and torch.equal(got.preact, want.preact)
 
 
+@pytest.mark.parametrize("M,ld", [(32776, 32776), (32776, 32784), (32777, 32777)])
+def test_outputs_larger_than_the_caches(M, ld):
+    """Just past 256 MB of output: rows whole 16 bytes apart, with a gap, and at an odd width."""
+    n, K = 4096, 64
+    r = _normal(M)
+    x, w = r(n, K).to(BF16), (r(M, K) / 8).to(BF16)
+    flat = r(n, ld).to(BF16)
+    out, res, gap = flat[:, :M], flat[:, :M].clone(), flat[:, M:].clone()
+    lce.lce_linear(x, w, residual=out, out=out, activation="relu")
+    for i in range(0, n, 1024):
+        xd, wd, rd = x[i:i + 1024].double(), w.double(), res[i:i + 1024].double()
+        want = (xd @ wd.t()).clamp_min(0) + rd
+        _within(out[i:i + 1024], want, _half(BF16) * want.abs() + (K + 8) * U * (xd.abs() @ wd.abs().t() + rd.abs()), "out")
+    assert torch.equal(flat[:, M:], gap)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("n,K,M", [(1, 8, 8), (3, 64, 40), (60, 512, 1000), (130, 200, 136), (257, 1024, 512),
                                    (1000, 264, 2048), (2100, 1032, 520)])

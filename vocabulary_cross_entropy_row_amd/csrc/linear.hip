@@ -60,6 +60,7 @@ constexpr ShapeInfo kShapes[SHAPES] = {
 };
 constexpr int kCus = 256;        // compute units of an MI355X
 constexpr int kMaxSplits = 16;
+constexpr int64_t kLastCache = int64_t(256) << 20;   // bytes of the cache in front of HBM
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of a launch
 
 struct Plan {
@@ -301,6 +302,13 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
     e.out = a.out;
     e.ldo = a.ldo;
     e.out_bf16 = a.out_bf16;
+    // An output that the last cache cannot hold for its reader need not displace the operands there:
+    // 4096 x 1024 x 65536 575 -> 530 us and with the cross-entropy that reads it 773 -> 725, 16384 x 512 x
+    // 32000 728 -> 635 and 1102 -> 985, 4096 x 1024 x 50256 e4m3 314 -> 290.  Smaller ones would cost their
+    // reader more than the product gains (4096 x 1024 x 32768 and the cross-entropy 353 -> 364), rows that
+    // start inside 16 bytes write parts of lines (4096 x 4096 x 50257 1366 -> 1400), and so do fp32 ones
+    // (4096 x 1024 x 32768 331 -> 374).
+    e.streams = a.out_bf16 && a.n * a.M * 2 > kLastCache && on16(a.out) && a.ldo % 8 == 0;
     e.preact = a.preact;
     e.ldp = a.ldp;
     e.n = a.n;

@@ -73,7 +73,7 @@ struct Epi {
     int64_t ldr;
     void *out;
     int64_t ldo;
-    bool out_bf16;
+    bool out_bf16, streams;   // streams: a bf16 output is stored past the caches
     void *preact;
     int64_t ldp;
     int64_t n, M;
@@ -248,7 +248,15 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v[p][u] += Elt<true>::get(ra[p], u);
             }
-            *reinterpret_cast<any16 *>(static_cast<uint16_t *>(e.out) + t * e.ldo + f) = Elt<true>::pack(v[p]);
+            any16 *o = reinterpret_cast<any16 *>(static_cast<uint16_t *>(e.out) + t * e.ldo + f);
+            const any16 q = Elt<true>::pack(v[p]);
+            if (e.streams) {
+                asm volatile("");   // before and after: or the two stores become one that does not stream
+                __builtin_nontemporal_store(q, o);
+                asm volatile("");
+            } else {
+                *o = q;
+            }
         }
     } else if (vec) {
 #pragma unroll
