@@ -16,8 +16,8 @@
 // stores, K accesses of 16 bytes (E values) per lane.  gfx950 takes those at any
 // address, so odd widths and strides run like aligned ones; only an access that
 // reaches past the row's end goes value by value.  8192 x 6656 bf16 with a residual:
-// forward 73 to 83 us (5.3 to 6.0 TB/s), backward 94 to 98 us (4.5 to 4.6 TB/s) and
-// 7 us for the partial rows of dL/dw; 4096 x 8192 to 8 bits 42 to 47 us (5.0 to 5.6
+// forward 74 to 78 us (5.6 to 5.9 TB/s), backward 92 to 98 us (4.5 to 4.7 TB/s) and
+// 5 us for the partial rows of dL/dw; 4096 x 8192 to 8 bits 42 to 44 us (5.3 to 5.6
 // TB/s).  A large copy reaches 4.9 TB/s.  Sums are fp32: within a lane in
 // column order, then across lanes in a fixed order, so results repeat bit for bit.
 #include <hip/hip_runtime.h>
@@ -383,10 +383,10 @@ struct Plan {
 };
 // Lanes by the number of accesses a row has: a 16-lane group for head-sized rows (four rows per wave),
 // then as many lanes as keep one or two accesses each: a row's time is one load, one reduction and one
-// store, and short ones keep more rows in flight.  Forward, residual, bf16: 16384 x 1536 35 us with 256
-// lanes of one access, 41 with a wave of four; 16384 x 4096 91 us with 512 of one, 99 with 256 of two;
-// 8192 x 6656 83 us with 512 of two, 93 with 256 of four; 16384 x 1024 22 us with a wave of two, 24
-// with 256 of one.
+// store, and short ones keep more rows in flight.  Forward, residual, bf16, the sum stored as y is:
+// 16384 x 1536 35 us with 256 lanes of one access, 41 with a wave of four; 16384 x 4096 91 us with 512 of
+// one, 99 with 256 of two; 8192 x 6656 83 us with 512 of two, 93 with 256 of four; 16384 x 1024 22 us with
+// a wave of two, 24 with 256 of one.
 Plan plan_of(int64_t H, int e) {
     const int64_t nv = (H + e - 1) / e;
     if (nv <= 16) return {16, 1};
