@@ -410,20 +410,22 @@ def lce_linear_backward(grad_out, x, weight, *, activation: str = "none", preact
     need = lce_linear_backward_workspace_bytes(n, K, M)
     if workspace is not None:
         _buf(workspace, "workspace", torch.uint8, need, dev)
-    _linear_backward(grad_out, ldg, gcode, x, ldx, weight, ldw, preact if act else None, ldp, act, grad_x, ldgx,
+    _linear_backward(grad_out, ldg, gcode, x, ldx, weight, ldw, preact if act else None, ldp, act, n, K, M, grad_x, ldgx,
                      grad_weight, wcode, grad_bias, bcode, workspace, stream)
     return LinearGrads(grad_x, grad_weight, grad_bias)
 
 
-def _linear_backward(g, ldg, gcode, x, ldx, weight, ldw, preact, ldp, act, gx, ldgx, gw, wcode, gb, bcode, workspace, stream):
+def _linear_backward(g, ldg, gcode, x, ldx, weight, ldw, preact, ldp, act, n, K, M, gx, ldgx, gw, wcode, gb, bcode,
+                     workspace, stream):
     """The call, its operands checked: allocates the workspace if there is none."""
-    n, K = x.shape
-    M = weight.shape[0]
     if workspace is None:   # clobbered by the call
-        workspace = torch.empty(max(lce_linear_backward_workspace_bytes(n, K, M), 1), dtype=torch.uint8, device=x.device)
+        bytes_ = lib().lce_linear_backward_workspace_bytes(n, K, M)
+        workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=x.device)
+    else:
+        bytes_ = workspace.numel()
     _check(lib().lce_linear_backward(g.data_ptr(), ldg, gcode, x.data_ptr(), ldx, weight.data_ptr(), ldw, _ptr(preact), ldp,
                                      act, n, K, M, _ptr(gx), ldgx, _ptr(gw), wcode, _ptr(gb), bcode, workspace.data_ptr(),
-                                     workspace.numel(), stream))
+                                     bytes_, stream))
 
 
 class _Linear(torch.autograd.Function):
@@ -459,18 +461,20 @@ def _linear_backward_once(ctx, g):   # on autograd's thread, as _norm_backward_o
     gx = gw = gb = None
     if need_x or need_w or need_b:
         M, K = weight.shape
-        dev, bcode = x.device, LCE_F32
+        bcode = LCE_F32
         if need_x:
-            gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            gx = torch.empty_like(x, memory_format=torch.contiguous_format)
         if need_w:
-            gw = torch.empty((M, K), dtype=weight.dtype, device=dev)
+            gw = torch.empty_like(weight, memory_format=torch.contiguous_format)
         if need_b:
-            gb = torch.empty(M, dtype=ctx.bias_dtype, device=dev)
+            gb = torch.empty(M, dtype=ctx.bias_dtype, device=x.device)
             bcode = _CODES[ctx.bias_dtype]
-        g2, x2 = _rows_of(g, M), _rows_of(x, K)
-        _linear_backward(g2, _ld(g2), _CODES[g2.dtype], x2, _ld(x2), weight, _ld(weight), preact, M,
-                         ACTIVATIONS[ctx.activation], None if gx is None else _rows_of(gx, K), K, gw, LCE_BF16, gb, bcode,
-                         None, _current_stream(dev.index))
+        rows, g2, ldx, ldg = x, g, K, M
+        if not (x.is_contiguous() and g.is_contiguous()):
+            rows, g2 = _rows_of(x, K), _rows_of(g, M)
+            ldx, ldg = _ld(rows), _ld(g2)
+        _linear_backward(g2, ldg, LCE_BF16, rows, ldx, weight, _ld(weight), preact, M, ACTIVATIONS[ctx.activation],
+                         x.numel() // K, K, M, gx, K, gw, LCE_BF16, gb, bcode, None, _current_stream(x.device.index))
     return gx, gw, gb, (g if need_r else None), None
 
 
