@@ -434,6 +434,9 @@ class _Linear(torch.autograd.Function):
         _on_gpu(x, "x")
         if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
             raise ValueError("x must have at least one dimension, and weight two")
+        for t, name in ((x, "x"), (weight, "weight")):   # the backward takes them as bf16, unchecked
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be torch.bfloat16 (got {t.dtype})")
         M = weight.shape[0]
         shape = (*x.shape[:-1], M)
         if residual is not None and residual.shape != shape:
