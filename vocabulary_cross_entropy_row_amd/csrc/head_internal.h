@@ -73,6 +73,10 @@ hipError_t launch_logits_process(const RulesArgs &a, bool is_bf16, hipStream_t s
 
 // ---- matrix product with an epilogue ----------------------------------------------
 
+// Longest row stride of what the product reads, in bytes: 256 rows, the most of a tile, and one step of
+// K read ahead keep 32-bit offsets.
+constexpr int64_t kLinearMaxStride = (int64_t(1) << 32) / 256 - 1024;
+
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
 
 struct LinearArgs {

@@ -747,9 +747,7 @@ lce_status check_linear(const char *fn, const void *x, int64_t ldx, const void *
                     fn, (long long)unit);
     if ((x && !is_aligned(x, 16)) || !is_aligned(weight, 16))
         return fail(LCE_ERR_UNSUPPORTED, "%s: x and weight must be 16-byte aligned", fn);
-    // 32-bit offsets inside a tile of 256 rows, one step of K read ahead
-    const int64_t most = (int64_t(1) << 32) / 256 - 1024;
-    if (ldx * es > most || ldw * es > most || n > 0x7fffffffLL / 256 || M > 0x7fffffffLL / 256)
+    if (ldx > lce::kLinearMaxStride / es || ldw > lce::kLinearMaxStride / es || n > 0x7fffffffLL / 256 || M > 0x7fffffffLL / 256)
         return fail(LCE_ERR_UNSUPPORTED, "%s: 256 rows of x or weight exceed 4 GiB, or n or M >= 2^23", fn);
     return LCE_OK;
 }

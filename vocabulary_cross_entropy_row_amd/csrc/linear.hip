@@ -339,7 +339,8 @@ hipError_t launch_linear_backward(const LinearGradArgs &a, hipStream_t st) {
     float *bias_part = reinterpret_cast<float *>(ws + L.off_bias), *part = reinterpret_cast<float *>(ws + L.off_part);
     const bool active = a.act != ACT_NONE;
     // without an activation a bf16 grad_out whose rows the product can read, and does not overwrite, is dz
-    const bool direct = !active && a.grad_bf16 && on16(a.grad_out) && a.ldg % 8 == 0 && a.grad_out != a.grad_x;
+    const bool direct = !active && a.grad_bf16 && on16(a.grad_out) && a.ldg % 8 == 0 &&
+                        a.ldg <= kLinearMaxStride / 2 && a.grad_out != a.grad_x;
     hipError_t e;
     TransposeJobs jobs{};
     int count = 0;
