@@ -56,3 +56,24 @@ def test_operands_other_than_bf16_are_refused(calls, xt, wt, grad):
     with pytest.raises(TypeError, match="must be torch.bfloat16"):
         lce.linear(x, w)
     assert not calls
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_without_gradients_any_width_and_no_preactivation(calls, mode):
+    """A Parameter asks for a gradient inside no_grad too; the call there takes widths that only the
+    backward refuses, and keeps nothing for it."""
+    x, w = torch.zeros(4, 16, dtype=BF16), torch.nn.Parameter(torch.zeros(7, 16, dtype=BF16))
+    with mode():
+        y = lce.linear(x, w, activation="gelu")
+    assert y.shape == (4, 7) and not y.requires_grad
+    assert [name for name, _ in calls] == ["forward"] and not calls[0][1][PREACT]
+    with pytest.raises(ValueError, match="multiple of 8"):
+        lce.linear(x, w)
+
+
+def test_residual_alone_keeps_no_preactivation(calls):
+    x, w = torch.zeros(4, 16, dtype=BF16), torch.zeros(7, 16, dtype=BF16)
+    r = torch.zeros(4, 7, dtype=BF16, requires_grad=True)
+    lce.linear(x, w, activation="gelu", residual=r).sum().backward()
+    assert [name for name, _ in calls] == ["forward"] and not calls[0][1][PREACT]
+    assert torch.equal(r.grad, torch.ones_like(r))

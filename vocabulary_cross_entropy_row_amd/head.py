@@ -430,7 +430,7 @@ def _linear_backward(g, ldg, gcode, x, ldx, weight, ldw, preact, ldp, act, n, K,
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, activation):
+    def forward(ctx, x, weight, bias, residual, activation, differentiate):
         _on_gpu(x, "x")
         if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
             raise ValueError("x must have at least one dimension, and weight two")
@@ -441,7 +441,7 @@ class _Linear(torch.autograd.Function):
         shape = (*x.shape[:-1], M)
         if residual is not None and residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
-        wanted = any(ctx.needs_input_grad[:3])
+        wanted = differentiate and any(ctx.needs_input_grad[:3])
         if wanted and M % 8:
             raise ValueError(f"gradients need a weight whose rows are a multiple of 8 (got {M})")
         keep = wanted and _activation(activation) != 0
@@ -478,7 +478,7 @@ def _linear_backward_once(ctx, g):   # on autograd's thread, as _norm_backward_o
             ldx, ldg = _ld(rows), _ld(g2)
         _linear_backward(g2, ldg, LCE_BF16, rows, ldx, weight, _ld(weight), preact, M, ACTIVATIONS[ctx.activation],
                          x.numel() // K, K, M, gx, K, gw, LCE_BF16, gb, bcode, None, _current_stream(x.device.index))
-    return gx, gw, gb, (g if need_r else None), None
+    return gx, gw, gb, (g if need_r else None), None, None
 
 
 _linear_backward_twice = torch.autograd.function.once_differentiable(_linear_backward_once)
@@ -492,7 +492,8 @@ def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
     Captured into a graph, forward and backward belong to one capture, and no graph of the same leaves
     built outside it may be alive: autograd would wait on the stream that one was built on.
     """
-    return _Linear.apply(x, weight, bias, residual, activation)
+    # inside no_grad needs_input_grad still says what the tensors ask for, and inside forward grad is off
+    return _Linear.apply(x, weight, bias, residual, activation, torch.is_grad_enabled())
 
 
 # ---- rules on logits -------------------------------------------------------------------------
