@@ -62,28 +62,27 @@ constexpr uint32_t kListed = 2048;
 template <bool BF16, int BIAS>
 constexpr int vecs_of() { return 8192 / (kThreads * Elt<BF16>::E) / (BIAS == OWN_WORD ? 2 : 1); }
 
-// scale T tanh(x / T).  Near zero an odd polynomial, else (1 - t) / (1 + t) with t = e^{-2 |x| / T} <= 1,
-// whose difference loses 2^-24 T / |x| of itself there.  fp32 logits need all of fp32: five terms up to
-// |x| = T / 4 (the next is below 2^-28 of x); bf16 ones are rounded 2^15 times coarser: two terms up to
-// T / 64 (2^-27), the quotient exact to 2^-18 beyond.  The sweep over the columns issues about as long
-// as it waits for memory, so the scale (1 / temperature) rides in the constants.
+// T tanh(x / T), with v = x / T.  Near zero an odd polynomial in v, else (1 - t) / (1 + t) with
+// t = e^{-2 |v|} <= 1, whose difference loses 2^-24 / |v| of itself there.  fp32 logits need all of fp32:
+// five terms up to |v| = 1 / 4 (the next is below 2^-28 of x); bf16 ones are rounded 2^15 times coarser: two
+// terms up to 1 / 64 (2^-27), the quotient exact to 2^-18 beyond.  Nothing but v overflows, whatever T is, and
+// then t is 0.  (1 / temperature is a factor of its own: in T it overflowed for small temperatures, which
+// made NaN of finite logits.)
 struct Softcap {
-    float c, T, k1, k3, near, u;   // c = -2 log2 e / T
-    __device__ __forceinline__ Softcap(float cap, float scale, bool bf16)
-        : c(-2.0f * dev::kLog2e / cap), T(cap * scale), k1(scale), k3(scale * (-1.0f / 3.0f) / (cap * cap)),
-          near(cap * (bf16 ? 0.015625f : 0.25f)), u(1.0f / cap) {}
+    float T, u;
+    __device__ __forceinline__ explicit Softcap(float cap) : T(cap), u(fminf(1.0f / cap, FLT_MAX)) {}
 };
 template <bool BF16>
 __device__ __forceinline__ float softcapped(float x, const Softcap &s) {
-    const float t = dev::exp2_fast(fabsf(x) * s.c);
+    const float v = x * s.u, v2 = v * v;
+    const float t = dev::exp2_fast(fabsf(v) * (-2.0f * dev::kLog2e));
     const float big = copysignf(fmaf(-s.T, t, s.T) * dev::rcp_fast(1.0f + t), x);
     if constexpr (BF16) {
-        return fabsf(x) < s.near ? x * fmaf(x * x, s.k3, s.k1) : big;
+        return fabsf(v) < 0.015625f ? x * fmaf(v2, -1.0f / 3.0f, 1.0f) : big;
     } else {
-        const float v = x * s.u, u2 = v * v;
         const float p =
-            fmaf(u2, fmaf(u2, fmaf(u2, fmaf(u2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-        return fabsf(x) < s.near ? x * (p * s.k1) : big;
+            fmaf(v2, fmaf(v2, fmaf(v2, fmaf(v2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+        return fabsf(v) < 0.25f ? x * p : big;
     }
 }
 
@@ -232,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
             if constexpr (BIAS) {
                 if (entry) bias = a.bias_values[row * a.ldbv + entry - 1];
             }
-            if (cap > 0.0f) z = softcapped<BF16>(z, Softcap(cap, 1.0f, BF16));
+            if (cap > 0.0f) z = softcapped<BF16>(z, Softcap(cap));
             if constexpr (HIST) {
                 const uint32_t made = (word & ~kPrompt) >> SHIFT;
                 if (made | (word & kPrompt)) z = z > 0.0f ? z / rep : z * rep;
@@ -248,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
     }
 
     const uint32_t hidden = __float_as_uint(a.mask_value);
-    const Softcap capped(cap > 0.0f ? cap : 1.0f, inv_temp, BF16);
+    const Softcap capped(cap > 0.0f ? cap : 1.0f);
 #pragma unroll
     for (int k = 0; k < VECS; ++k) {
         const int local = (k * kThreads + tid) * E;
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
         float o[E];
         if (cap > 0.0f) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = softcapped<BF16>(Elt<BF16>::get(x[k], e), capped);
+            for (int e = 0; e < E; ++e) o[e] = softcapped<BF16>(Elt<BF16>::get(x[k], e), capped) * inv_temp;
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = Elt<BF16>::get(x[k], e) * inv_temp;
