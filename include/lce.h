@@ -357,8 +357,10 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
  * lce_ce_stats reads them.  Matrices are row-major with a row stride in elements;
  * columns past the width are neither read nor written, and any alignment of the
  * element's size works unless a call says otherwise.  An output may be the same
- * buffer as an input of its type, at the same place and stride; other overlap is
- * not allowed.  n == 0 is valid.
+ * buffer as an input matrix of its type and shape, at the same place and stride,
+ * unless a call says otherwise; other overlap is not allowed.  An output in the
+ * place of what all rows read (weight, bias, the rules' lists and values) is
+ * LCE_ERR_INVALID_ARG.  n == 0 is valid.
  */
 
 /*
@@ -500,8 +502,8 @@ size_t lce_linear_workspace_bytes(int64_t n, int64_t K, int64_t M, lce_dtype in_
  *                 M) bytes: dz, and dz, x and weight transposed.  Clobbered; calls
  *                 that share it must not run at the same time.
  * K and M must be multiples of 8, n and M at most 2^23 - 512, and alignments as for
- * lce_linear; grad_x and grad_weight may be in the place of an input.  n == 0 writes
- * zeros to grad_weight and grad_bias.
+ * lce_linear; grad_x and grad_weight may be in the place of an input, grad_bias not
+ * (LCE_ERR_INVALID_ARG).  n == 0 writes zeros to grad_weight and grad_bias.
  */
 lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *x, int64_t ldx,
                                const void *weight, int64_t ldw, const void *preact, int64_t ldp, lce_activation act,

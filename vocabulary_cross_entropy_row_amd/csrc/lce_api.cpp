@@ -528,6 +528,11 @@ lce_status check_matrix(const char *fn, const char *name, const void *p, int64_t
     return LCE_OK;
 }
 
+// An output in the place of an input that every row or tile reads: some would read it overwritten.
+lce_status check_apart(const char *fn, const char *out_name, const void *out, const char *in_name, const void *in) {
+    return out && out == in ? fail(LCE_ERR_INVALID_ARG, "%s: %s must not be %s", fn, out_name, in_name) : LCE_OK;
+}
+
 lce_status check_norm_sizes(const char *fn, int64_t n, int64_t H, lce_dtype dtype, const void *weight,
                             lce_dtype weight_dtype, float weight_offset) {
     if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
@@ -568,6 +573,11 @@ lce_status lce_rms_norm(const void *x, int64_t ldx, lce_dtype dtype, const void 
         return st;
     if (y_dtype == LCE_E4M3 && !scale)
         return fail(LCE_ERR_INVALID_ARG, "%s: scale is required for an e4m3 output", fn);
+    if ((st = check_apart(fn, "y", y, "weight", weight)) != LCE_OK ||
+        (st = check_apart(fn, "sum", sum, "weight", weight)) != LCE_OK ||
+        (st = check_apart(fn, "rstd", rstd, "weight", weight)) != LCE_OK ||
+        (st = check_apart(fn, "scale", y_dtype == LCE_E4M3 ? scale : nullptr, "weight", weight)) != LCE_OK)
+        return st;
     lce::NormArgs a;
     a.x = x;
     a.residual = residual;
@@ -620,6 +630,7 @@ lce_status lce_rms_norm_backward(const void *grad_y, int64_t ldg, const void *s,
             if (!is_aligned(workspace, 16))
                 return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
         }
+        if ((st = check_apart(fn, "grad_x", grad_x, "weight", weight)) != LCE_OK) return st;
     }
     lce::NormGradArgs a;
     a.gy = grad_y;
@@ -692,7 +703,12 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
     if (n > 0x7fffffffLL) return fail(LCE_ERR_UNSUPPORTED, "%s: n > 2^31-1", fn);
     if (n == 0) return ok();
     if ((st = check_matrix(fn, "logits", logits, ldx, V, dtype, true)) != LCE_OK ||
-        (st = check_matrix(fn, "out", out, ldo, V, dtype, true)) != LCE_OK)
+        (st = check_matrix(fn, "out", out, ldo, V, dtype, true)) != LCE_OK ||
+        (st = check_apart(fn, "out", out, "bias_values", bias_values)) != LCE_OK ||
+        (st = check_apart(fn, "out", out, "repetition", repetition)) != LCE_OK ||
+        (st = check_apart(fn, "out", out, "presence", presence)) != LCE_OK ||
+        (st = check_apart(fn, "out", out, "frequency", frequency)) != LCE_OK ||
+        (st = check_apart(fn, "out", out, "temperature", temperature)) != LCE_OK)
         return st;
     lce::RulesArgs a;
     a.logits = logits;
@@ -794,6 +810,9 @@ lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ld
         return fail(LCE_ERR_INVALID_ARG, "%s: out and preact must not be x or weight", fn);
     if (preact && (preact == residual || preact == out))
         return fail(LCE_ERR_INVALID_ARG, "%s: preact must not be residual or out", fn);
+    if ((st = check_apart(fn, "out", out, "bias", bias)) != LCE_OK ||
+        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK)
+        return st;
     lce::LinearArgs a{};
     a.x = x;
     a.weight = weight;
@@ -862,6 +881,11 @@ lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad
         return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
     if (need > 0 && !is_aligned(workspace, 256))
         return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    if ((st = check_apart(fn, "grad_bias", grad_bias, "grad_out", grad_out)) != LCE_OK ||
+        (st = check_apart(fn, "grad_bias", grad_bias, "preact", preact)) != LCE_OK ||
+        (st = check_apart(fn, "grad_bias", grad_bias, "x", x)) != LCE_OK ||
+        (st = check_apart(fn, "grad_bias", grad_bias, "weight", weight)) != LCE_OK)
+        return st;
     lce::LinearGradArgs a{};
     a.grad_out = grad_out;
     a.ldg = ldg;
