@@ -24,16 +24,19 @@ def _call_stream(fn):
     """Runs a binding function with its call stream and device current; the function receives the
     stream's handle as ``stream``.  The common call -- no stream named, tensors of the current
     device -- switches nothing."""
+    name = fn.__code__.co_varnames[0]   # of the operand whose device it is, which may come by name
+
     @functools.wraps(fn)
-    def wrapper(first, *args, stream=None, **kw):
+    def wrapper(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not (isinstance(first, torch.Tensor) and first.is_cuda):
-            return fn(first, *args, stream=0, **kw)   # the function's own checks raise
+            return fn(*args, stream=0, **kw)   # the function's own checks raise
         device = first.device
         if stream is None and device.index == torch.cuda.current_device():
-            return fn(first, *args, stream=_current_stream(device.index), **kw)
+            return fn(*args, stream=_current_stream(device.index), **kw)
         st = _torch_stream(stream, device)
         with torch.cuda.device(device), torch.cuda.stream(st):
-            return fn(first, *args, stream=st.cuda_stream, **kw)
+            return fn(*args, stream=st.cuda_stream, **kw)
     return wrapper
 
 
