@@ -205,11 +205,11 @@ def _on_gpu(t, name: str):
 
 
 def _buf(t, name: str, dtype, numel: int, device, required: bool = False) -> None:
-    import torch
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
         return
+    import torch
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:

@@ -12,7 +12,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import LCE_BF16, LCE_E4M3, LCE_F32, _check, _on_gpu, _ptr, _torch_stream, lib
+from . import LCE_BF16, LCE_E4M3, LCE_F32, _buf, _check, _on_gpu, _ptr, _torch_stream, lib
 
 _CODES = {torch.float32: LCE_F32, torch.bfloat16: LCE_BF16, torch.float8_e4m3fn: LCE_E4M3}
 # The current stream's handle, without the stream object around it (3 us of a 10 us call).
@@ -65,22 +65,6 @@ def _rows(t, name: str, dtype, n: int, width: int, device, required: bool = Fals
     if column != 1 and width > 1:
         raise ValueError(f"{name} must have unit column stride")
     return row if n > 1 else width
-
-
-def _buf(t, name: str, dtype, numel: int, device, required: bool = False) -> None:
-    """Checks a contiguous buffer of at least ``numel`` values."""
-    if t is None:
-        if required:
-            raise ValueError(f"{name} is required")
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{name} needs at least {numel} contiguous elements (got {list(t.shape)}, strides {t.stride()})")
 
 
 # ---- root-mean-square norm -------------------------------------------------------------------
