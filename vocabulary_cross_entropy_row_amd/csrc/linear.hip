@@ -51,7 +51,7 @@ constexpr int64_t kLastCache = int64_t(256) << 20;   // bytes of the cache in fr
 template <class S>
 hipError_t launch_shape(const linear::Args &g, bool fp8, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(g.per_xcd) * 8u), block(64 * S::NW);
-    const bool tail = g.kbytes % S::STEP != 0;
+    const bool tail = g.kbytes % linear::kStep != 0;
     if (fp8) {
         if (tail) hipLaunchKernelGGL((linear::linear_kernel<S, true, true>), grid, block, 0, st, g);
         else hipLaunchKernelGGL((linear::linear_kernel<S, true, false>), grid, block, 0, st, g);

@@ -40,8 +40,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "ce_device.h"
 #include "head_internal.h"
 
@@ -93,8 +91,7 @@ struct Args {
 
 // LDS position of chunk c of row r is c ^ swz(r): the 16 rows that one LDS cycle serves for a fragment
 // read (consecutive rows, one chunk) land on 16 distinct 16-byte groups of the 256-byte bank window.
-template <int CPR>   // chunks per row
-__device__ __forceinline__ int swz(int r) { return (r / (16 / CPR)) & (CPR - 1); }
+__device__ __forceinline__ int swz(int r) { return (r / 2) & 7; }
 
 // A buffer descriptor built from wave-uniform values, so it lives in SGPRs.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
@@ -291,21 +288,24 @@ __device__ __forceinline__ void finish(const Epi &e, const Cols &c, int64_t t0, 
     }
 }
 
-// One tile shape: BF x BT by WF x WT waves, SA steps of w and SB of x in LDS, STEP bytes of each row.
-template <int BF_, int BT_, int WF_, int WT_, int SA_, int SB_, int STEP_ = 128>
+constexpr int kStep = 128;                    // bytes of K per row and step
+constexpr int kChunks = kStep / 16;           // 16-byte chunks in them
+constexpr int kLoadRows = 1024 / kStep;       // rows that a wave's load of 1 KB takes
+
+// One tile shape: BF x BT by WF x WT waves, SA steps of w and SB of x in LDS.
+template <int BF_, int BT_, int WF_, int WT_, int SA_, int SB_>
 struct Shape {
-    static constexpr int BF = BF_, BT = BT_, WF = WF_, WT = WT_, SA = SA_, SB = SB_, STEP = STEP_;
-    static constexpr int CPR = STEP / 16, RPL = 1024 / STEP;        // chunks per row, rows per 1 KB load
+    static constexpr int BF = BF_, BT = BT_, WF = WF_, WT = WT_, SA = SA_, SB = SB_;
     static constexpr int NW = WF * WT;
     static constexpr int FI = BF / WF / 32, TJ = BT / WT / 32;      // 32 x 32 tiles per wave
-    static constexpr int LA = BF / RPL / NW, LB = BT / RPL / NW;    // 1 KB loads per wave and step
-    static constexpr int A_BYTES = BF * STEP, B_BYTES = BT * STEP;
+    static constexpr int LA = BF / kLoadRows / NW, LB = BT / kLoadRows / NW;   // 1 KB loads per wave and step
+    static constexpr int A_BYTES = BF * kStep, B_BYTES = BT * kStep;
     static constexpr int OUT_LD = FI * 32 + 4;                      // floats per token of a wave's epilogue tile
     static constexpr int LOOP_LDS = SA * A_BYTES + SB * B_BYTES;
     static constexpr int OUT_LDS = NW * 32 * OUT_LD * 4;
     static constexpr int LDS = LOOP_LDS > OUT_LDS ? LOOP_LDS : OUT_LDS;
     static constexpr int PER_CU = 160 * 1024 / LDS < 8 / NW ? 160 * 1024 / LDS : (8 / NW > 0 ? 8 / NW : 1);
-    static_assert(FI >= 1 && TJ >= 1 && LA * RPL * NW == BF && LB * RPL * NW == BT && LDS <= 160 * 1024, "tile shape");
+    static_assert(FI >= 1 && TJ >= 1 && LA * kLoadRows * NW == BF && LB * kLoadRows * NW == BT && LDS <= 160 * 1024, "tile shape");
     static_assert((SA == SB || SA == SB + 1) && SB >= 2, "steps in flight");
 };
 
@@ -343,8 +343,8 @@ template <class S, bool FP8, bool KTAIL>
 __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kernel(Args g) {
     using F = Frag<FP8>;
     using frag = typename F::type;
-    constexpr int FI = S::FI, TJ = S::TJ, KK = S::STEP / F::BYTES, LA = S::LA, LB = S::LB, SA = S::SA, SB = S::SB;
-    constexpr int STEP = S::STEP, CPR = S::CPR, RPL = S::RPL;
+    constexpr int FI = S::FI, TJ = S::TJ, KK = kStep / F::BYTES, LA = S::LA, LB = S::LB, SA = S::SA, SB = S::SB;
+    static_assert(KK % 2 == 0, "a step's first sub-step is always in the first fragment set");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[S::LDS];
 
     // Workgroups are dealt round robin over the 8 XCDs; each XCD walks a contiguous range of the
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
     const int gt = min(GROUP, g.tiles_t - first_t);
     const int within = mn - first_t * g.tiles_f;
     const int t0 = (first_t + within % gt) * S::BT, f0 = within / gt * S::BF;
-    const int steps_total = (g.kbytes + STEP - 1) / STEP;
+    const int steps_total = (g.kbytes + kStep - 1) / kStep;
     const int kbeg = static_cast<int>(static_cast<int64_t>(steps_total) * ks / g.splits);
     const int kend = static_cast<int>(static_cast<int64_t>(steps_total) * (ks + 1) / g.splits);
     const int nsteps = kend - kbeg;
@@ -375,30 +375,30 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
     const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(
         g.x + static_cast<int64_t>(t0) * g.ldx, static_cast<uint32_t>((tr - 1) * g.ldx + g.kbytes));
 
-    // this wave's loads: RPL rows x STEP bytes each, lane -> row lane / CPR, position lane % CPR
+    // this wave's loads: kLoadRows rows of kStep bytes each, lane -> row lane / kChunks, position lane % kChunks
     constexpr int kMaxLoads = 8;
     static_assert(LA <= kMaxLoads && LB <= kMaxLoads, "load slots");
     uint32_t voffA[kMaxLoads], voffB[kMaxLoads];
-    const int lrow = lane / CPR, lpos = lane % CPR;
-    // byte of K the lane's chunk starts at: with eight chunks a row, load blocks alternate between two
+    const int lrow = lane / kChunks, lpos = lane % kChunks;
+    // byte of K the lane's chunk starts at: load blocks alternate between two
     int kb[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) kb[p] = (lpos ^ swz<CPR>(p * RPL + lrow)) * 16;
+    for (int p = 0; p < 2; ++p) kb[p] = (lpos ^ swz(p * kLoadRows + lrow)) * 16;
 #pragma unroll
     for (int j = 0; j < LA; ++j) {
-        const int r = (j * S::NW + wave) * RPL + lrow;
-        voffA[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.ldw) + (lpos ^ swz<CPR>(r)) * 16u;
+        const int r = (j * S::NW + wave) * kLoadRows + lrow;
+        voffA[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.ldw) + (lpos ^ swz(r)) * 16u;
     }
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
-        const int r = (j * S::NW + wave) * RPL + lrow;
-        voffB[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.ldx) + (lpos ^ swz<CPR>(r)) * 16u;
+        const int r = (j * S::NW + wave) * kLoadRows + lrow;
+        voffB[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.ldx) + (lpos ^ swz(r)) * 16u;
     }
     auto load_a = [&](int step, int slot_a) {
 #pragma unroll
         for (int j = 0; j < LA; ++j) {
             unsigned char *dst = lds + slot_a * S::A_BYTES + (j * S::NW + wave) * 1024;
-            const int k0 = step * STEP;
+            const int k0 = step * kStep;
             if constexpr (KTAIL) {
                 const uint32_t v = k0 + kb[(j * S::NW + wave) & 1] >= g.kbytes ? kOutside : voffA[j] + k0;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, v, 0, 0, 0);
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
 #pragma unroll
         for (int j = 0; j < LB; ++j) {
             unsigned char *dst = lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (j * S::NW + wave) * 1024;
-            const int k0 = step * STEP;
+            const int k0 = step * kStep;
             if constexpr (KTAIL) {
                 const uint32_t v = k0 + kb[(j * S::NW + wave) & 1] >= g.kbytes ? kOutside : voffB[j] + k0;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, v, 0, 0, 0);
@@ -425,12 +425,12 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
 #pragma unroll
         for (int i = 0; i < FI; ++i) {
             const int r = (wf * FI + i) * 32 + (lane & 31);
-            af[i] = F::load(At + r * STEP, swz<CPR>(r), kk, half);
+            af[i] = F::load(At + r * kStep, swz(r), kk, half);
         }
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
             const int r = (wt * TJ + j) * 32 + (lane & 31);
-            bf[j] = F::load(Bt + r * STEP, swz<CPR>(r), kk, half);
+            bf[j] = F::load(Bt + r * kStep, swz(r), kk, half);
         }
     };
     // Spread the next sub-step's LDS reads, and in sub-step 0 the loads, between the MFMAs.
@@ -476,13 +476,11 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
     // settle the scalar loads so the LDS waits inside the loop count precisely
     __builtin_amdgcn_s_waitcnt(0xC07F);
     int sa = 0, sb = 0;   // slots of step s
-    // FIRST: which of the two fragment sets holds the step's first sub-step
-    auto one_step = [&](int s, auto first) {
-        constexpr int FIRST = decltype(first)::value;
+    auto one_step = [&](int s) {
         const int na = sa + 1 == SA ? 0 : sa + 1, nb = sb + 1 == SB ? 0 : sb + 1;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            const bool odd = (FIRST + kk) & 1;
+            const bool odd = kk & 1;
             frag *ac = odd ? a1 : a0, *bc = odd ? b1 : b0;
             frag *an = odd ? a0 : a1, *bn = odd ? b0 : b1;
             __builtin_amdgcn_sched_barrier(0);
@@ -511,14 +509,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void linear_kern
         sa = na;
         sb = nb;
     };
-    if constexpr (KK % 2 == 0) {
-        for (int s = 0; s < nsteps; ++s) one_step(s, std::integral_constant<int, 0>{});
-    } else {
-        for (int s = 0; s < nsteps; s += 2) {
-            one_step(s, std::integral_constant<int, 0>{});
-            if (s + 1 < nsteps) one_step(s + 1, std::integral_constant<int, 1>{});
-        }
-    }
+    for (int s = 0; s < nsteps; ++s) one_step(s);
 
     // epilogue: a wave's own LDS region, 32 tokens at a time
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
