@@ -472,9 +472,9 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
  *   workspace     device, 16-byte aligned, lce_linear_workspace_bytes(...) bytes;
  *                 may be NULL where that is 0.  Clobbered; calls that share it must
  *                 not run at the same time.
- * n and M are any size; K, ldx and ldw must be whole 16 bytes and x and weight
- * 16-byte aligned (LCE_ERR_UNSUPPORTED otherwise); the other operands may lie
- * anywhere their type may.  out and preact must not be x or weight, nor preact residual
+ * n and M are below 2^23; K, ldx and ldw must be whole 16 bytes, ldx and ldw at most
+ * 16 MiB - 1 KB, and x and weight 16-byte aligned (LCE_ERR_UNSUPPORTED otherwise); the
+ * other operands may lie anywhere their type may.  out and preact must not be x or weight, nor preact residual
  * or out (LCE_ERR_INVALID_ARG).  The same inputs give the same bits.  n == 0 is valid.
  */
 lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ldw, lce_dtype in_dtype,

@@ -38,3 +38,21 @@ def test_grad_out_rows_far_apart(n, K, M, ld):
     xl, wl = x.clone().requires_grad_(), w.clone().requires_grad_()
     gx, gw = torch.autograd.grad(lce.linear(xl, wl), (xl, wl), far)
     assert torch.equal(gx, want.grad_x) and torch.equal(gw, want.grad_weight)
+
+
+def test_last_tokens_of_long_sequences():
+    """x's rows 32 MiB apart: the product and its gradients as from a contiguous copy."""
+    B, T, K, M = 3, 4097, 4096, 264
+    g = torch.Generator(device=DEV).manual_seed(1)
+    hidden = torch.zeros(B, T, K, device=DEV, dtype=BF16)
+    hidden[:, -1] = torch.randn(B, K, generator=g, device=DEV).to(BF16)
+    w = (torch.randn(M, K, generator=g, device=DEV) / 64).to(BF16).requires_grad_()
+    c = torch.randn(B, M, generator=g, device=DEV).to(BF16)
+    near = hidden[:, -1].contiguous().requires_grad_()
+    want = lce.linear(near, w, activation="silu")
+    x = hidden[:, -1].requires_grad_()
+    assert x.stride(0) * 2 > 1 << 24
+    got = lce.linear(x, w, activation="silu")
+    assert torch.equal(got, want)
+    for a, b in zip(torch.autograd.grad(got, (x, w), c), torch.autograd.grad(want, (near, w), c)):
+        assert torch.equal(a, b)

@@ -77,3 +77,14 @@ def test_residual_alone_keeps_no_preactivation(calls):
     lce.linear(x, w, activation="gelu", residual=r).sum().backward()
     assert [name for name, _ in calls] == ["forward"] and not calls[0][1][PREACT]
     assert torch.equal(r.grad, torch.ones_like(r))
+
+
+def test_rows_far_apart_are_copied(calls):
+    """As the last tokens of long sequences are: the library reads rows up to 16 MiB - 1 KB apart."""
+    LDX, LDX_BACKWARD = 1, 4
+    w = torch.zeros(8, 16, dtype=BF16)
+    for ld, taken in (((1 << 23) - 512, (1 << 23) - 512), ((1 << 23) - 504, 16), (1 << 24, 16)):
+        x = torch.empty(ld + 16, dtype=BF16)[:1].as_strided((2, 16), (ld, 1)).requires_grad_()
+        lce.linear(x, w).backward(torch.zeros(2, 8, dtype=BF16))
+        assert calls[-2][1][LDX] == calls[-1][1][LDX_BACKWARD] == taken
+        assert x.grad.shape == (2, 16)

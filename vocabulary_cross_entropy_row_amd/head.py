@@ -272,6 +272,15 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
 
 # ---- matrix product with an epilogue ---------------------------------------------------------
 
+_MAX_LD = (1 << 23) - 512   # elements between the rows of a bf16 operand, as the product reads them
+
+
+def _operand_rows(x, K: int):
+    """x's rows as the product reads them; copied where they lie too far apart."""
+    rows = _rows_of(x, K)
+    return rows.contiguous() if _ld(rows) > _MAX_LD else rows
+
+
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
@@ -433,7 +442,7 @@ class _Linear(torch.autograd.Function):
             raise ValueError(f"gradients need a weight whose rows are a multiple of 8 (got {M})")
         keep = wanted and _activation(activation) != 0
         out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        preact = lce_linear(_rows_of(x, x.shape[-1]), weight, bias=bias, activation=activation,
+        preact = lce_linear(_operand_rows(x, x.shape[-1]), weight, bias=bias, activation=activation,
                             residual=None if residual is None else _rows_of(residual, M), want_preact=keep,
                             out=_rows_of(out, M)).preact
         ctx.save_for_backward(x, weight, preact)
@@ -461,7 +470,7 @@ def _linear_backward_once(ctx, g):   # on autograd's thread, as _norm_backward_o
             bcode = _CODES[ctx.bias_dtype]
         rows, g2, ldx, ldg = x, g, K, M
         if not (x.is_contiguous() and g.is_contiguous()):
-            rows, g2 = _rows_of(x, K), _rows_of(g, M)
+            rows, g2 = _operand_rows(x, K), _rows_of(g, M)
             ldx, ldg = _ld(rows), _ld(g2)
         _linear_backward(g2, ldg, LCE_BF16, rows, ldx, weight, _ld(weight), preact, M, ACTIVATIONS[ctx.activation],
                          x.numel() // K, K, M, gx, K, gw, LCE_BF16, gb, bcode, None, _current_stream(x.device.index))
