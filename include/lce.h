@@ -61,6 +61,8 @@ typedef enum {
     LCE_ACT_GELU_TANH = 3,   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
     LCE_ACT_SILU = 4         /* z / (1 + e^-z) */
 } lce_activation;
+/* Their own arithmetic, and that of their slopes, is off by at most 2^-20 (|z| + 1): more than an fp32
+ * step where act(z) is small (GELU at -3: 5e-5 of the value; past -5, where it is under 2e-6, 0.2 to 2%). */
 
 /*
  * Bytes of device workspace lce_ce_fwd_bwd needs for n rows of V columns
@@ -370,7 +372,8 @@ lce_status lce_flce_backward(const void *hidden, const void *weight, const int64
  *   y_ij   = s_ij rstd_i (weight_j + weight_offset)
  * with y taken from the rounded s, the rows a later reader and the backward see.
  * With y_dtype LCE_E4M3, y holds e4m3(y_ij / scale_i) and scale_i = max_j |y_ij| /
- * 448 (1 for a row of zeros, at least 2^-126).  Sums are fp32.  A row that holds
+ * 448 (1 for a row of zeros, at least 2^-126); the division is a multiplication by
+ * the rounded 1 / scale_i.  Sums are fp32.  A row that holds
  * an infinity or a NaN gives what that arithmetic gives, in that row alone.
  *   x, residual   device, dtype F32 or BF16; residual may be NULL.
  *   weight        device [H] F32 or BF16, or NULL (ones, offset not added).
@@ -419,7 +422,8 @@ lce_status lce_rms_norm_backward(const void *grad_y, int64_t ldg, const void *s,
  *   z = seen ? (z > 0 ? z / repetition_i : z repetition_i) : z
  *   z = c > 0 ? z - frequency_i c - presence_i : z
  *   z = z + the last bias_values entry of row i whose id is j, if there is one
- *   z = temperature_i > 0 ? z / temperature_i : z
+ *   z = temperature_i > 0 ? z / temperature_i : z   (times the rounded reciprocal;
+ *                                                     below 2^-128 it counts as 2^-128)
  *   out_ij = j allowed for row i ? z : mask_value
  *   logits, out     device [n, ldx] / [n, ldo], dtype F32 or BF16; may be the same.
  *   history         device token ids [n, L], row stride ldh (0: one list for all
@@ -466,9 +470,11 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
  *   residual      device [n, ldr], out_dtype, or NULL; may be `out` itself.
  *   out           device [n, ldo], out_dtype: BF16, or F32 with BF16 operands.  (The
  *                 8-bit matrix instructions cut each group of eight products to
- *                 2^-13 of its largest before the fp32 sum: far below a bf16
- *                 rounding, not an fp32 result.)
- *   preact        device BF16 [n, ldp], or NULL: z, for lce_linear_backward.
+ *                 2^-13 of its largest before the fp32 sum: 2^4 finer than a bf16
+ *                 rounding of products that size, but not of an output in which such
+ *                 products cancel.)
+ *   preact        device BF16 [n, ldp], or NULL: z rounded, for lce_linear_backward,
+ *                 which takes the activation's slope there.
  *   workspace     device, 16-byte aligned, lce_linear_workspace_bytes(...) bytes;
  *                 may be NULL where that is 0.  Clobbered; calls that share it must
  *                 not run at the same time.

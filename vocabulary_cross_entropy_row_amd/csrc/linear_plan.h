@@ -18,8 +18,9 @@ enum { BIG, WIDE, LOW, TINY, ROWS16, ROWS32, SHAPES };   // ROWS: linear_rows_ke
 // workgroup's start and end, the launch, and what its tile moves at (bytes per us); for a product split
 // along K the second launch and the rate of the partial sums.  Fitted to the times of each shape, with
 // 1 to 16 splits, over 208 random bf16 products (n 1 to 4096, K 256 to 8192, M 256 to 202048) and 112
-// e4m3 ones: off by 10 to 14% (root mean square); the choice that the estimates make is 3% slower than
-// the fastest measured one on geometric average.
+// e4m3 ones, before outputs above 256 MB were streamed: on those products off by 10 to 14% (root mean
+// square), and the choice that the estimates make 3% slower than the fastest measured one on geometric
+// average.  They have not been held against other products.
 struct Cost {
     double step[3], tile, launch, rate, fold, fold_rate;
 };

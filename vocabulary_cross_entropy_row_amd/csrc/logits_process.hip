@@ -148,6 +148,8 @@ __global__ __launch_bounds__(kThreads) void logits_process_kernel(RulesArgs a, u
         const int64_t r = a.mask_rows ? a.mask_rows[row] : row;
         if (r >= 0 && r < a.R) words = a.allowed + r * a.ldm;
     }
+    // A factor in place of a division, ten instructions a logit: one rounding more (2^-24 of a value that bf16
+    // rounds to 2^-9; fp32 logits with every rule are off by 4e-8 on the whole, 2.5e-8 with divisions).
     const float inv_temp = temp > 0.0f ? fminf(1.0f / temp, FLT_MAX) : 1.0f;   // finite, so that 0 stays 0
     // mask bits of columns c .. c + E - 1: they lie in one word or two (those before the row or past V do
     // not matter)

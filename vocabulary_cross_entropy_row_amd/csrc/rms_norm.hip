@@ -14,11 +14,13 @@
 // Both are bound by memory: every value is read once and written once, so a row
 // lives in the registers of LPR lanes (16 to 1024) between its load and its
 // stores, K accesses of 16 bytes (E values) per lane.  gfx950 takes those at any
-// address, so odd widths and strides run like aligned ones; only an access that
-// reaches past the row's end goes value by value.  8192 x 6656 bf16 with a residual:
-// forward 74 to 78 us (5.6 to 5.9 TB/s), backward 92 to 98 us (4.5 to 4.7 TB/s) and
-// 5 us for the partial rows of dL/dw; 4096 x 8192 to 8 bits 42 to 44 us (5.3 to 5.6
-// TB/s).  A large copy reaches 4.9 TB/s.  Sums are fp32: within a lane in
+// address; only an access that reaches past the row's end goes value by value.
+// 8192 x 6656 bf16 with a residual: forward 73 to 78 us (5.6 to 6.0 TB/s), backward
+// 92 to 98 us (4.5 to 4.7 TB/s) and 5 us for the partial rows of dL/dw; 4096 x 8192 to
+// 8 bits 42 to 44 us (5.3 to 5.6 TB/s).  A large copy reaches 4.9 TB/s.  Rows off the
+// 16-byte boundaries cost more (a row stride of 6657: 91 and 119 us), and so does a cut
+// last access, in bf16 most of all: 8192 x 6655 in rows of 6656 105 and 266 us, packed
+// 123 and 294; fp32 157 and 183, 150 and 164 at 6656.  Sums are fp32: within a lane in
 // column order, then across lanes in a fixed order, so results repeat bit for bit.
 #include <hip/hip_runtime.h>
 #include <algorithm>
@@ -251,7 +253,10 @@ __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_kernel(NormArgs a) {
 // keeps its part of dL/dw in registers, one fp32 sum per column.  The next row's
 // values are requested before this row is reduced and stored.  They wait as
 // loaded, not widened, so that sixteen waves fit a CU: 8192 x 6656 bf16 takes
-// 136 us with widened rows, no request ahead and twelve waves.
+// 136 us with widened rows, no request ahead and twelve waves.  With TAIL and two
+// accesses a lane the value-by-value branches of every operand take more registers
+// than that leaves: bf16 129 of them with a wave a row (twelve waves a CU) and 182
+// with 512 lanes (eight); with 1024 lanes 44 are spilled, and 50 of fp32's four accesses.
 template <bool BF16, int LPR, int K, bool TAIL>   // TAIL: the last access of a row reaches past its end
 __global__ __launch_bounds__(threads_of(LPR)) void rms_norm_backward_kernel(NormGradArgs a) {
     constexpr int E = Elt<BF16>::E, ROWS = threads_of(LPR) / LPR;
@@ -425,7 +430,8 @@ void pick_fwd(const NormArgs &a, hipStream_t st) {
 template <bool BF16, int LPR, int K>
 int64_t launch_bwd(const NormGradArgs &a, hipStream_t st) {
     constexpr int ROWS = threads_of(LPR) / LPR;
-    // sixteen waves on every compute unit: all groups run at once, and few partial rows
+    // Sixteen waves on every compute unit, and few partial rows.  Without TAIL all groups run at once; where
+    // a kernel's registers leave fewer waves the rest of the groups follow.
     const int64_t most = std::min<int64_t>(kNormMaxGroups, static_cast<int64_t>(device_cu_count()) * (1024 / threads_of(LPR)));
     const int64_t groups = std::min((a.n + ROWS - 1) / ROWS, most);
     const dim3 grid(static_cast<unsigned>(groups)), block(threads_of(LPR));
