@@ -56,3 +56,12 @@ def test_last_tokens_of_long_sequences():
     assert torch.equal(got, want)
     for a, b in zip(torch.autograd.grad(got, (x, w), c), torch.autograd.grad(want, (near, w), c)):
         assert torch.equal(a, b)
+
+
+def test_a_parameter_of_odd_width_without_gradients():
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(9, 128, generator=g, device=DEV).to(BF16)
+    w = torch.nn.Parameter((torch.randn(1003, 128, generator=g, device=DEV) / 8).to(BF16))
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(lce.linear(x, w, activation="gelu"), lce.lce_linear(x, w.detach(), activation="gelu").out)

@@ -18,11 +18,11 @@
 // residual, pre-activation and output move 16 bytes at a time.
 //
 // 256 x 256 tiles, 1024 x 6656 x 202048 bf16: 2.2 ms, 1.25 PFLOP/s with the matrix
-// units busy 71% of the time at the 1.5 to 1.7 GHz that their power leaves (all-zero
+// units busy 71% of the time at the 1.4 to 1.7 GHz that their power leaves (all-zero
 // operands run 1.4 times as fast); the library product of 8192 to 16384 cubed reaches
 // 1.42 to 1.55.  A step of K takes 1.5 us and a tile's start and end 8 to 10, half of
 // that stores, which nothing overlaps.  e4m3, 4096 x 8192 x 8192: 245 us, 2.2 PFLOP/s,
-// matrix units busy 47% at 2.1 GHz; the waves wait for operands (a row stride of 8192
+// matrix units busy 47 to 54% at 2.0 to 2.1 GHz; the waves wait for operands (a row stride of 8192
 // bytes costs 8% of that; five tiles of 64 bytes in flight instead of 2.5 of 128 gain
 // nothing).
 //
