@@ -483,7 +483,8 @@ _linear_backward_twice = torch.autograd.function.once_differentiable(_linear_bac
 def linear(x, weight, bias=None, *, activation: str = "none", residual=None):
     """Autograd form of the product over the last dimension of ``x``: act(x weight^T + bias) + residual,
     all of x, weight and residual bfloat16 (bias bfloat16 or float32), the output bfloat16 with x's
-    leading dimensions.  Gradients have their inputs' types; sums are fp32.
+    leading dimensions.  Gradients have their inputs' types; sums are fp32.  Where x, weight or bias asks
+    for one, weight must have a multiple of 8 rows.
 
     Captured into a graph, forward and backward belong to one capture, and no graph of the same leaves
     built outside it may be alive: autograd would wait on the stream that one was built on.
