@@ -50,7 +50,8 @@ typedef enum {
 } lce_status;
 
 /* LCE_E4M3 (8-bit floats, 4 exponent and 3 mantissa bits, largest 448): only where a call names it. */
-typedef enum { LCE_F32 = 0, LCE_BF16 = 1, LCE_E4M3 = 2 } lce_dtype;
+/* LCE_E8M0 (a power of two as its exponent plus 127 in a byte, 255 NaN): only as the type of scales. */
+typedef enum { LCE_F32 = 0, LCE_BF16 = 1, LCE_E4M3 = 2, LCE_E8M0 = 3 } lce_dtype;
 
 typedef enum { LCE_RED_NONE = 0, LCE_RED_MEAN = 1, LCE_RED_SUM = 2 } lce_reduction;
 
@@ -518,6 +519,101 @@ lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad
                                size_t workspace_bytes, hipStream_t stream);
 
 size_t lce_linear_backward_workspace_bytes(int64_t n, int64_t K, int64_t M);
+
+/*
+ * ---- 8-bit products with a scale for each block of 128, and the orthogonalised update ----
+ *
+ * A matrix [rows, K] in e4m3 is cut along K into blocks of 128 values, the last one
+ * shorter, with a scale for each: of one row (LCE_BLOCKS_ROW, scales [rows,
+ * ceil(K / 128)]) or of 128 rows (LCE_BLOCKS_TILE, scales [ceil(rows / 128),
+ * ceil(K / 128)]).  Scale (i, b) lies s_row i + s_col b elements from the first.
+ */
+typedef enum { LCE_BLOCKS_ROW = 0, LCE_BLOCKS_TILE = 1 } lce_blocks;
+
+/*
+ * Quantises x into such blocks, and / or its transpose into blocks of its own:
+ *   scale = the smallest power of two with max|x| <= 448 scale over the block (1 where
+ *           all are 0, at least 2^-126)
+ *   value = e4m3(x / scale), exact but for the one rounding
+ * A block that holds an infinity or a NaN has a NaN for its scale and its values, and
+ * no other block changes.
+ *   x         device [n, ldx], dtype F32 or BF16.
+ *   values    device e4m3 [n, ldv], blocks as `blocks` says, or NULL: not wanted.
+ *   scale     device, scale_dtype LCE_E8M0 or LCE_F32 (the same powers of two),
+ *             strides s_row and s_col.
+ *   values_t  device e4m3 [K, ldvt] of the transpose, or NULL, with blocks_t, scale_t
+ *             [K or ceil(K / 128), ceil(n / 128)] and its strides.
+ * Columns past the width are not written.  n and K are at least 0 and 1; the blocks
+ * of 128 x 128 number fewer than 2^24 (LCE_ERR_UNSUPPORTED otherwise).  Outputs must
+ * not be x or one another (LCE_ERR_INVALID_ARG).  n == 0 is valid.
+ */
+lce_status lce_quantize_blocks(const void *x, int64_t ldx, lce_dtype dtype, int64_t n, int64_t K, void *values,
+                               int64_t ldv, lce_blocks blocks, void *scale, int64_t s_row, int64_t s_col,
+                               void *values_t, int64_t ldvt, lce_blocks blocks_t, void *scale_t, int64_t st_row,
+                               int64_t st_col, lce_dtype scale_dtype, hipStream_t stream);
+
+/*
+ * Matrix product of such operands, x in row blocks and weight in tiles:
+ *   z_if   = sum_b scale_x[i, b] scale_w[f / 128, b] sum_{k in b} x_ik weight_fk + bias_f
+ *   out_if = act(z_if) + residual_if
+ * The block sums are taken by the 8-bit matrix instructions (which cut their products
+ * as lce_linear says), all else in fp32, and each output is rounded to bf16 once.
+ *   x, weight     device e4m3 [n, ldx], [M, ldw].
+ *   scale_x       device, LCE_F32 (any numbers) or LCE_E8M0, strides sx_row, sx_col.
+ *   scale_w       the same for weight, sw_row per 128 rows.  Scales that are e8m0 on
+ *                 both sides are applied by the matrix instructions.
+ *   bias          device [M] F32 or BF16, or NULL.
+ *   residual      device bf16 [n, ldr], or NULL; may be `out` itself.
+ *   out           device bf16 [n, ldo].
+ *   preact        device bf16 [n, ldp], or NULL: z rounded.
+ *   workspace     device, 16-byte aligned, lce_linear_blocks_workspace_bytes(...)
+ *                 bytes; may be NULL where that is 0.  Clobbered; calls that share it
+ *                 must not run at the same time.
+ * n and M are below 2^23; ldx and ldw must be multiples of 16 and at most 16 MiB - 1 KB,
+ * x and weight 16-byte aligned (LCE_ERR_UNSUPPORTED otherwise); K may be any, and what
+ * a row holds past it does not matter.  out and preact must not be x, weight or a
+ * scale, nor preact residual or out (LCE_ERR_INVALID_ARG).  The same inputs give the
+ * same bits.  n == 0 is valid.
+ */
+lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, int64_t sx_row, int64_t sx_col,
+                             lce_dtype scale_x_dtype, const void *weight, int64_t ldw, const void *scale_w,
+                             int64_t sw_row, int64_t sw_col, lce_dtype scale_w_dtype, const void *bias,
+                             lce_dtype bias_dtype, lce_activation act, const void *residual, int64_t ldr, int64_t n,
+                             int64_t K, int64_t M, void *out, int64_t ldo, void *preact, int64_t ldp, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+size_t lce_linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M);
+
+/*
+ * Backward of a product whose operands were quantised from x [n, K] (row blocks) and
+ * weight [M, K] (tiles), straight through their rounding.  With Q the quantiser in row
+ * blocks (e8m0 scales):
+ *   grad_x = Q(grad_out) weight,  grad_weight = Q(grad_out^T) x,
+ *   grad_bias = column sums of grad_out (not quantised)
+ * where weight and x are what their 8-bit forms stand for.
+ *   grad_out      device [n, ldg] BF16 or F32 (grad_dtype).
+ *   xt, scale_xt  x transposed, e4m3 [K, ldxt] in tiles with e8m0 scales, as
+ *                 lce_quantize_blocks gives them (values_t, scale_t); read for
+ *                 grad_weight, else may be NULL.
+ *   wt, scale_wt  weight transposed, e4m3 [K, ldwt] in tiles; read for grad_x.
+ *   grad_x        device bf16 [n, ldgx], or NULL.
+ *   grad_weight   device bf16 [M, K] contiguous, or NULL; overwritten.
+ *   grad_bias     device [M] BF16 or F32 (grad_bias_dtype), or NULL; overwritten.
+ *   workspace     device, 256-byte aligned, lce_linear_blocks_backward_workspace_bytes(
+ *                 n, K, M) bytes.  Clobbered; calls that share it must not run at the
+ *                 same time.
+ * Sizes and alignments as for lce_linear_blocks, K below 2^23, n and M at most 2^23 -
+ * 1024 and fewer than 2^24 blocks in grad_out.  Outputs must not be an operand
+ * (LCE_ERR_INVALID_ARG).  n == 0 writes zeros to grad_weight and grad_bias.
+ */
+lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *xt,
+                                      int64_t ldxt, const void *scale_xt, int64_t sxt_row, int64_t sxt_col,
+                                      const void *wt, int64_t ldwt, const void *scale_wt, int64_t swt_row,
+                                      int64_t swt_col, int64_t n, int64_t K, int64_t M, void *grad_x, int64_t ldgx,
+                                      void *grad_weight, void *grad_bias, lce_dtype grad_bias_dtype, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t M);
 
 /*
  * Text of the most recent error on the calling thread ("" if none).  Valid

@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblce.so")
 
 LCE_OK, LCE_ERR_INVALID_ARG, LCE_ERR_UNSUPPORTED, LCE_ERR_HIP = 0, 1, 2, 3
-LCE_F32, LCE_BF16, LCE_E4M3 = 0, 1, 2
+LCE_F32, LCE_BF16, LCE_E4M3, LCE_E8M0 = 0, 1, 2, 3
 LCE_RED_NONE, LCE_RED_MEAN, LCE_RED_SUM = 0, 1, 2
 REDUCTIONS = {"none": LCE_RED_NONE, "mean": LCE_RED_MEAN, "sum": LCE_RED_SUM}
 ABI_VERSION = 3
@@ -101,6 +101,18 @@ def lib() -> ctypes.CDLL:
                                       p]
     L.lce_linear_backward_workspace_bytes.restype = sz
     L.lce_linear_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lce_quantize_blocks.restype = ci
+    L.lce_quantize_blocks.argtypes = [p, i64, ci, i64, i64, p, i64, ci, p, i64, i64, p, i64, ci, p, i64, i64, ci, p]
+    L.lce_linear_blocks.restype = ci
+    L.lce_linear_blocks.argtypes = [p, i64, p, i64, i64, ci, p, i64, p, i64, i64, ci, p, ci, ci, p, i64, i64, i64, i64, p,
+                                    i64, p, i64, p, sz, p]
+    L.lce_linear_blocks_workspace_bytes.restype = sz
+    L.lce_linear_blocks_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lce_linear_blocks_backward.restype = ci
+    L.lce_linear_blocks_backward.argtypes = [p, i64, ci, p, i64, p, i64, i64, p, i64, p, i64, i64, i64, i64, i64, p, i64, p,
+                                             p, ci, p, sz, p]
+    L.lce_linear_blocks_backward_workspace_bytes.restype = sz
+    L.lce_linear_blocks_backward_workspace_bytes.argtypes = [i64, i64, i64]
     if L.lce_abi_version() != ABI_VERSION:
         raise ImportError("liblce.so ABI version mismatch; rebuild it")
     _lib = L
@@ -694,11 +706,17 @@ def _deferred_flce_class():
 _DeferredFLCE = _LazyFunction(_deferred_flce_class)
 
 
-# The operators around the cross-entropy.  head.py imports torch, so it is loaded on first use.
+# The operators around the cross-entropy, and the 8-bit products.  head.py and products.py import torch,
+# so they are loaded on first use.
 _HEAD = frozenset((
     "ACTIVATIONS", "LinearGrads", "LinearResult", "NormResult", "lce_linear", "lce_linear_backward",
     "lce_linear_backward_workspace_bytes", "lce_linear_workspace_bytes", "lce_logits_process", "lce_rms_norm",
     "lce_rms_norm_backward", "lce_rms_norm_workspace_bytes", "linear", "rms_norm"))
+
+_PRODUCTS = frozenset((
+    "BLOCKS", "BlocksResult", "lce_linear_blocks", "lce_linear_blocks_backward",
+    "lce_linear_blocks_backward_workspace_bytes", "lce_linear_blocks_workspace_bytes", "lce_quantize_blocks",
+    "linear_blocks"))
 
 
 def __getattr__(name):
@@ -706,8 +724,12 @@ def __getattr__(name):
         from . import head
         value = globals()[name] = getattr(head, name)
         return value
+    if name in _PRODUCTS:
+        from . import products
+        value = globals()[name] = getattr(products, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted(set(globals()) | _HEAD)
+    return sorted(set(globals()) | _HEAD | _PRODUCTS)

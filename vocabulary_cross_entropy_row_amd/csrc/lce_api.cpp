@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "blocks_internal.h"
 #include "head_internal.h"
 #include "lce_internal.h"
 
@@ -908,6 +909,230 @@ lce_status lce_linear_backward(const void *grad_out, int64_t ldg, lce_dtype grad
     a.grad_bias_bf16 = grad_bias_dtype == LCE_BF16;
     a.workspace = workspace;
     return hip_status(lce::launch_linear_backward(a, stream), "lce_linear_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Strides of a [rows, cols] array of scales, no two at one place where it is written.
+lce_status check_scale(const char *fn, const char *name, const void *p, int64_t s_row, int64_t s_col, int64_t rows,
+                       int64_t cols, lce_dtype dtype, bool written) {
+    if (dtype != LCE_F32 && dtype != LCE_E8M0)
+        return fail(LCE_ERR_INVALID_ARG, "%s: %s must be fp32 or e8m0 (got dtype %d)", fn, name, (int)dtype);
+    if (!p) return fail(LCE_ERR_INVALID_ARG, "%s: %s is required", fn, name);
+    if (s_row < 0 || s_col < 0) return fail(LCE_ERR_INVALID_ARG, "%s: the strides of %s must be >= 0", fn, name);
+    if (s_row > INT64_MAX / 8 / rows || s_col > INT64_MAX / 8 / cols)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the strides of %s are too large", fn, name);
+    const bool by_row = (cols <= 1 || s_col >= 1) && (rows <= 1 || s_row >= (cols - 1) * s_col + 1);
+    const bool by_col = (rows <= 1 || s_row >= 1) && (cols <= 1 || s_col >= (rows - 1) * s_row + 1);
+    if (written && !by_row && !by_col)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the strides of %s (%lld, %lld) put two scales at one place", fn, name,
+                    (long long)s_row, (long long)s_col);
+    if (dtype == LCE_F32 && !is_aligned(p, 4)) return fail(LCE_ERR_INVALID_ARG, "%s: %s must be 4-byte aligned", fn, name);
+    return LCE_OK;
+}
+
+// An e4m3 matrix as the product reads it.
+lce_status check_blocked(const char *fn, const char *name, const void *p, int64_t ld, int64_t K) {
+    if (!p) return fail(LCE_ERR_INVALID_ARG, "%s: %s is required", fn, name);
+    if (ld < K)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the row stride of %s (%lld) must be >= %lld", fn, name, (long long)ld, (long long)K);
+    if (ld % 16 || !is_aligned(p, 16))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: %s must be 16-byte aligned with a row stride of whole 16 bytes", fn, name);
+    if (ld > lce::kLinearMaxStride)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: 256 rows of %s exceed 4 GiB", fn, name);
+    return LCE_OK;
+}
+
+lce_status check_blocks_sizes(const char *fn, int64_t n, int64_t K, int64_t M) {
+    if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
+    if (K < 1) return fail(LCE_ERR_INVALID_ARG, "%s: K must be >= 1 (got %lld)", fn, (long long)K);
+    if (M < 1) return fail(LCE_ERR_INVALID_ARG, "%s: M must be >= 1 (got %lld)", fn, (long long)M);
+    if (n > 0x7fffffffLL / 256 || M > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: n or M >= 2^23", fn);
+    return LCE_OK;
+}
+
+// whether 128 x 128 blocks of [n, K] number fewer than 2^24
+bool few_blocks(int64_t n, int64_t K) {
+    const int64_t rows = n / 128 + 1, cols = K / 128 + 1;
+    return rows < (int64_t(1) << 24) && cols < (int64_t(1) << 24) && rows * cols < (int64_t(1) << 24);
+}
+
+}  // namespace
+
+extern "C" {
+
+lce_status lce_quantize_blocks(const void *x, int64_t ldx, lce_dtype dtype, int64_t n, int64_t K, void *values,
+                               int64_t ldv, lce_blocks blocks, void *scale, int64_t s_row, int64_t s_col,
+                               void *values_t, int64_t ldvt, lce_blocks blocks_t, void *scale_t, int64_t st_row,
+                               int64_t st_col, lce_dtype scale_dtype, hipStream_t stream) {
+    const char *fn = "lce_quantize_blocks";
+    if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
+    if (K < 1) return fail(LCE_ERR_INVALID_ARG, "%s: K must be >= 1 (got %lld)", fn, (long long)K);
+    if (!f32_or_bf16(dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    for (int b : {(int)blocks, (int)blocks_t})
+        if (b != LCE_BLOCKS_ROW && b != LCE_BLOCKS_TILE) return fail(LCE_ERR_INVALID_ARG, "%s: unknown blocks %d", fn, b);
+    if (!few_blocks(n, K)) return fail(LCE_ERR_UNSUPPORTED, "%s: 2^24 or more blocks of 128 x 128", fn);
+    if (n == 0) return ok();
+    if (!values && !values_t) return fail(LCE_ERR_INVALID_ARG, "%s: values or values_t is required", fn);
+    const int64_t bn = (n + 127) / 128, bk = (K + 127) / 128;
+    lce_status st;
+    if ((st = check_matrix(fn, "x", x, ldx, K, dtype, true)) != LCE_OK ||
+        (st = check_matrix(fn, "values", values, ldv, K, LCE_E4M3, false)) != LCE_OK ||
+        (st = check_matrix(fn, "values_t", values_t, ldvt, n, LCE_E4M3, false)) != LCE_OK)
+        return st;
+    if (values && (st = check_scale(fn, "scale", scale, s_row, s_col, blocks == LCE_BLOCKS_TILE ? bn : n, bk, scale_dtype, true)) != LCE_OK)
+        return st;
+    if (values_t && (st = check_scale(fn, "scale_t", scale_t, st_row, st_col, blocks_t == LCE_BLOCKS_TILE ? bk : K, bn, scale_dtype, true)) != LCE_OK)
+        return st;
+    const void *outs[4] = {values, values ? scale : nullptr, values_t, values_t ? scale_t : nullptr};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return fail(LCE_ERR_INVALID_ARG, "%s: two outputs are the same buffer", fn);
+    for (const void *o : outs)
+        if (o == x) return fail(LCE_ERR_INVALID_ARG, "%s: an output must not be x", fn);
+    lce::QuantizeArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.n = n;
+    a.K = K;
+    const bool e8m0 = scale_dtype == LCE_E8M0;
+    a.q = {static_cast<unsigned char *>(values), ldv, scale, s_row, s_col, blocks == LCE_BLOCKS_TILE, e8m0};
+    a.qt = {static_cast<unsigned char *>(values_t), ldvt, scale_t, st_row, st_col, blocks_t == LCE_BLOCKS_TILE, e8m0};
+    return hip_status(lce::launch_quantize_blocks(a, dtype == LCE_BF16, stream), "lce_quantize_blocks launch");
+}
+
+size_t lce_linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M) {
+    if (n < 0 || K < 1 || M < 1) return 0;
+    return lce::linear_blocks_workspace_bytes(n, K, M);
+}
+
+lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, int64_t sx_row, int64_t sx_col,
+                             lce_dtype scale_x_dtype, const void *weight, int64_t ldw, const void *scale_w,
+                             int64_t sw_row, int64_t sw_col, lce_dtype scale_w_dtype, const void *bias,
+                             lce_dtype bias_dtype, lce_activation act, const void *residual, int64_t ldr, int64_t n,
+                             int64_t K, int64_t M, void *out, int64_t ldo, void *preact, int64_t ldp, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+    const char *fn = "lce_linear_blocks";
+    lce_status st = check_blocks_sizes(fn, n, K, M);
+    if (st != LCE_OK) return st;
+    if (act < LCE_ACT_NONE || act > LCE_ACT_SILU) return fail(LCE_ERR_INVALID_ARG, "%s: unknown activation %d", fn, act);
+    if (bias && !f32_or_bf16(bias_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown bias dtype %d", fn, (int)bias_dtype);
+    if (bias && !is_aligned(bias, dtype_bytes(bias_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: bias must be %zu-byte aligned", fn, dtype_bytes(bias_dtype));
+    if (n == 0) return ok();
+    const int64_t bk = (K + 127) / 128;
+    if ((st = check_blocked(fn, "x", x, ldx, K)) != LCE_OK || (st = check_blocked(fn, "weight", weight, ldw, K)) != LCE_OK ||
+        (st = check_scale(fn, "scale_x", scale_x, sx_row, sx_col, n, bk, scale_x_dtype, false)) != LCE_OK ||
+        (st = check_scale(fn, "scale_w", scale_w, sw_row, sw_col, (M + 127) / 128, bk, scale_w_dtype, false)) != LCE_OK ||
+        (st = check_matrix(fn, "residual", residual, ldr, M, LCE_BF16, false)) != LCE_OK ||
+        (st = check_matrix(fn, "out", out, ldo, M, LCE_BF16, true)) != LCE_OK ||
+        (st = check_matrix(fn, "preact", preact, ldp, M, LCE_BF16, false)) != LCE_OK)
+        return st;
+    const size_t need = lce::linear_blocks_workspace_bytes(n, K, M);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (need > 0 && !is_aligned(workspace, 16))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    for (const void *o : {static_cast<const void *>(out), static_cast<const void *>(preact)})
+        if (o && (o == x || o == weight || o == scale_x || o == scale_w))
+            return fail(LCE_ERR_INVALID_ARG, "%s: out and preact must not be x, weight or a scale", fn);
+    if (preact && (preact == residual || preact == out))
+        return fail(LCE_ERR_INVALID_ARG, "%s: preact must not be residual or out", fn);
+    if ((st = check_apart(fn, "out", out, "bias", bias)) != LCE_OK ||
+        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK)
+        return st;
+    lce::BlocksArgs a{};
+    a.x = x;
+    a.weight = weight;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.n = n;
+    a.K = K;
+    a.M = M;
+    a.sx = {scale_x, sx_row, sx_col, scale_x_dtype == LCE_E8M0};
+    a.sw = {scale_w, sw_row, sw_col, scale_w_dtype == LCE_E8M0};
+    a.bias = bias;
+    a.bias_bf16 = bias_dtype == LCE_BF16;
+    a.act = act;
+    a.residual = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    a.preact = preact;
+    a.ldp = ldp;
+    a.part = static_cast<float *>(workspace);
+    return hip_status(lce::launch_linear_blocks(a, stream), "lce_linear_blocks launch");
+}
+
+size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
+    if (n < 0 || K < 1 || M < 1) return 0;
+    return lce::linear_blocks_backward_workspace_bytes(n, K, M);
+}
+
+lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *xt,
+                                      int64_t ldxt, const void *scale_xt, int64_t sxt_row, int64_t sxt_col,
+                                      const void *wt, int64_t ldwt, const void *scale_wt, int64_t swt_row,
+                                      int64_t swt_col, int64_t n, int64_t K, int64_t M, void *grad_x, int64_t ldgx,
+                                      void *grad_weight, void *grad_bias, lce_dtype grad_bias_dtype, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream) {
+    const char *fn = "lce_linear_blocks_backward";
+    lce_status st = check_blocks_sizes(fn, n, K, M);
+    if (st != LCE_OK) return st;
+    if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
+    if (n > (1 << 23) - 1024 || M > (1 << 23) - 1024)   // row lengths of what the products read
+        return fail(LCE_ERR_UNSUPPORTED, "%s: n and M must be <= 2^23 - 1024 (got %lld, %lld)", fn, (long long)n, (long long)M);
+    if (!few_blocks(n, M)) return fail(LCE_ERR_UNSUPPORTED, "%s: 2^24 or more blocks of 128 x 128 in grad_out", fn);
+    if (!f32_or_bf16(grad_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_out dtype %d", fn, (int)grad_dtype);
+    if (grad_bias && !f32_or_bf16(grad_bias_dtype))
+        return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_bias dtype %d", fn, (int)grad_bias_dtype);
+    const int64_t bn = (n + 127) / 128, bk = (K + 127) / 128, bm = (M + 127) / 128;
+    if (n > 0) {
+        if ((st = check_matrix(fn, "grad_out", grad_out, ldg, M, grad_dtype, true)) != LCE_OK ||
+            (st = check_matrix(fn, "grad_x", grad_x, ldgx, K, LCE_BF16, false)) != LCE_OK)
+            return st;
+        if (grad_weight && ((st = check_blocked(fn, "xt", xt, ldxt, n)) != LCE_OK ||
+                            (st = check_scale(fn, "scale_xt", scale_xt, sxt_row, sxt_col, bk, bn, LCE_E8M0, false)) != LCE_OK))
+            return st;
+        if (grad_x && ((st = check_blocked(fn, "wt", wt, ldwt, M)) != LCE_OK ||
+                       (st = check_scale(fn, "scale_wt", scale_wt, swt_row, swt_col, bk, bm, LCE_E8M0, false)) != LCE_OK))
+            return st;
+    }
+    if (grad_weight && !is_aligned(grad_weight, 2))
+        return fail(LCE_ERR_INVALID_ARG, "%s: grad_weight must be 2-byte aligned", fn);
+    if (grad_bias && !is_aligned(grad_bias, dtype_bytes(grad_bias_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: grad_bias must be %zu-byte aligned", fn, dtype_bytes(grad_bias_dtype));
+    const size_t need = lce::linear_blocks_backward_workspace_bytes(n, K, M);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (need > 0 && !is_aligned(workspace, 256))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    const void *ins[5] = {grad_out, xt, scale_xt, wt, scale_wt};
+    const void *outs[3] = {grad_x, grad_weight, grad_bias};
+    for (const void *o : outs)
+        for (const void *i : ins)
+            if (o && o == i) return fail(LCE_ERR_INVALID_ARG, "%s: an output must not be an operand", fn);
+    lce::BlocksGradArgs a{};
+    a.grad_out = grad_out;
+    a.ldg = ldg;
+    a.grad_bf16 = grad_dtype == LCE_BF16;
+    a.xt = xt;
+    a.ldxt = ldxt;
+    a.sxt = {scale_xt, sxt_row, sxt_col, true};
+    a.wt = wt;
+    a.ldwt = ldwt;
+    a.swt = {scale_wt, swt_row, swt_col, true};
+    a.n = n;
+    a.K = K;
+    a.M = M;
+    a.grad_x = grad_x;
+    a.ldgx = ldgx;
+    a.grad_weight = grad_weight;
+    a.grad_bias = grad_bias;
+    a.grad_bias_bf16 = grad_bias_dtype == LCE_BF16;
+    a.workspace = workspace;
+    return hip_status(lce::launch_linear_blocks_backward(a, stream), "lce_linear_blocks_backward launch");
 }
 
 }  // extern "C"

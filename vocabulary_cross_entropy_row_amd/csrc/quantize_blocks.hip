@@ -1,0 +1,211 @@
+// Quantiser into blocks of 128:
+//   s_b = the smallest power of two with max |x| <= 448 s_b over block b (1 where that is 0, at least
+//         2^-126; NaN where the block holds an infinity or a NaN)
+//   q   = e4m3(x / s_b)
+// of a matrix and / or of its transpose, each in row blocks (1 x 128) or tiles (128 x 128).
+//
+// A power of two makes the division exact, so each value is rounded once and the same in any arithmetic,
+// and the scale is a byte that the matrix instruction applies by itself.  With max = m 2^E, 1 <= m < 2,
+// and 448 = 1.75 2^8 the exponent is E - 8, or E - 7 where m > 1.75: integer work on the bits.  The
+// largest magnitude is taken as the integer maximum of the bits without sign, which orders NaN above
+// infinity above every number.
+//
+// A workgroup takes 128 x 128 values, so x is read once whatever is asked for.  A thread holds 8 x 8
+// of them: a row's 128 lie in 16 neighbouring lanes, a column's in 16 lanes of four waves, and the eight
+// rows of a column make eight neighbouring bytes of the transpose, which goes out through LDS in whole
+// 128-byte rows.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "blocks_internal.h"
+#include "ce_device.h"
+#include "linear_mfma.h"
+
+namespace lce {
+namespace {
+
+using dev::Elt;
+using dev::u32x4;
+
+constexpr uint32_t kMinExponent = 1;   // 2^-126
+
+// exponent byte of the scale for the bits of the largest magnitude
+__device__ __forceinline__ uint32_t scale_exponent(uint32_t bits) {
+    if (bits >= 0x7f800000u) return 255u;   // an infinity or a NaN
+    if (bits == 0u) return 127u;
+    const uint32_t e = (bits >> 23) + ((bits & 0x7fffffu) > 0x600000u ? 1u : 0u);   // biased exponent of 2^8 s
+    return e > 8u + kMinExponent ? e - 8u : kMinExponent;
+}
+// 1 / s, as x / s = x (1 / s): exact
+__device__ __forceinline__ float inverse_scale(uint32_t e) {
+    return e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - e) << 23);
+}
+__device__ __forceinline__ void put_scale(const BlockedOut &o, int64_t i, int64_t j, uint32_t e) {
+    const int64_t at = i * o.s_row + j * o.s_col;
+    if (o.e8m0) static_cast<unsigned char *>(o.scale)[at] = static_cast<unsigned char>(e);
+    else static_cast<float *>(o.scale)[at] = e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+}
+// four values as e4m3; the conversion saturates nothing that a scale leaves (|v| <= 448) and keeps NaN
+__device__ __forceinline__ uint32_t four(float a, float b, float c, float d) {
+    int v = 0;
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, v, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+    return static_cast<uint32_t>(v);
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// the largest of 16 neighbouring lanes
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
+    m = umax(m, static_cast<uint32_t>(dev::dpp_i<dev::kDppXor1>(static_cast<int>(m))));
+    m = umax(m, static_cast<uint32_t>(dev::dpp_i<dev::kDppXor2>(static_cast<int>(m))));
+    m = umax(m, static_cast<uint32_t>(dev::dpp_i<dev::kDppHalfMirror>(static_cast<int>(m))));
+    return umax(m, static_cast<uint32_t>(dev::dpp_i<dev::kDppMirror>(static_cast<int>(m))));
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a, int tiles_c) {
+    __shared__ __attribute__((aligned(16))) unsigned char flat[128 * 128];   // the transpose: 16-byte chunk c of row r at c ^ (r / 8 mod 8)
+    __shared__ uint32_t col_max[4][128];
+    __shared__ float col_sum[4][128];
+    __shared__ uint32_t wave_max[4];
+    const int tile = blockIdx.x, br = tile / tiles_c, bc = tile - br * tiles_c;
+    const int64_t r0 = br * 128ll, c0 = bc * 128ll;
+    const int t = threadIdx.x, ch = t & 15, g = t >> 4, lane = t & 63, wave = t >> 6;
+    const int64_t gr = r0 + g * 8, gc = c0 + ch * 8;
+    float v[8][8];   // rows gr .. gr + 7, columns gc .. gc + 7
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = gr + i;
+        if (row < a.n && gc + 8 <= a.K) {
+            if constexpr (BF16) {
+                const u32x4 q = *reinterpret_cast<const linear::any16 *>(static_cast<const uint16_t *>(a.x) + row * a.ldx + gc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = Elt<true>::get(q, e);
+            } else {
+                const linear::any16 *q = reinterpret_cast<const linear::any16 *>(static_cast<const float *>(a.x) + row * a.ldx + gc);
+                const u32x4 p = q[0], s = q[1];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = Elt<false>::get(e < 4 ? p : s, e & 3);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[i][e] = row < a.n && gc + e < a.K ? Elt<BF16>::load_one(a.x, row * a.ldx + gc + e) : 0.0f;
+        }
+    }
+    uint32_t rmax[8], cmax[8], all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rmax[i] = cmax[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(v[i][e]) & 0x7fffffffu;
+            rmax[i] = umax(rmax[i], b);
+            cmax[e] = umax(cmax[e], b);
+        }
+    const bool want_tile = (a.q.values && a.q.tile) || (a.qt.values && a.qt.tile);
+    if (want_tile) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = umax(all, rmax[i]);
+        all = row16_max(all);
+        all = umax(all, static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 16)));
+        all = umax(all, static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 32)));
+        if (lane == 0) wave_max[wave] = all;
+    }
+    if (a.qt.values && !a.qt.tile) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t c = cmax[e];
+            c = umax(c, static_cast<uint32_t>(__shfl_xor(static_cast<int>(c), 16)));
+            c = umax(c, static_cast<uint32_t>(__shfl_xor(static_cast<int>(c), 32)));
+            if (lane < 16) col_max[wave][ch * 8 + e] = c;
+        }
+    }
+    if (a.part) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float c = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c += v[i][e];
+            c += __shfl_xor(c, 16);
+            c += __shfl_xor(c, 32);
+            if (lane < 16) col_sum[wave][ch * 8 + e] = c;
+        }
+    }
+    __syncthreads();
+    uint32_t tile_e = 0;
+    if (want_tile) {
+        all = umax(umax(wave_max[0], wave_max[1]), umax(wave_max[2], wave_max[3]));
+        tile_e = scale_exponent(all);
+        if (t == 0 && a.q.values && a.q.tile) put_scale(a.q, br, bc, tile_e);
+        if (t == 0 && a.qt.values && a.qt.tile) put_scale(a.qt, bc, br, tile_e);
+    }
+    if (a.part && t < 128 && c0 + t < a.K)
+        a.part[br * a.K + c0 + t] = (col_sum[0][t] + col_sum[1][t]) + (col_sum[2][t] + col_sum[3][t]);
+    if (a.q.values) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t e = tile_e;
+            if (!a.q.tile) {
+                e = scale_exponent(row16_max(rmax[i]));
+                if (ch == 0 && gr + i < a.n) put_scale(a.q, gr + i, bc, e);
+            }
+            const float inv = inverse_scale(e);
+            const uint32_t lo = four(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            const uint32_t hi = four(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+            if (gr + i >= a.n) continue;
+            unsigned char *o = a.q.values + (gr + i) * a.q.ld + gc;
+            if (gc + 8 <= a.K && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+                *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int e8 = 0; e8 < 8; ++e8)
+                    if (gc + e8 < a.K) o[e8] = static_cast<unsigned char>((e8 < 4 ? lo : hi) >> (8 * (e8 & 3)));
+            }
+        }
+    }
+    if (!a.qt.values) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int c = ch * 8 + e;
+        uint32_t ex = tile_e;
+        if (!a.qt.tile) {
+            ex = scale_exponent(umax(umax(col_max[0][c], col_max[1][c]), umax(col_max[2][c], col_max[3][c])));
+            if (g == 0 && c0 + c < a.K) put_scale(a.qt, c0 + c, br, ex);
+        }
+        const float inv = inverse_scale(ex);
+        const uint2 w = make_uint2(four(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv),
+                                   four(v[4][e] * inv, v[5][e] * inv, v[6][e] * inv, v[7][e] * inv));
+        *reinterpret_cast<uint2 *>(flat + c * 128 + (((g >> 1) ^ (ch & 7)) * 16) + (g & 1) * 8) = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const int idx = t + h * 256, c = idx >> 3, chunk = idx & 7;
+        const int64_t row = c0 + c, col = r0 + chunk * 16;
+        if (row >= a.K || col >= a.n) continue;
+        const u32x4 q = *reinterpret_cast<const u32x4 *>(flat + c * 128 + ((chunk ^ ((c >> 3) & 7)) * 16));
+        unsigned char *o = a.qt.values + row * a.qt.ld + col;
+        if (col + 16 <= a.n && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            *reinterpret_cast<u32x4 *>(o) = q;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (col + e < a.n) o[e] = static_cast<unsigned char>(q[e >> 2] >> (8 * (e & 3)));
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_blocks(const QuantizeArgs &a, bool is_bf16, hipStream_t st) {
+    if (a.n <= 0 || a.K <= 0) return hipSuccess;
+    const int64_t tr = (a.n + 127) / 128, tc = (a.K + 127) / 128;
+    if (tr * tc >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(tr * tc)), block(256);
+    if (is_bf16) hipLaunchKernelGGL((quantize_kernel<true>), grid, block, 0, st, a, static_cast<int>(tc));
+    else hipLaunchKernelGGL((quantize_kernel<false>), grid, block, 0, st, a, static_cast<int>(tc));
+    return hipGetLastError();
+}
+
+}  // namespace lce
