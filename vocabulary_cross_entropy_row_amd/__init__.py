@@ -113,6 +113,10 @@ def lib() -> ctypes.CDLL:
                                              p, ci, p, sz, p]
     L.lce_linear_blocks_backward_workspace_bytes.restype = sz
     L.lce_linear_blocks_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lce_orthogonalise.restype = ci
+    L.lce_orthogonalise.argtypes = [p, i64, i64, ci, i64, i64, i64, ci, f32, f32, f32, f32, p, i64, i64, p, sz, p]
+    L.lce_orthogonalise_workspace_bytes.restype = sz
+    L.lce_orthogonalise_workspace_bytes.argtypes = [i64, i64, i64]
     if L.lce_abi_version() != ABI_VERSION:
         raise ImportError("liblce.so ABI version mismatch; rebuild it")
     _lib = L
@@ -715,8 +719,8 @@ _HEAD = frozenset((
 
 _PRODUCTS = frozenset((
     "BLOCKS", "BlocksResult", "lce_linear_blocks", "lce_linear_blocks_backward",
-    "lce_linear_blocks_backward_workspace_bytes", "lce_linear_blocks_workspace_bytes", "lce_quantize_blocks",
-    "linear_blocks"))
+    "lce_linear_blocks_backward_workspace_bytes", "lce_linear_blocks_workspace_bytes", "lce_orthogonalise",
+    "lce_orthogonalise_workspace_bytes", "lce_quantize_blocks", "linear_blocks"))
 
 
 def __getattr__(name):

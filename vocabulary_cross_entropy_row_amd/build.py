@@ -30,6 +30,7 @@ HALF_FAMILIES = [5, 6, 7, 8, 9, 10]
 UNITS = [("ce_kernels.hip", [], "ce_kernels"), ("flce.hip", [], "flce"), ("ce_split.hip", [], "ce_split"),
          ("rms_norm.hip", [], "rms_norm"), ("logits_process.hip", [], "logits_process"), ("linear.hip", [], "linear"),
          ("quantize_blocks.hip", [], "quantize_blocks"), ("linear_blocks.hip", [], "linear_blocks"),
+         ("orthogonalise.hip", [], "orthogonalise"),
          ("lce_api.cpp", ["-x", "hip"], "lce_api")] + [
     ("ce_rows_inst.hip", [f"-DLCE_BF16={b}", f"-DLCE_KR={kr}", f"-DLCE_KL={kl}", "-DLCE_UA=0"], f"ce_rows_{b}_{kr}_{kl}")
     for b in (1, 0) for kr, kl in FAMILIES] + [

@@ -1136,3 +1136,80 @@ lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dty
 }
 
 }  // extern "C"
+
+namespace {
+
+// Sizes of the orthogonalised update: 256 rows of what its products read below 4 GiB, launches below 2^32
+// threads.
+lce_status check_ortho(const char *fn, int64_t batch, int64_t rows, int64_t cols) {
+    if (batch < 0) return fail(LCE_ERR_INVALID_ARG, "%s: batch must be >= 0 (got %lld)", fn, (long long)batch);
+    if (rows < 1 || cols < 1)
+        return fail(LCE_ERR_INVALID_ARG, "%s: rows and cols must be >= 1 (got %lld, %lld)", fn, (long long)rows, (long long)cols);
+    if (rows > (1 << 20) || cols > (1 << 20) || batch > 65535)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: rows and cols must be <= 2^20, batch <= 65535", fn);
+    // tiles of 64 x 64 at most: of X, and of A
+    const int64_t r = (rows < cols ? rows : cols) / 64 + 1, c = (rows < cols ? cols : rows) / 64 + 1;
+    if (r * c >= (int64_t(1) << 23) || batch * r * c >= (int64_t(1) << 23))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: 2^23 or more tiles of 64 x 64", fn);
+    return LCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lce_orthogonalise_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    if (check_ortho("lce_orthogonalise_workspace_bytes", batch, rows, cols) != LCE_OK) return 0;
+    return lce::orthogonalise_workspace_bytes(batch, rows, cols);
+}
+
+lce_status lce_orthogonalise(const void *g, int64_t ldg, int64_t g_batch_stride, lce_dtype dtype, int64_t batch,
+                             int64_t rows, int64_t cols, int steps, float a, float b, float c, float eps, void *out,
+                             int64_t ldo, int64_t out_batch_stride, void *workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    const char *fn = "lce_orthogonalise";
+    lce_status st = check_ortho(fn, batch, rows, cols);
+    if (st != LCE_OK) return st;
+    if (!f32_or_bf16(dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    if (steps < 1 || steps > 100) return fail(LCE_ERR_INVALID_ARG, "%s: steps must be 1 to 100 (got %d)", fn, steps);
+    if (!isfinite(a) || !isfinite(b) || !isfinite(c))
+        return fail(LCE_ERR_INVALID_ARG, "%s: the coefficients must be finite (got %g, %g, %g)", fn, (double)a, (double)b, (double)c);
+    if (!(eps >= 0.0f) || isinf(eps))
+        return fail(LCE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0 (got %g)", fn, (double)eps);
+    if (batch == 0) return ok();
+    if ((st = check_matrix(fn, "g", g, ldg, cols, dtype, true)) != LCE_OK ||
+        (st = check_matrix(fn, "out", out, ldo, cols, LCE_BF16, true)) != LCE_OK)
+        return st;
+    if (batch > 1 && g_batch_stride < 0)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the batch stride of g must be >= 0", fn);
+    const bool apart = out_batch_stride >= (rows - 1) * ldo + cols ||
+                       (out_batch_stride >= cols && ldo >= (batch - 1) * out_batch_stride + cols);
+    if (batch > 1 && !apart)
+        return fail(LCE_ERR_INVALID_ARG, "%s: the batch stride of out (%lld) makes matrices overlap", fn, (long long)out_batch_stride);
+    if ((st = check_apart(fn, "out", out, "g", g)) != LCE_OK) return st;
+    const size_t need = lce::orthogonalise_workspace_bytes(batch, rows, cols);
+    if (!workspace || workspace_bytes < need)
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (!is_aligned(workspace, 256))
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    lce::OrthoArgs o{};
+    o.g = g;
+    o.ldg = ldg;
+    o.batch_stride = g_batch_stride;
+    o.batch = batch;
+    o.rows = rows;
+    o.cols = cols;
+    o.g_bf16 = dtype == LCE_BF16;
+    o.out = out;
+    o.ldo = ldo;
+    o.out_batch_stride = out_batch_stride;
+    o.steps = steps;
+    o.a = a;
+    o.b = b;
+    o.c = c;
+    o.eps = eps;
+    o.workspace = workspace;
+    return hip_status(lce::launch_orthogonalise(o, stream), "lce_orthogonalise launch");
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
-"""8-bit products with a scale for each block of 128: the quantiser, the product, and the product's
-training form.
+"""8-bit products with a scale for each block of 128 (the quantiser, the product, the product's training
+form), and the orthogonalised update of a weight.
 
 Argument marshalling for the C entry points of the same names (include/lce.h), in the manner of head.py.
 """
@@ -325,3 +325,53 @@ def linear_blocks(x, weight, bias=None, *, residual=None):
     Under capture, what ``linear`` says of it holds here too.
     """
     return _LinearBlocks.apply(x, weight, bias, residual, torch.is_grad_enabled())
+
+
+# ---- orthogonalised update -------------------------------------------------------------------
+
+def lce_orthogonalise_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(lib().lce_orthogonalise_workspace_bytes(int(batch), int(rows), int(cols)))
+
+
+def _matrices(t, name: str, dtype, shape, device):
+    """Checks a [batch, rows, cols] or [rows, cols] operand; returns (row stride, batch stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return (t.stride(-2) if rows > 1 else cols), (t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else 0)
+
+
+@_call_stream
+def lce_orthogonalise(g, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None,
+                      workspace=None, stream=None):
+    """The orthogonalised update of a matrix ``g`` [rows, cols], or of each of a batch [batch, rows, cols]
+    (bfloat16 or float32, unit column stride): X = g / (its norm + eps), then ``steps`` times
+    X <- a X + (b A + c A A) X with A = X X^T (X^T X of a matrix taller than wide) and ``coefficients``
+    (a, b, c).  Returns bfloat16 of g's shape, ``out`` if it is given."""
+    dev = _on_gpu(g, "g")
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g must be [rows, cols] or [batch, rows, cols] (got {list(g.shape)})")
+    a, b, c = (float(v) for v in coefficients)
+    code = _float_code(g, "g")
+    ldg, batch_stride = _matrices(g, "g", g.dtype, g.shape, dev)
+    batch, (rows, cols) = (g.shape[0] if g.dim() == 3 else 1), g.shape[-2:]
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    ldo, out_stride = _matrices(out, "out", torch.bfloat16, g.shape, dev)
+    need = lib().lce_orthogonalise_workspace_bytes(batch, rows, cols)
+    if workspace is not None:
+        _buf(workspace, "workspace", torch.uint8, need, dev)
+    elif need:   # clobbered by the call
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().lce_orthogonalise(g.data_ptr(), ldg, batch_stride, code, batch, rows, cols, int(steps), a, b, c, float(eps),
+                                   out.data_ptr(), ldo, out_stride, _ptr(workspace),
+                                   0 if workspace is None else workspace.numel(), stream))
+    return out
