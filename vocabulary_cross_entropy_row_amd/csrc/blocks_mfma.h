@@ -62,17 +62,23 @@ __device__ __forceinline__ int load_scale(const Scales &s, int64_t at) {
     return static_cast<const int *>(s.p)[at];
 }
 
+// the block's product, added to acc where the scales are powers of two
 template <bool POW2>
 __device__ __forceinline__ f4v block_product(i32x8 a, i32x8 b, f4v acc, int sa, int sb) {
     if constexpr (POW2) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, sa, 0, sb);
-    const f4v t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, (f4v){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-    const float s = __int_as_float(sb);   // both scales
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, (f4v){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+}
+// Holds a value to its place in the order of the code: what forms it comes before, and volatile
+// statements, LDS reads among them, stay on their sides.  (The matrix instructions have no place of their
+// own, and the compiler puts every LDS read of a step ahead of the first of them.)
+__device__ __forceinline__ void pin(f4v &v) { asm volatile("" : "+v"(v)::"memory"); }
+__device__ __forceinline__ f4v scaled_sum(f4v t, float s, f4v acc) {
     return (f4v){fmaf(t.x, s, acc.x), fmaf(t.y, s, acc.y), fmaf(t.z, s, acc.z), fmaf(t.w, s, acc.w)};
 }
 
-// KTAIL: K is no whole number of blocks, so each load checks its chunk, and the bytes of the last chunk
-// past K are made zeros in LDS.
-template <class S, bool POW2, bool KTAIL>
+// Where K is no whole number of blocks, the last step reads on into the next row, and those bytes are made
+// zeros in LDS (a check of every load instead took registers that the large tile does not have).
+template <class S, bool POW2>
 __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kernel(Args g) {
     constexpr int FI = 2 * S::FI, TJ = 2 * S::TJ, LA = S::LA, LB = S::LB, SA = S::SA, SB = S::SB;   // 16 x 16 tiles
     __shared__ __attribute__((aligned(1024))) unsigned char lds[S::LDS];
@@ -109,9 +115,6 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
     static_assert(LA <= kMaxLoads && LB <= kMaxLoads, "load slots");
     uint32_t voffA[kMaxLoads], voffB[kMaxLoads];
     const int lrow = lane / kChunks, lpos = lane % kChunks;
-    int kb[2];   // byte of K the lane's chunk starts at: load blocks alternate between two
-#pragma unroll
-    for (int p = 0; p < 2; ++p) kb[p] = (lpos ^ swz(p * kLoadRows + lrow)) * 16;
 #pragma unroll
     for (int j = 0; j < LA; ++j) {
         const int r = (j * S::NW + wave) * kLoadRows + lrow;
@@ -126,26 +129,14 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
 #pragma unroll
         for (int j = 0; j < LA; ++j) {
             unsigned char *dst = lds + slot_a * S::A_BYTES + (j * S::NW + wave) * 1024;
-            const int k0 = step * kStep;
-            if constexpr (KTAIL) {
-                const uint32_t v = k0 + kb[(j * S::NW + wave) & 1] >= g.K ? kOutside : voffA[j] + k0;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, v, 0, 0, 0);
-            } else {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, voffA[j], k0, 0, 0);
-            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, voffA[j], step * kStep, 0, 0);
         }
     };
     auto load_b = [&](int step, int slot_b) {
 #pragma unroll
         for (int j = 0; j < LB; ++j) {
             unsigned char *dst = lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (j * S::NW + wave) * 1024;
-            const int k0 = step * kStep;
-            if constexpr (KTAIL) {
-                const uint32_t v = k0 + kb[(j * S::NW + wave) & 1] >= g.K ? kOutside : voffB[j] + k0;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, v, 0, 0, 0);
-            } else {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, voffB[j], k0, 0, 0);
-            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, voffB[j], step * kStep, 0, 0);
         }
     };
     // 16-row tile q of an operand's tile: the lane's two chunks
@@ -156,18 +147,21 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
         const i32x4 b = *reinterpret_cast<const i32x4 *>(row + ((4 + quad) ^ swz(r)) * 16);
         return (i32x8){a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     };
-    // the bytes past K in the last chunk, in a tile that is whole: zeros
-    auto clear_tail = [&](int step, int slot_a, int slot_b) {
-        const int chunk = (g.K - step * kStep) >> 4, from = g.K & 15;
+    // the bytes past K of the last step's tiles, which are whole in LDS: zeros
+    const bool cut = g.K % kStep != 0 && kend == steps_total;
+    auto clear_tail = [&](int slot_a, int slot_b) {
+        const int from = g.K % kStep;
         for (int r = threadIdx.x; r < S::BF + S::BT; r += 64 * S::NW) {
+            const int sw = swz(r < S::BF ? r : r - S::BF);
             unsigned char *row = r < S::BF ? lds + slot_a * S::A_BYTES + r * kStep
                                            : lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (r - S::BF) * kStep;
-            unsigned char *p = row + (chunk ^ swz(r < S::BF ? r : r - S::BF)) * 16;
-            for (int i = from; i < 16; ++i) p[i] = 0;
+            for (int i = from; i & 15; ++i) row[((i >> 4) ^ sw) * 16 + (i & 15)] = 0;
+            for (int c = (from + 15) >> 4; c < kChunks; ++c)
+                *reinterpret_cast<u32x4 *>(row + (c ^ sw) * 16) = (u32x4){0u, 0u, 0u, 0u};
         }
-        __syncthreads();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        asm volatile("s_barrier" ::: "memory");
     };
-    const bool cut = KTAIL && (g.K & 15) != 0 && kend == steps_total;
     // the wave's scales: one per token in the lanes, one of its features
     const bool has_token = lane < TJ * 16 && t0 + wt * TJ * 16 + lane < g.n;
     const int64_t sx_at = has_token ? (t0 + wt * TJ * 16 + lane) * g.sx.s_row : 0;
@@ -188,57 +182,96 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
 
-    // The order of requests and the count of those that may be outstanding are linear_kernel's; the scales
-    // of step s + 1 are requested ahead of step s's tiles, so that count covers them.
+    // Requests go out in the order scales of step s + 1, x of step s + SB - 1, w of step s + SA - 1, in step
+    // s; past the last step they ask for the last one again, so that the counts stay what they are.  When
+    // step s ends, this many of the wave's newest loads may be outstanding while step s + 1 is whole.
     constexpr int LEFT = (SB - 2) * (LA + LB) + (SA > SB ? LA : 0);
     static_assert(LEFT < 64, "vmcnt");
+    const int last = nsteps - 1;
     StepScales next{};
+    i32x8 b[TJ], a[2];
+    f4v t[4];   // products on their way to the accumulators
+    int f[TJ], w_scale = 0;
+    auto request_x = [&](int s, int slot_b) { load_b(kbeg + min(s, last), slot_b); };
+    auto request_w = [&](int s, int slot_a) { load_a(kbeg + min(s, last), slot_a); };
+    auto hand_over = [&](int s, int slot_a, int slot_b) {   // step s is whole in LDS, for every wave
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+        if (cut && s == last) clear_tail(slot_a, slot_b);
+    };
+    int sa = 0, sb = 0;   // slots of step s
     if (nsteps > 0) {
         next = load_scales(kbeg);
-        for (int s = 1 - SA; s < 0; ++s) {
-            const int tb = s + SB - 1, ta = s + SA - 1;
-            if (tb >= 0 && tb < nsteps) load_b(kbeg + tb, tb % SB);
-            if (ta < nsteps) load_a(kbeg + ta, ta % SA);
+        for (int s = 1 - SA; s < 0; ++s) {   // as steps before 0 would have asked
+            if (s + SB - 1 >= 0) request_x(s + SB - 1, s + SB - 1);
+            request_w(s + SA - 1, s + SA - 1);
         }
-        if (nsteps >= SA) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (cut && nsteps == 1) clear_tail(kbeg, 0, 0);
+        hand_over(0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) b[j] = frag(lds + SA * S::A_BYTES, wt * TJ + j);
+        a[0] = frag(lds, wf * FI);
+        if constexpr (!POW2) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) t[q] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
+        }
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    int sa = 0, sb = 0;   // slots of step s
     for (int s = 0; s < nsteps; ++s) {
         const int na = sa + 1 == SA ? 0 : sa + 1, nb = sb + 1 == SB ? 0 : sb + 1;
-        const unsigned char *At = lds + sa * S::A_BYTES, *Bt = lds + SA * S::A_BYTES + sb * S::B_BYTES;
-        i32x8 b[TJ], a[2];
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) b[j] = frag(Bt, wt * TJ + j);
-        a[0] = frag(At, wf * FI);
+        const unsigned char *At = lds + sa * S::A_BYTES;
+        const unsigned char *An = lds + na * S::A_BYTES, *Bn = lds + SA * S::A_BYTES + nb * S::B_BYTES;
         // a lane's token of tile j is lane 16 j + l % 16 of the wave's
-        int f[TJ];
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
             f[j] = __builtin_amdgcn_ds_bpermute((j * 16 + l16) * 4, next.x);
             if constexpr (!POW2) f[j] = __float_as_int(__int_as_float(f[j]) * __int_as_float(next.w));
         }
-        const int w_scale = next.w;
-        if (s + 1 < nsteps) next = load_scales(kbeg + s + 1);
-        if (s + SB - 1 < nsteps) load_b(kbeg + s + SB - 1, sb == 0 ? SB - 1 : sb - 1);
-        if (s + SA - 1 < nsteps) load_a(kbeg + s + SA - 1, sa == 0 ? SA - 1 : sa - 1);
+        w_scale = next.w;
+        next = load_scales(kbeg + min(s + 1, last));
+        request_x(s + SB - 1, sb == 0 ? SB - 1 : sb - 1);
+        request_w(s + SA - 1, sa == 0 ? SA - 1 : sa - 1);
 #pragma unroll
         for (int i = 0; i < FI; ++i) {
-            if (i + 1 < FI) a[(i + 1) & 1] = frag(At, wf * FI + i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + 1 < FI) {
+                a[(i + 1) & 1] = frag(At, wf * FI + i + 1);
+            } else {   // the wave has read all of step s; the next one's operands follow the last products
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                hand_over(s + 1, na, nb);
+                a[0] = frag(An, wf * FI);
+            }
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) acc[i][j] = block_product<POW2>(a[i & 1], b[j], acc[i][j], w_scale, f[j]);
+            for (int j = 0; j < TJ; ++j) {
+                const int q = i * TJ + j;
+                if constexpr (POW2) {
+                    acc[i][j] = block_product<true>(a[i & 1], b[j], acc[i][j], w_scale, f[j]);
+                } else {   // a product is added two later
+                    t[q & 3] = block_product<false>(a[i & 1], b[j], t[q & 3], 0, 0);
+                    if (q >= 2) {
+                        const int pi = (q - 2) / TJ, pj = (q - 2) % TJ;
+                        acc[pi][pj] = scaled_sum(t[(q - 2) & 3], __int_as_float(f[pj]), acc[pi][pj]);
+                        pin(acc[pi][pj]);
+                    }
+                }
+                if (i + 1 == FI) {
+                    pin(POW2 ? acc[i][j] : t[q & 3]);
+                    b[j] = frag(Bn, wt * TJ + j);
+                }
+            }
+            if constexpr (POW2) {
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) pin(acc[i][j]);
+            }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (s + SA - 1 < nsteps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (cut && s + 2 == nsteps) clear_tail(kbeg + s + 1, na, nb);
+        if constexpr (!POW2) {
+#pragma unroll
+            for (int q = FI * TJ - 2; q < FI * TJ; ++q)
+                acc[q / TJ][q % TJ] = scaled_sum(t[q & 3], __int_as_float(f[q % TJ]), acc[q / TJ][q % TJ]);
+        }
         sa = na;
         sb = nb;
     }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();   // every wave is done with the operand tiles, and nothing is on its way there
 
     // epilogue: a wave's own LDS region, 32 tokens at a time
     constexpr int LPT = FI * 2, TPP = 64 / LPT;   // lanes per token, tokens per pass
@@ -371,9 +404,8 @@ __global__ __launch_bounds__(64 * kRowsWaves, 2) void blocks_rows_kernel(Args g)
             const i32x8 w = join(q.w[u]);
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                int f = q.sx[t][u];
-                if constexpr (!POW2) f = __float_as_int(__int_as_float(f) * __int_as_float(q.sw[u]));
-                acc[t] = block_product<POW2>(w, join(q.x[t][u]), acc[t], q.sw[u], f);
+                const f4v p = block_product<POW2>(w, join(q.x[t][u]), acc[t], q.sw[u], q.sx[t][u]);
+                acc[t] = POW2 ? p : scaled_sum(p, __int_as_float(q.sx[t][u]) * __int_as_float(q.sw[u]), acc[t]);
             }
         }
     };

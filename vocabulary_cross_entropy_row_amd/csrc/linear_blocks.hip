@@ -27,14 +27,8 @@ using Tiny = linear::Shape<64, 32, 2, 1, 4, 4>;
 template <class S>
 hipError_t launch_shape(const blocks::Args &g, bool pow2, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(g.per_xcd) * 8u), block(64 * S::NW);
-    const bool tail = g.K % blocks::kStep != 0;
-    if (pow2) {
-        if (tail) hipLaunchKernelGGL((blocks::blocks_kernel<S, true, true>), grid, block, 0, st, g);
-        else hipLaunchKernelGGL((blocks::blocks_kernel<S, true, false>), grid, block, 0, st, g);
-    } else {
-        if (tail) hipLaunchKernelGGL((blocks::blocks_kernel<S, false, true>), grid, block, 0, st, g);
-        else hipLaunchKernelGGL((blocks::blocks_kernel<S, false, false>), grid, block, 0, st, g);
-    }
+    if (pow2) hipLaunchKernelGGL((blocks::blocks_kernel<S, true>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((blocks::blocks_kernel<S, false>), grid, block, 0, st, g);
     return hipGetLastError();
 }
 template <int TT>
