@@ -125,19 +125,13 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
         const int r = (j * S::NW + wave) * kLoadRows + lrow;
         voffB[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.ldx) + (lpos ^ swz(r)) * 16u;
     }
-    auto load_a = [&](int step, int slot_a) {
-#pragma unroll
-        for (int j = 0; j < LA; ++j) {
-            unsigned char *dst = lds + slot_a * S::A_BYTES + (j * S::NW + wave) * 1024;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, voffA[j], step * kStep, 0, 0);
-        }
+    auto load_a = [&](int step, int slot_a, int j) {
+        unsigned char *dst = lds + slot_a * S::A_BYTES + (j * S::NW + wave) * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)dst, 16, voffA[j], step * kStep, 0, 0);
     };
-    auto load_b = [&](int step, int slot_b) {
-#pragma unroll
-        for (int j = 0; j < LB; ++j) {
-            unsigned char *dst = lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (j * S::NW + wave) * 1024;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, voffB[j], step * kStep, 0, 0);
-        }
+    auto load_b = [&](int step, int slot_b, int j) {
+        unsigned char *dst = lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (j * S::NW + wave) * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsB, (lds_ptr)dst, 16, voffB[j], step * kStep, 0, 0);
     };
     // 16-row tile q of an operand's tile: the lane's two chunks
     auto frag = [&](const unsigned char *tile_at, int q) {
@@ -182,18 +176,27 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
 
-    // Requests go out in the order scales of step s + 1, x of step s + SB - 1, w of step s + SA - 1, in step
-    // s; past the last step they ask for the last one again, so that the counts stay what they are.  When
-    // step s ends, this many of the wave's newest loads may be outstanding while step s + 1 is whole.
-    constexpr int LEFT = (SB - 2) * (LA + LB) + (SA > SB ? LA : 0);
+    // Requests go out in the order scales of step s + 1, w of step s + SA - 1, x of step s + SB, in step s,
+    // a few with each group of products (all at once they hold up the products behind them); past the
+    // last step they ask for the last one again, so that the counts stay what they are.  x of step s + SB
+    // takes the place of step s's, whose fragments every wave has in registers by a barrier ahead of the
+    // first of those requests: so both operands are asked for two steps ahead with five tiles of LDS.
+    static_assert(SA == SB + 1, "both operands' requests of a step are for the same wait");
+    constexpr int PER = (LA + LB + FI - 1) / FI, FIRST_X = LA / PER > 0 ? LA / PER : 1;
+    // when step s ends, what it and the SB - 2 before it asked for may be outstanding while step s + 1 is whole
+    constexpr int BEFORE = (FI - 1) * PER < LA + LB ? (FI - 1) * PER : LA + LB;
+    constexpr int LEFT = (SB - 2) * (LA + LB) + BEFORE;
+    static_assert(FIRST_X * PER <= LA, "x is asked for behind the barrier");
     static_assert(LEFT < 64, "vmcnt");
     const int last = nsteps - 1;
     StepScales next{};
     i32x8 b[TJ], a[2];
     f4v t[4];   // products on their way to the accumulators
     int f[TJ], w_scale = 0;
-    auto request_x = [&](int s, int slot_b) { load_b(kbeg + min(s, last), slot_b); };
-    auto request_w = [&](int s, int slot_a) { load_a(kbeg + min(s, last), slot_a); };
+    auto request = [&](int s, int slot_a, int slot_b, int q) {   // request q of step s
+        if (q < LA) load_a(kbeg + min(s + SA - 1, last), slot_a, q);
+        else if (q < LA + LB) load_b(kbeg + min(s + SB, last), slot_b, q - LA);
+    };
     auto hand_over = [&](int s, int slot_a, int slot_b) {   // step s is whole in LDS, for every wave
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
         asm volatile("s_barrier" ::: "memory");
@@ -202,10 +205,10 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
     int sa = 0, sb = 0;   // slots of step s
     if (nsteps > 0) {
         next = load_scales(kbeg);
-        for (int s = 1 - SA; s < 0; ++s) {   // as steps before 0 would have asked
-            if (s + SB - 1 >= 0) request_x(s + SB - 1, s + SB - 1);
-            request_w(s + SA - 1, s + SA - 1);
-        }
+#pragma unroll
+        for (int s = 0; s < SB; ++s)   // as steps before 0 would have asked
+#pragma unroll
+            for (int q = 0; q < LA + LB; ++q) request(s - SB, s, s, q);
         hand_over(0, 0, 0);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) b[j] = frag(lds + SA * S::A_BYTES, wt * TJ + j);
@@ -227,17 +230,26 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
         }
         w_scale = next.w;
         next = load_scales(kbeg + min(s + 1, last));
-        request_x(s + SB - 1, sb == 0 ? SB - 1 : sb - 1);
-        request_w(s + SA - 1, sa == 0 ? SA - 1 : sa - 1);
+        const int fa = sa == 0 ? SA - 1 : sa - 1;   // free since the last step ended
 #pragma unroll
         for (int i = 0; i < FI; ++i) {
             __builtin_amdgcn_sched_barrier(0);
+            if (i == FIRST_X) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // b, which the first products have used
+                asm volatile("s_barrier" ::: "memory");
+            }
+            if (i + 1 < FI) {
+#pragma unroll
+                for (int q = i * PER; q < (i + 1) * PER; ++q) request(s, fa, sb, q);
+            }
             if (i + 1 < FI) {
                 a[(i + 1) & 1] = frag(At, wf * FI + i + 1);
             } else {   // the wave has read all of step s; the next one's operands follow the last products
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 hand_over(s + 1, na, nb);
                 a[0] = frag(An, wf * FI);
+#pragma unroll
+                for (int q = i * PER; q < LA + LB; ++q) request(s, fa, sb, q);
             }
 #pragma unroll
             for (int j = 0; j < TJ; ++j) {

@@ -20,9 +20,9 @@ using namespace linear_plan;
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 using Big = linear::Shape<256, 256, 2, 4, 3, 2>;
-using Wide = linear::Shape<256, 128, 4, 2, 3, 3>;
-using Low = linear::Shape<128, 64, 2, 2, 3, 3>;
-using Tiny = linear::Shape<64, 32, 2, 1, 4, 4>;
+using Wide = linear::Shape<256, 128, 4, 2, 3, 2>;
+using Low = linear::Shape<128, 64, 2, 2, 3, 2>;
+using Tiny = linear::Shape<64, 32, 2, 1, 4, 3>;
 
 template <class S>
 hipError_t launch_shape(const blocks::Args &g, bool pow2, hipStream_t st) {
