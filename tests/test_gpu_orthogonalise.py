@@ -1,7 +1,7 @@
 """The orthogonalised update on the GPU against its definition in 64 bits.
 
-Tolerances.  The same recursion with the kernel's roundings put in (X as hi + lo in fp16, the operand hi;
-the diagonals of A and B kept, the rest in fp16), in 64 bits otherwise, is off from the definition by some
+Tolerances.  The same recursion with the kernel's roundings put in (X as fp16 and what that leaves in e4m3,
+the operand the former; the diagonals of A and B kept, the rest in fp16), in 64 bits otherwise, is off from the definition by some
 `dev` that the matrix's own spectrum decides.  The kernel rounds at the same places, so its deviation is of
 the same size; sums in another order and values next to a rounding's border change which way single
 roundings go, not how large they are.  It is held to three times dev in the 2-norm, and each
@@ -59,7 +59,8 @@ def rounded(G, steps=5, abc=ABC, eps=1e-7):
 
     for _ in range(steps):
         hi = half(X, S)
-        X = hi + half(X - hi, S)
+        up = 2.0 ** 19 / S
+        X = hi + ((X - hi) * S * up).clamp(-448, 448).float().to(torch.float8_e4m3fn).double() / up / S
         A = hi @ hi.t()
         D = A.diagonal().clone()
         O = half(A - torch.diag(D), 1024.0)

@@ -192,6 +192,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
     StepScales next{};
     i32x8 b[TJ], a[2];
     f4v t[4];   // products on their way to the accumulators
+    constexpr int LAG = 3;
     int f[TJ], w_scale = 0;
     auto request = [&](int s, int slot_a, int slot_b, int q) {   // request q of step s
         if (q < LA) load_a(kbeg + min(s + SA - 1, last), slot_a, q);
@@ -256,16 +257,17 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
                 const int q = i * TJ + j;
                 if constexpr (POW2) {
                     acc[i][j] = block_product<true>(a[i & 1], b[j], acc[i][j], w_scale, f[j]);
-                } else {   // a product is added two later
+                } else {   // a product is added LAG later, when it has left the matrix core
                     t[q & 3] = block_product<false>(a[i & 1], b[j], t[q & 3], 0, 0);
-                    if (q >= 2) {
-                        const int pi = (q - 2) / TJ, pj = (q - 2) % TJ;
-                        acc[pi][pj] = scaled_sum(t[(q - 2) & 3], __int_as_float(f[pj]), acc[pi][pj]);
+                    pin(t[q & 3]);
+                    if (q >= LAG) {
+                        const int pi = (q - LAG) / TJ, pj = (q - LAG) % TJ;
+                        acc[pi][pj] = scaled_sum(t[(q - LAG) & 3], __int_as_float(f[pj]), acc[pi][pj]);
                         pin(acc[pi][pj]);
                     }
                 }
                 if (i + 1 == FI) {
-                    pin(POW2 ? acc[i][j] : t[q & 3]);
+                    if constexpr (POW2) pin(acc[i][j]);
                     b[j] = frag(Bn, wt * TJ + j);
                 }
             }
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
         }
         if constexpr (!POW2) {
 #pragma unroll
-            for (int q = FI * TJ - 2; q < FI * TJ; ++q)
+            for (int q = FI * TJ - LAG; q < FI * TJ; ++q)
                 acc[q / TJ][q % TJ] = scaled_sum(t[q & 3], __int_as_float(f[q % TJ]), acc[q / TJ][q % TJ]);
         }
         sa = na;

@@ -11,18 +11,26 @@
 #include "blocks_internal.h"
 #include "blocks_mfma.h"
 #include "head_internal.h"
-#include "linear_plan.h"
+#include "blocks_plan.h"
 
 namespace lce {
 namespace {
 
-using namespace linear_plan;
+using namespace blocks_plan;
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 using Big = linear::Shape<256, 256, 2, 4, 3, 2>;
 using Wide = linear::Shape<256, 128, 4, 2, 3, 2>;
 using Low = linear::Shape<128, 64, 2, 2, 3, 2>;
 using Tiny = linear::Shape<64, 32, 2, 1, 4, 3>;
+
+template <class S>
+constexpr bool planned(int i) {
+    return kShapes[i].bf == S::BF && kShapes[i].bt == S::BT && kShapes[i].threads == 64 * S::NW && kShapes[i].per_cu == S::PER_CU;
+}
+static_assert(planned<Big>(BIG) && planned<Wide>(WIDE) && planned<Low>(LOW) && planned<Tiny>(TINY) &&
+              kShapes[ROWS16].threads == 64 * blocks::kRowsWaves && kShapes[ROWS32].threads == 64 * blocks::kRowsWaves,
+              "the plan's tiles are the kernels'");
 
 template <class S>
 hipError_t launch_shape(const blocks::Args &g, bool pow2, hipStream_t st) {
@@ -43,6 +51,10 @@ hipError_t launch_rows(const blocks::Args &g, bool pow2, hipStream_t st) {
         else hipLaunchKernelGGL((blocks::blocks_rows_kernel<false, false, TT>), grid, block, 0, st, g);
     }
     return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t values) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < values; i += static_cast<int64_t>(gridDim.x) * 256) p[i] = 0;
 }
 
 // Workspace of the backward: the two quantised forms of grad_out with their scales, the bias's partial
@@ -73,13 +85,14 @@ GradLayout grad_layout(int64_t n, int64_t K, int64_t M) {
 
 size_t linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M) {
     if (n <= 0 || M <= 0 || K <= 0) return 0;
-    const Plan p = plan_of(n, K, M, true);
-    return p.splits > 1 ? static_cast<size_t>(p.splits) * n * round_up(M, 8) * 4 : 0;
+    const int splits = std::max(plan_of(n, K, M, true).splits, plan_of(n, K, M, false).splits);   // whatever the scales' type
+    return splits > 1 ? static_cast<size_t>(splits) * n * round_up(M, 8) * 4 : 0;
 }
 
 hipError_t launch_linear_blocks(const BlocksArgs &a, hipStream_t st) {
     if (a.n <= 0 || a.M <= 0) return hipSuccess;
-    const Plan p = plan_of(a.n, a.K, a.M, true);
+    const bool pow2 = a.sx.e8m0 && a.sw.e8m0;
+    const Plan p = plan_of(a.n, a.K, a.M, pow2);
     const ShapeInfo &s = kShapes[p.shape];
     blocks::Args g;
     g.w = static_cast<const unsigned char *>(a.weight);
@@ -114,7 +127,6 @@ hipError_t launch_linear_blocks(const BlocksArgs &a, hipStream_t st) {
     e.ldp = a.ldp;
     e.n = a.n;
     e.M = a.M;
-    const bool pow2 = a.sx.e8m0 && a.sw.e8m0;
     hipError_t err;
     switch (p.shape) {
         case BIG: err = launch_shape<Big>(g, pow2, st); break;
@@ -168,7 +180,12 @@ hipError_t launch_linear_blocks_backward(const BlocksGradArgs &a, hipStream_t st
         g.part = reinterpret_cast<float *>(ws + L.off_part);
         if ((e = launch_linear_blocks(g, st)) != hipSuccess) return e;
     }
-    if (a.grad_weight) {   // without tokens: a product over no blocks, zeros
+    if (a.grad_weight && a.n == 0) {
+        const int64_t values = a.M * a.K;
+        hipLaunchKernelGGL(zero_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(values, 256), 16384))), dim3(256), 0,
+                           st, static_cast<uint16_t *>(a.grad_weight), values);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    } else if (a.grad_weight) {
         BlocksArgs g{};
         g.x = ws + L.off_gt;
         g.ldx = L.ldgt;

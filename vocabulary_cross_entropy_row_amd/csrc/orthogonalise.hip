@@ -44,7 +44,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kUnit = 64;             // fp16 values of K in a step
 constexpr float kScaleO = 1024.0f, kScaleB = 256.0f;
-constexpr int kNormGroups = 64;           // partial sums of squares per matrix
+constexpr int kNormGroups = 1024;         // partial sums of squares per matrix, at most
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -57,36 +57,81 @@ __device__ __forceinline__ u32x4 pack_h8(const float (&v)[8]) {
     return __builtin_bit_cast(u32x4, h);
 }
 
+typedef float f2v __attribute__((ext_vector_type(2)));
+// What fp16 leaves of eight values, in e4m3 times `up`
+__device__ __forceinline__ uint2 pack_rest(const float (&v)[8], float up) {
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r[e] = fminf(fmaxf((v[e] - static_cast<float>(static_cast<_Float16>(v[e]))) * up, -448.0f), 448.0f);
+    int a = 0, b = 0;
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], a, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], b, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], b, true);
+    return make_uint2(static_cast<uint32_t>(a), static_cast<uint32_t>(b));
+}
+__device__ __forceinline__ void unpack(u32x4 hi, uint2 lo, float down, float (&v)[8]) {
+    const h8 h = __builtin_bit_cast(h8, hi);
+    const f2v r[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.x), false), __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.x), true),
+                      __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.y), false), __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.y), true)};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(r[e >> 1][e & 1], down, static_cast<float>(h[e]));
+}
+
+// eight values of a row from column c on, zeros from `cols` on
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, int64_t row, int64_t c, int64_t cols, float (&v)[8]) {
+    if (c + 8 <= cols) {
+        if constexpr (BF16) {
+            const u32x4 q = *reinterpret_cast<const any16 *>(static_cast<const uint16_t *>(p) + row + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = Elt<true>::get(q, e);
+        } else {
+            const any16 *q = reinterpret_cast<const any16 *>(static_cast<const float *>(p) + row + c);
+            const u32x4 x = q[0], y = q[1];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = Elt<false>::get(e < 4 ? x : y, e & 3);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? Elt<BF16>::load_one(p, row + c + e) : 0.0f;
+    }
+}
+
 // ---- the norm, and X in fp16 -----------------------------------------------------------------
 
 struct LoadArgs {
     const void *g;
     int64_t ldg, gb;                  // strides of G (elements)
     int64_t rows, cols;               // of G
-    double *part;                     // [batch][kNormGroups]
-    uint16_t *hi, *lo, *xt;           // X [rp][ldx], X^T [cp][ldt]
+    double *part;                     // [batch][kNormGroups], the first `groups` used
+    int groups;
+    uint16_t *hi, *xt;                // X [rp][ldx], X^T [cp][ldt]
+    unsigned char *lo;                // as X
     int64_t ldx, ldt, xb, tb;         // row and batch strides (elements)
     int rp, cp;                       // padded rows and columns of X
     int tall;                         // X is G^T
-    float s, eps;
+    float s, up, eps;
 };
 
-// Sums of squares in fp64, a fixed share of the rows' 1024-value pieces per workgroup: no square of a
+// Sums of squares in fp64, a fixed share of the rows' 2048-value pieces per workgroup: no square of a
 // finite fp32 value overflows, and the order is fixed.
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_kernel(LoadArgs a) {
     __shared__ double sums[4];
-    const int64_t pieces = (a.cols + 1023) / 1024, total = a.rows * pieces;
+    const int64_t pieces = (a.cols + 2047) / 2048, total = a.rows * pieces;
     const int64_t base = blockIdx.y * a.gb;
     double sum = 0.0;
-    for (int64_t i = blockIdx.x; i < total; i += kNormGroups) {
-        const int64_t row = i / pieces, c = (i - row * pieces) * 1024 + threadIdx.x * 4;
-        const int64_t at = base + row * a.ldg + c;
-        float v[4];
+    for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+        const int64_t row = i / pieces, c = (i - row * pieces) * 2048 + threadIdx.x * 8;
+        float v[8];
+        load8<BF16>(a.g, base + row * a.ldg, c, c < a.cols ? a.cols : 0, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < a.cols ? Elt<BF16>::load_one(a.g, at + e) : 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += static_cast<double>(v[e]) * static_cast<double>(v[e]);
+        for (int e = 0; e < 8; e += 2) {
+            // two squares of 24-bit values in fp64 are exact; their sum rounds once
+            sum += static_cast<double>(v[e]) * static_cast<double>(v[e]) + static_cast<double>(v[e + 1]) * static_cast<double>(v[e + 1]);
+        }
     }
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
@@ -99,31 +144,34 @@ __global__ __launch_bounds__(256) void norm_kernel(LoadArgs a) {
 template <bool BF16>
 __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
     __shared__ float tile[64][65];
-    __shared__ float factor;
+    __shared__ double sums[4];
     const int t = threadIdx.x, z = blockIdx.z;
-    if (t < 64) {
-        double s = a.part[z * kNormGroups + t];
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
-        if (t == 0) factor = static_cast<float>(static_cast<double>(a.s) / (sqrt(s) + static_cast<double>(a.eps)));
-    }
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of X
     const int g0 = a.tall ? c0 : r0, h0 = a.tall ? r0 : c0;   // of G
-    float v[16];
+    float v[2][8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t row = g0 + i * 4 + (t >> 6), col = h0 + (t & 63);
-        v[i] = row < a.rows && col < a.cols ? Elt<BF16>::load_one(a.g, z * a.gb + row * a.ldg + col) : 0.0f;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = g0 + i * 32 + (t >> 3);
+        load8<BF16>(a.g, z * a.gb + row * a.ldg, h0 + (t & 7) * 8, row < a.rows ? a.cols : 0, v[i]);
     }
-    __syncthreads();
+    double s = 0.0;
+    for (int i = t; i < a.groups; i += 256) s += a.part[z * kNormGroups + i];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) tile[i * 4 + (t >> 6)][t & 63] = v[i] * factor;
+    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+    if ((t & 63) == 0) sums[t >> 6] = s;
+    __syncthreads();
+    s = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    const float factor = static_cast<float>(static_cast<double>(a.s) / (sqrt(s) + static_cast<double>(a.eps)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[i * 32 + (t >> 3)][(t & 7) * 8 + e] = v[i][e] * factor;
     __syncthreads();
     // eight values along a row of X, and along a row of X^T
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int line = i * 32 + (t >> 3), at = (t & 7) * 8;
-        float p[8], q[8], rest[8];
+        float p[8], q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             p[e] = tile[line][at + e];   // of G
@@ -137,11 +185,9 @@ __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
                 q[e] = x;
             }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rest[e] = p[e] - static_cast<float>(static_cast<_Float16>(p[e]));
         const int64_t x_at = z * a.xb + static_cast<int64_t>(r0 + line) * a.ldx + c0 + at;
         *reinterpret_cast<u32x4 *>(a.hi + x_at) = pack_h8(p);
-        *reinterpret_cast<u32x4 *>(a.lo + x_at) = pack_h8(rest);
+        *reinterpret_cast<uint2 *>(a.lo + x_at) = pack_rest(p, a.up);
         *reinterpret_cast<u32x4 *>(a.xt + z * a.tb + static_cast<int64_t>(c0 + line) * a.ldt + r0 + at) = pack_h8(q);
     }
 }
@@ -155,8 +201,9 @@ struct Args {
     int64_t ldw, ldx, wb, xb;         // row and batch strides (elements)
     int rows_w, rows_x;               // multiples of 64
     int steps;                        // of K
-    int tiles_f, per_batch, total, splits, per_xcd;   // tiles; per_batch: of one matrix, all splits
-    float *part;                      // splits > 1: [batch][splits][rows][rows] fp32
+    int tiles_f, per_batch, total;    // tiles: per row of them, of one matrix, of all
+    int groups, per_xcd;              // workgroups; ceil(groups / 8)
+    float *part;                      // groups != total: [2 groups][side][side] fp32
     // epilogue
     float inv;                        // of the products' scale
     uint16_t *o;                      // O [rows][ldo]: written by GRAM, read by POLY
@@ -164,7 +211,9 @@ struct Args {
     int64_t ldo, ob;
     float *d, *e;                     // diagonals of A, and a + that of B: [batch][rows]
     float a, b, c;
-    uint16_t *hi, *lo, *xt;           // X and the next X^T
+    uint16_t *hi, *xt;                // X and the next X^T
+    unsigned char *lo;
+    float up, down;                   // of lo
     int64_t ldh, hb, ldt, tb;
     void *out;                        // LAST: bf16
     int64_t ldout, outb;
@@ -172,28 +221,34 @@ struct Args {
     int tall;
 };
 
-// GRAM: values v of A to O and its diagonal.  POLY: values of O O to B.
+// Tile mn of a lower triangle, row ti of which holds ti + 1
+__device__ __forceinline__ void triangle(int mn, int &ti, int &fi) {
+    ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(mn) + 1.0f) - 1.0f) * 0.5f);
+    while (ti * (ti + 1) / 2 > mn) --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= mn) ++ti;
+    fi = mn - ti * (ti + 1) / 2;
+}
+
+// GRAM: values v of A to O and its diagonal.  POLY: values of O O to B, from O there, the diagonal at t and
+// at f .. f + 7.
 template <int EPI>
-__device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, int f, float (&v)[8]) {
-    float *d = g.d + static_cast<int64_t>(z) * g.rows_x;
+__device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, int f, u32x4 oq, float dt, const float (&df)[8], float (&v)[8]) {
     if constexpr (EPI == GRAM) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             v[u] *= g.inv;
             if (t == f + u) {
-                d[t] = v[u];
+                g.d[static_cast<int64_t>(z) * g.rows_x + t] = v[u];
                 v[u] = 0.0f;
             }
             v[u] *= kScaleO;
         }
     } else {
-        const u32x4 oq = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
         const h8 o = __builtin_bit_cast(h8, oq);
-        const float dt = d[t];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float df = d[f + u], ov = static_cast<float>(o[u]) * (1.0f / kScaleO);
-            float square = fmaf(dt + df, ov, v[u] * g.inv);
+            const float ov = static_cast<float>(o[u]) * (1.0f / kScaleO);
+            float square = fmaf(dt + df[u], ov, v[u] * g.inv);
             if (t == f + u) {
                 square = fmaf(dt, dt, square);   // O is 0 there
                 g.e[static_cast<int64_t>(z) * g.rows_x + t] = g.a + fmaf(g.c, square, g.b * dt);
@@ -205,6 +260,9 @@ __device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, in
     }
 }
 
+// The steps of all tiles are one sequence, cut into equal ranges: the unit at which range i of n starts
+__device__ __forceinline__ int64_t range_start(int64_t units, int n, int i) { return units * i / n; }
+
 template <class S, int EPI>
 __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kernel(Args g) {
     constexpr int FI = S::FI, TJ = S::TJ, KK = 4, LA = S::LA, LB = S::LB, SA = S::SA, SB = S::SB;
@@ -212,38 +270,24 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     static_assert(!SYM || S::BF == S::BT, "tiles of a symmetric product are square");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[S::LDS];
 
-    // each XCD walks a contiguous range of the tiles
-    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-    const int tile = xcd * g.per_xcd + slot;
-    if (slot >= g.per_xcd || tile >= g.total) return;
-    const int z = tile / g.per_batch, in_batch = tile - z * g.per_batch;
-    const int per_split = g.per_batch / g.splits, ks = in_batch / per_split, mn = in_batch - ks * per_split;
-    int ti, fi;
-    if constexpr (SYM) {   // row ti of the lower triangle holds ti + 1 tiles
-        ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(mn) + 1.0f) - 1.0f) * 0.5f);
-        while (ti * (ti + 1) / 2 > mn) --ti;
-        while ((ti + 1) * (ti + 2) / 2 <= mn) ++ti;
-        fi = mn - ti * (ti + 1) / 2;
-    } else {   // groups of four token tiles, its token tiles fastest
-        constexpr int GROUP = 4;
-        const int tiles_t = per_split / g.tiles_f;
-        const int first_t = mn / (GROUP * g.tiles_f) * GROUP;
-        const int gt = min(GROUP, tiles_t - first_t);
-        const int within = mn - first_t * g.tiles_f;
-        ti = first_t + within % gt;
-        fi = within / gt;
+    // Each XCD takes a contiguous range of the workgroups' ranges.  With as many workgroups as tiles a range
+    // is a tile.  Otherwise ranges start and end inside tiles, and what a workgroup has of such a tile goes
+    // to memory: slot 2 w for the piece that its range starts with, 2 w + 1 for one that it ends with.
+    const int w = (blockIdx.x & 7) * g.per_xcd + (blockIdx.x >> 3);
+    if (static_cast<int>(blockIdx.x >> 3) >= g.per_xcd || w >= g.groups) return;
+    const bool whole = !SYM || g.groups == g.total;
+    int tile = w, s0 = 0, left = g.steps;   // left: steps of the range
+    if (!whole) {
+        const int64_t units = static_cast<int64_t>(g.total) * g.steps, from = range_start(units, g.groups, w);
+        left = __builtin_amdgcn_readfirstlane(static_cast<int>(range_start(units, g.groups, w + 1) - from));
+        tile = __builtin_amdgcn_readfirstlane(static_cast<int>(from / g.steps));
+        s0 = __builtin_amdgcn_readfirstlane(static_cast<int>(from - static_cast<int64_t>(tile) * g.steps));
     }
-    const int t0 = ti * S::BT, f0 = fi * S::BF;
-    const int kbeg = static_cast<int>(static_cast<int64_t>(g.steps) * ks / g.splits);
-    const int nsteps = static_cast<int>(static_cast<int64_t>(g.steps) * (ks + 1) / g.splits) - kbeg;
 
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wf = wave / S::WT, wt = wave % S::WT;
-    const int fr = min(S::BF, g.rows_w - f0), tr = min(S::BT, g.rows_x - t0);
     const uint32_t ldw = static_cast<uint32_t>(g.ldw * 2), ldx = static_cast<uint32_t>(g.ldx * 2), kbytes = g.steps * kStep;
-    const __amdgpu_buffer_rsrc_t rsA = uniform_rsrc(g.w + z * g.wb + f0 * g.ldw, (fr - 1) * ldw + kbytes);
-    const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(g.x + z * g.xb + t0 * g.ldx, (tr - 1) * ldx + kbytes);
     constexpr int kMaxLoads = 8;
     static_assert(LA <= kMaxLoads && LB <= kMaxLoads, "load slots");
     uint32_t voffA[kMaxLoads], voffB[kMaxLoads];
@@ -258,6 +302,25 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
         const int r = (j * S::NW + wave) * kLoadRows + lrow;
         voffB[j] = static_cast<uint32_t>(r) * ldx + (lpos ^ swz(r)) * 16u;
     }
+    while (left > 0) {
+    const int z = __builtin_amdgcn_readfirstlane(tile / g.per_batch), mn = tile - z * g.per_batch;
+    int ti, fi;
+    if constexpr (SYM) {
+        triangle(mn, ti, fi);
+    } else {   // groups of four token tiles, its token tiles fastest
+        constexpr int GROUP = 4;
+        const int tiles_t = g.per_batch / g.tiles_f;
+        const int first_t = mn / (GROUP * g.tiles_f) * GROUP;
+        const int gt = min(GROUP, tiles_t - first_t);
+        const int within = mn - first_t * g.tiles_f;
+        ti = first_t + within % gt;
+        fi = within / gt;
+    }
+    const int t0 = __builtin_amdgcn_readfirstlane(ti * S::BT), f0 = __builtin_amdgcn_readfirstlane(fi * S::BF);
+    const int kbeg = s0, nsteps = min(left, g.steps - s0);
+    const int fr = min(S::BF, g.rows_w - f0), tr = min(S::BT, g.rows_x - t0);
+    const __amdgpu_buffer_rsrc_t rsA = uniform_rsrc(g.w + z * g.wb + f0 * g.ldw, (fr - 1) * ldw + kbytes);
+    const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(g.x + z * g.xb + t0 * g.ldx, (tr - 1) * ldx + kbytes);
     auto load_a = [&](int step, int slot_a) {
 #pragma unroll
         for (int j = 0; j < LA; ++j)
@@ -352,81 +415,104 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     };
     for (int s = 0; s < nsteps; ++s) one_step(s);
 
-    // epilogue: a wave's own LDS region, 32 tokens at a time, eight features of a token per lane
+    // epilogue: a wave's own LDS region, 32 tokens at a time, eight features of a token per lane; what it
+    // reads of X or O for them is asked for all at once
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();
     constexpr int LPT = FI * 4, TPP = 64 / LPT, PASSES = 32 / TPP;
     float *reg = reinterpret_cast<float *>(lds) + wave * 32 * S::OUT_LD;
     const int lf = (lane % LPT) * 8;
     const int f = f0 + wf * FI * 32 + lf;
+    const bool piece = SYM && nsteps != g.steps;
     // rows of X^T, of the mirrored tile, or of the output of a tall matrix
-    const bool turned = EPI == APPLY || (SYM && ti != fi && g.splits == 1) || (EPI == LAST && g.tall);
+    const bool turned = EPI == APPLY || (SYM && ti != fi && !piece) || (EPI == LAST && g.tall);
+    float df[8] = {};
+    if (EPI == POLY && !piece && f < g.rows_w) {
+        const float4 *d = reinterpret_cast<const float4 *>(g.d + static_cast<int64_t>(z) * g.rows_x + f);
+        const float4 x = d[0], y = d[1];
+        df[0] = x.x; df[1] = x.y; df[2] = x.z; df[3] = x.w;
+        df[4] = y.x; df[5] = y.y; df[6] = y.z; df[7] = y.w;
+    }
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
         const int tj = t0 + (wt * TJ + j) * 32;
+        const bool there = tj < g.rows_x && f < g.rows_w;   // rows come in 64s: all 32 tokens or none
 #pragma unroll
         for (int i = 0; i < FI; ++i)
 #pragma unroll
             for (int r = 0; r < 16; r += 4)
                 *reinterpret_cast<float4 *>(reg + (lane & 31) * S::OUT_LD + i * 32 + (r >> 2) * 8 + half * 4) =
                     make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (tj >= g.rows_x || f0 + wf * FI * 32 >= g.rows_w) continue;   // rows come in 64s: all 32, and all or none of each 32 features
-#pragma unroll 2
-        for (int p = 0; p < PASSES; ++p) {
-            const int tl = p * TPP + lane / LPT, t = tj + tl;
-            float *at = reg + tl * S::OUT_LD + lf;
-            if (f >= g.rows_w) continue;
-            const float4 x = reinterpret_cast<const float4 *>(at)[0], y = reinterpret_cast<const float4 *>(at)[1];
-            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            if constexpr (SYM) {
-                if (g.splits > 1) {
-                    float4 *o = reinterpret_cast<float4 *>(
-                        g.part + ((static_cast<int64_t>(z) * g.splits + ks) * g.rows_x + t) * g.rows_x + f);
-                    o[0] = x;
-                    o[1] = y;
-                    continue;
-                }
-                symmetric_values<EPI>(g, z, t, f, v);
-                *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
-            } else {
-                const int64_t h_at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
-                const h8 hi = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(g.hi + h_at));
-                const h8 lo = __builtin_bit_cast(h8, *reinterpret_cast<const u32x4 *>(g.lo + h_at));
-                const float e = g.e[static_cast<int64_t>(z) * g.rows_x + t];
+        asm volatile("" ::: "memory");   // the accumulators' registers are free for what follows
+        u32x4 hi[PASSES];   // of X, or O
+        uint2 lo[PASSES];
+        float et[PASSES];   // the diagonal at the token
+        if (there && EPI != GRAM && !piece) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    v[u] = fmaf(e, static_cast<float>(hi[u]) + static_cast<float>(lo[u]), v[u] * (1.0f / kScaleB));
-                if constexpr (EPI == APPLY) {
-                    float rest[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) rest[u] = v[u] - static_cast<float>(static_cast<_Float16>(v[u]));
-                    *reinterpret_cast<u32x4 *>(g.hi + h_at) = pack_h8(v);
-                    *reinterpret_cast<u32x4 *>(g.lo + h_at) = pack_h8(rest);
+            for (int p = 0; p < PASSES; ++p) {
+                const int t = tj + p * TPP + lane / LPT;
+                if constexpr (EPI == POLY) {
+                    hi[p] = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
                 } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) v[u] *= g.inv;
-                    if (!g.tall && t < g.r) {
-                        uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + static_cast<int64_t>(t) * g.ldout + f;
-                        if (f + 8 <= g.cols) {
-                            *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (f + u < g.cols) Elt<true>::store_one(o, u, v[u]);
-                        }
-                    }
+                    const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
+                    hi[p] = *reinterpret_cast<const u32x4 *>(g.hi + at);
+                    lo[p] = *reinterpret_cast<const uint2 *>(g.lo + at);
                 }
-            }
-            if (turned) {
-                reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                et[p] = (EPI == POLY ? g.d : g.e)[static_cast<int64_t>(z) * g.rows_x + t];
             }
         }
         __builtin_amdgcn_wave_barrier();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (turned) {   // four lanes a feature, eight of its 32 tokens each
+        if (there) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int tl = p * TPP + lane / LPT, t = tj + tl;
+                float *at = reg + tl * S::OUT_LD + lf;
+                const float4 x = reinterpret_cast<const float4 *>(at)[0], y = reinterpret_cast<const float4 *>(at)[1];
+                float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                if constexpr (SYM) {
+                    if (piece) {
+                        float4 *o = reinterpret_cast<float4 *>(
+                            g.part + ((2ll * w + (kbeg == 0 ? 1 : 0)) * S::BT + (t - t0)) * S::BF + (f - f0));
+                        o[0] = x;
+                        o[1] = y;
+                        continue;
+                    }
+                    symmetric_values<EPI>(g, z, t, f, hi[p], et[p], df, v);
+                    *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+                } else {
+                    float was[8];
+                    unpack(hi[p], lo[p], g.down, was);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] = fmaf(et[p], was[u], v[u] * (1.0f / kScaleB));
+                    if constexpr (EPI == APPLY) {
+                        const int64_t h_at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
+                        *reinterpret_cast<u32x4 *>(g.hi + h_at) = pack_h8(v);
+                        *reinterpret_cast<uint2 *>(g.lo + h_at) = pack_rest(v, g.up);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] *= g.inv;
+                        if (!g.tall && t < g.r) {
+                            uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + static_cast<int64_t>(t) * g.ldout + f;
+                            if (f + 8 <= g.cols) {
+                                *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    if (f + u < g.cols) Elt<true>::store_one(o, u, v[u]);
+                            }
+                        }
+                    }
+                }
+                if (turned) {
+                    reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (turned && tj < g.rows_x) {   // four lanes a feature, eight of its 32 tokens each
 #pragma unroll 2
             for (int q = 0; q < FI * 2; ++q) {
                 const int fl = q * 16 + (lane >> 2), tl = (lane & 3) * 8;
@@ -454,32 +540,56 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
         __builtin_amdgcn_wave_barrier();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
+    left -= nsteps;
+    ++tile;
+    s0 = 0;
+    if (left > 0) __syncthreads();   // the sums are out of LDS before the next tile's operands come in
+    }
 }
 
-// The partial sums of A's K splits, added in their order, 64 x 64 values on or below the diagonal a
-// workgroup, stored as they are and transposed.
-__global__ __launch_bounds__(256) void gram_fold_kernel(Args g) {
-    __shared__ float tile[64][65];
-    const int z = blockIdx.y, mn = blockIdx.x, th = threadIdx.x;
-    int ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(mn) + 1.0f) - 1.0f) * 0.5f);
-    while (ti * (ti + 1) / 2 > mn) --ti;
-    while ((ti + 1) * (ti + 2) / 2 <= mn) ++ti;
-    const int fi = mn - ti * (ti + 1) / 2;
-    const int64_t one = static_cast<int64_t>(g.rows_x) * g.rows_x;
+// The pieces of the tiles that more than one workgroup had, added in the order of their steps, 64 x 64 values
+// a workgroup, stored as they are and, off the diagonal, transposed.
+template <int SIDE, int EPI>
+__global__ __launch_bounds__(256) void fold_kernel(Args g) {
+    constexpr int PARTS = SIDE / 64;
+    __shared__ float turn[64][65];
+    const int tile = blockIdx.x / (PARTS * PARTS), part = blockIdx.x % (PARTS * PARTS), th = threadIdx.x;
+    const int64_t units = static_cast<int64_t>(g.total) * g.steps, from = static_cast<int64_t>(tile) * g.steps;
+    // the last range that starts at or before a unit u is ceil((u + 1) groups / units) - 1
+    auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * g.groups + units - 1) / units) - 1; };
+    const int first = owner(from), last = owner(from + g.steps - 1);
+    if (first == last) return;
+    const int z = tile / g.per_batch;
+    int ti, fi;
+    triangle(tile - z * g.per_batch, ti, fi);
+    const int t0 = ti * SIDE + part / PARTS * 64, f0 = fi * SIDE + part % PARTS * 64;
+    if (t0 >= g.rows_x || f0 >= g.rows_w) return;   // rows come in 64s
+    const int first_slot = 2 * first + (range_start(units, g.groups, first) <= from ? 1 : 0);
+    const float *dz = g.d + static_cast<int64_t>(z) * g.rows_x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int tl = i * 32 + (th >> 3), fl = (th & 7) * 8, t = ti * 64 + tl, f = fi * 64 + fl;
-        const float *p = g.part + static_cast<int64_t>(z) * g.splits * one + static_cast<int64_t>(t) * g.rows_x + f;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int k = 0; k < g.splits; ++k) {
-            const float4 x = reinterpret_cast<const float4 *>(p + k * one)[0], y = reinterpret_cast<const float4 *>(p + k * one)[1];
+        const int tl = i * 32 + (th >> 3), fl = (th & 7) * 8, t = t0 + tl, f = f0 + fl;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, df[8] = {};
+        for (int k = first; k <= last; ++k) {
+            const int64_t slot = k == first ? first_slot : 2 * k;
+            const float4 *p = reinterpret_cast<const float4 *>(
+                g.part + (slot * SIDE + part / PARTS * 64 + tl) * SIDE + part % PARTS * 64 + fl);
+            const float4 x = p[0], y = p[1];
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
             v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
         }
-        symmetric_values<GRAM>(g, z, t, f, v);
-        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+        u32x4 o = {0u, 0u, 0u, 0u};
+        float dt = 0.0f;
+        if constexpr (EPI == POLY) {
+            o = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
+            dt = dz[t];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) tile[tl][fl + u] = v[u];
+            for (int u = 0; u < 8; ++u) df[u] = dz[f + u];
+        }
+        symmetric_values<EPI>(g, z, t, f, o, dt, df, v);
+        *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) turn[tl][fl + u] = v[u];
     }
     if (ti == fi) return;
     __syncthreads();
@@ -488,8 +598,8 @@ __global__ __launch_bounds__(256) void gram_fold_kernel(Args g) {
         const int fl = i * 32 + (th >> 3), tl = (th & 7) * 8;
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = tile[tl + u][fl];
-        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(fi * 64 + fl) * g.ldo + ti * 64 + tl) = pack_h8(v);
+        for (int u = 0; u < 8; ++u) v[u] = turn[tl + u][fl];
+        *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(f0 + fl) * g.ldo + t0 + tl) = pack_h8(v);
     }
 }
 
@@ -503,32 +613,42 @@ constexpr int kSide[SHAPES] = {256, 128, 64}, kThreads[SHAPES] = {512, 256, 256}
 static_assert(Big::BF == 256 && Mid::BF == 128 && Small::BF == 64, "sides");
 // us of a step of K with as many workgroups per CU as fit, of a tile's start and end
 constexpr double kStepUs[SHAPES] = {1.25, 0.70, 0.30}, kTileUs[SHAPES] = {9.0, 6.0, 4.0};
-constexpr int kCus = 256, kMaxSplits = 16;
+constexpr int kCus = 256;
 
 struct Plan {
-    int shape, splits;
-    int64_t tiles;   // of one matrix, one split
+    int shape, groups;
+    int64_t tiles, total;   // of one matrix, of the batch
 };
 int64_t tiles_of(int64_t rows_x, int64_t rows_w, int side, bool sym) {
     const int64_t t = ceil_div(rows_x, side);
     return sym ? t * (t + 1) / 2 : t * ceil_div(rows_w, side);
 }
-Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool sym, bool split) {
-    Plan best{SMALL, 1, 0};
+// The shape with the least estimated time, a workgroup a tile; or (symmetric products) as many workgroups as
+// fit on the card, with equal ranges of all steps, which costs each two ends and the launch that adds the
+// pieces up.
+Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool sym) {
+    Plan best{SMALL, 0, 0, 0};
     double best_us = 1e30;
     for (int i = 0; i < SHAPES; ++i) {
-        const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym);
-        for (int sp = 1; sp <= (split ? kMaxSplits : 1) && (sp == 1 || steps / sp >= 4); ++sp) {
-            const int64_t groups = batch * tiles * sp, slots = static_cast<int64_t>(kCus) * kPerCu[i];
-            double us = static_cast<double>(ceil_div(groups, slots)) * (static_cast<double>(ceil_div(steps, sp)) * kStepUs[i] + kTileUs[i]);
-            if (sp > 1) us += 4.0 + static_cast<double>(batch) * sp * rows_x * rows_x * 4 / 3e6;
-            if (us < best_us - 1e-9) {
-                best_us = us;
-                best = {i, sp, tiles};
-            }
+        const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym), total = batch * tiles, slots = static_cast<int64_t>(kCus) * kPerCu[i];
+        const double whole = static_cast<double>(ceil_div(total, slots)) * (static_cast<double>(steps) * kStepUs[i] + kTileUs[i]);
+        if (whole < best_us - 1e-9) {
+            best_us = whole;
+            best = {i, static_cast<int>(total), tiles, total};
+        }
+        const int64_t groups = std::min(slots, total * steps / 4);
+        if (!sym || groups == total || groups < 1) continue;
+        const double depth = static_cast<double>(ceil_div(total * steps, groups)), pieces = static_cast<double>(std::min(2 * total, total + groups));
+        const double even = depth * kStepUs[i] + 2.0 * kTileUs[i] + 4.0 + pieces * kSide[i] * kSide[i] * 8 / 4e6;
+        if (even < best_us - 1e-9) {
+            best_us = even;
+            best = {i, static_cast<int>(groups), tiles, total};
         }
     }
     return best;
+}
+size_t piece_bytes(const Plan &p) {
+    return p.groups == p.total ? 0 : static_cast<size_t>(p.groups) * 2 * kSide[p.shape] * kSide[p.shape] * 4;
 }
 
 struct Layout {
@@ -546,14 +666,14 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     L.cp = round_up(L.c, kUnit);
     L.ldx = apart(L.cp);
     L.ldr = apart(L.rp);
-    L.gram = plan_of(batch, L.rp, L.rp, L.cp / kUnit, true, true);
-    L.poly = plan_of(batch, L.rp, L.rp, L.rp / kUnit, true, false);
-    L.apply = plan_of(batch, L.rp, L.cp, L.rp / kUnit, false, false);
+    L.gram = plan_of(batch, L.rp, L.rp, L.cp / kUnit, true);
+    L.poly = plan_of(batch, L.rp, L.rp, L.rp / kUnit, true);
+    L.apply = plan_of(batch, L.rp, L.cp, L.rp / kUnit, false);
     const size_t x = align256(static_cast<size_t>(batch) * L.rp * L.ldx * 2), t = align256(static_cast<size_t>(batch) * L.cp * L.ldr * 2);
     const size_t s = align256(static_cast<size_t>(batch) * L.rp * L.ldr * 2), v = align256(static_cast<size_t>(batch) * L.rp * 4);
     size_t o = 0;
     L.off_hi = o;    o += x;
-    L.off_lo = o;    o += x;
+    L.off_lo = o;    o += x / 2;
     L.off_t0 = o;    o += t;
     L.off_t1 = o;    o += t;
     L.off_o = o;     o += s;
@@ -562,25 +682,36 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     L.off_e = o;     o += v;
     L.off_norm = o;  o += align256(static_cast<size_t>(batch) * kNormGroups * 8);
     L.off_part = o;
-    if (L.gram.splits > 1) o += align256(static_cast<size_t>(batch) * L.gram.splits * L.rp * L.rp * 4);
+    o += std::max(piece_bytes(L.gram), piece_bytes(L.poly));
     L.bytes = o;
     return L;
 }
 
-template <int EPI>
-hipError_t launch_product(Args g, const Plan &p, int64_t batch, hipStream_t st) {
-    g.splits = p.splits;
-    g.per_batch = static_cast<int>(p.tiles * p.splits);
-    g.total = static_cast<int>(batch * p.tiles * p.splits);
-    g.tiles_f = static_cast<int>(ceil_div(g.rows_w, kSide[p.shape]));
-    g.per_xcd = static_cast<int>(ceil_div(g.total, 8));
-    const dim3 grid(static_cast<unsigned>(g.per_xcd) * 8u), block(kThreads[p.shape]);
-    switch (p.shape) {
-        case BIG: hipLaunchKernelGGL((ortho_kernel<Big, EPI>), grid, block, 0, st, g); break;
-        case MID: hipLaunchKernelGGL((ortho_kernel<Mid, EPI>), grid, block, 0, st, g); break;
-        default: hipLaunchKernelGGL((ortho_kernel<Small, EPI>), grid, block, 0, st, g); break;
+template <class S, int EPI>
+hipError_t launch_tiles(const Args &g, hipStream_t st) {
+    hipLaunchKernelGGL((ortho_kernel<S, EPI>), dim3(static_cast<unsigned>(g.per_xcd) * 8u), dim3(64 * S::NW), 0, st, g);
+    if constexpr (EPI == GRAM || EPI == POLY) {
+        if (g.groups != g.total) {
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            constexpr int parts = S::BF / 64 * (S::BF / 64);
+            hipLaunchKernelGGL((fold_kernel<S::BF, EPI>), dim3(static_cast<unsigned>(g.total) * parts), dim3(256), 0, st, g);
+        }
     }
     return hipGetLastError();
+}
+template <int EPI>
+hipError_t launch_product(Args g, const Plan &p, hipStream_t st) {
+    g.groups = p.groups;
+    g.per_batch = static_cast<int>(p.tiles);
+    g.total = static_cast<int>(p.total);
+    g.tiles_f = static_cast<int>(ceil_div(g.rows_w, kSide[p.shape]));
+    g.per_xcd = static_cast<int>(ceil_div(g.groups, 8));
+    switch (p.shape) {
+        case BIG: return launch_tiles<Big, EPI>(g, st);
+        case MID: return launch_tiles<Mid, EPI>(g, st);
+        default: return launch_tiles<Small, EPI>(g, st);
+    }
 }
 
 }  // namespace
@@ -605,7 +736,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     l.cols = a.cols;
     l.part = reinterpret_cast<double *>(ws + L.off_norm);
     l.hi = half(L.off_hi);
-    l.lo = half(L.off_lo);
+    l.lo = reinterpret_cast<unsigned char *>(ws + L.off_lo);
     l.xt = half(L.off_t0);
     l.ldx = L.ldx;
     l.ldt = L.ldr;
@@ -615,8 +746,12 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     l.cp = static_cast<int>(L.cp);
     l.tall = tall;
     l.s = s;
+    l.up = ldexpf(1.0f, 19) / s;   // |X| up to 1.3: the rest, half a step of fp16, stays below 448
     l.eps = a.eps;
-    const dim3 norm_grid(kNormGroups, static_cast<unsigned>(a.batch));
+    // a workgroup a piece of 2048 values, up to 1024 of them a matrix and about as many for a batch
+    const int64_t pieces = a.rows * ceil_div(a.cols, 2048);
+    l.groups = static_cast<int>(std::min(pieces, std::max<int64_t>(64, kNormGroups / a.batch)));
+    const dim3 norm_grid(static_cast<unsigned>(l.groups), static_cast<unsigned>(a.batch));
     const dim3 load_grid(static_cast<unsigned>(L.cp / 64), static_cast<unsigned>(L.rp / 64), static_cast<unsigned>(a.batch));
     hipError_t e;
     if (a.g_bf16) hipLaunchKernelGGL((norm_kernel<true>), norm_grid, dim3(256), 0, st, l);
@@ -640,6 +775,8 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     g.c = a.c;
     g.hi = l.hi;
     g.lo = l.lo;
+    g.up = l.up;
+    g.down = 1.0f / l.up;
     g.ldh = L.ldx;
     g.hb = l.xb;
     g.ldt = L.ldr;
@@ -657,27 +794,20 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         g.rows_w = static_cast<int>(L.rp);
         g.steps = static_cast<int>(L.cp / kUnit);
         g.inv = 1.0f / (s * s);
-        if ((e = launch_product<GRAM>(g, L.gram, a.batch, st)) != hipSuccess) return e;
-        if (L.gram.splits > 1) {
-            g.splits = L.gram.splits;
-            const int64_t blocks = L.rp / 64;
-            hipLaunchKernelGGL(gram_fold_kernel, dim3(static_cast<unsigned>(blocks * (blocks + 1) / 2), static_cast<unsigned>(a.batch)),
-                               dim3(256), 0, st, g);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        if ((e = launch_product<GRAM>(g, L.gram, st)) != hipSuccess) return e;
         g.w = g.x = g.o;
         g.ldw = g.ldx = L.ldr;
         g.wb = g.xb = g.ob;
         g.steps = static_cast<int>(L.rp / kUnit);
         g.inv = 1.0f / (kScaleO * kScaleO);
-        if ((e = launch_product<POLY>(g, L.poly, a.batch, st)) != hipSuccess) return e;
+        if ((e = launch_product<POLY>(g, L.poly, st)) != hipSuccess) return e;
         g.x = g.bo;
         g.w = half(k & 1 ? L.off_t1 : L.off_t0);
         g.xt = half(k & 1 ? L.off_t0 : L.off_t1);
         g.wb = l.tb;
         g.rows_w = static_cast<int>(L.cp);
         g.inv = 1.0f / s;
-        e = k + 1 < a.steps ? launch_product<APPLY>(g, L.apply, a.batch, st) : launch_product<LAST>(g, L.apply, a.batch, st);
+        e = k + 1 < a.steps ? launch_product<APPLY>(g, L.apply, st) : launch_product<LAST>(g, L.apply, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
