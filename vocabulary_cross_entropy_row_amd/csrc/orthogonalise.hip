@@ -260,6 +260,56 @@ __device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, in
     }
 }
 
+// APPLY and LAST: the product's values v of eight features of a token to X' in all its forms, but for the
+// transposed one.  LAST leaves what the output's transpose holds in v.
+template <int EPI>
+__device__ __forceinline__ void apply_values(const Args &g, int z, int t, int f, u32x4 hi, uint2 lo, float et, float (&v)[8]) {
+    float was[8];
+    unpack(hi, lo, g.down, was);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = fmaf(et, was[u], v[u] * (1.0f / kScaleB));
+    if constexpr (EPI == APPLY) {
+        const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
+        *reinterpret_cast<u32x4 *>(g.hi + at) = pack_h8(v);
+        *reinterpret_cast<uint2 *>(g.lo + at) = pack_rest(v, g.up);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= g.inv;
+        if (!g.tall && t < g.r) {
+            uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + static_cast<int64_t>(t) * g.ldout + f;
+            if (f + 8 <= g.cols) {
+                *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (f + u < g.cols) Elt<true>::store_one(o, u, v[u]);
+            }
+        }
+    }
+}
+// Eight tokens of one feature: the mirrored tile, X^T, or a row of a tall output
+template <int EPI>
+__device__ __forceinline__ void turned_values(const Args &g, int z, int64_t row, int t, const float (&v)[8]) {
+    if constexpr (EPI == GRAM || EPI == POLY) {
+        *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + row * g.ldo + t) = pack_h8(v);
+    } else if constexpr (EPI == APPLY) {
+        *reinterpret_cast<u32x4 *>(g.xt + z * g.tb + row * g.ldt + t) = pack_h8(v);
+    } else if (row < g.cols) {
+        uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + row * g.ldout + t;
+        if (t + 8 <= g.r) {
+            *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (t + u < g.r) Elt<true>::store_one(o, u, v[u]);
+        }
+    }
+}
+template <int EPI>
+__device__ __forceinline__ void symmetric_store(const Args &g, int z, int t, int f, const float (&v)[8]) {
+    *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+}
+
 // The steps of all tiles are one sequence, cut into equal ranges: the unit at which range i of n starts
 __device__ __forceinline__ int64_t range_start(int64_t units, int n, int i) { return units * i / n; }
 
@@ -479,30 +529,9 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
                         continue;
                     }
                     symmetric_values<EPI>(g, z, t, f, hi[p], et[p], df, v);
-                    *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+                    symmetric_store<EPI>(g, z, t, f, v);
                 } else {
-                    float was[8];
-                    unpack(hi[p], lo[p], g.down, was);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) v[u] = fmaf(et[p], was[u], v[u] * (1.0f / kScaleB));
-                    if constexpr (EPI == APPLY) {
-                        const int64_t h_at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
-                        *reinterpret_cast<u32x4 *>(g.hi + h_at) = pack_h8(v);
-                        *reinterpret_cast<uint2 *>(g.lo + h_at) = pack_rest(v, g.up);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] *= g.inv;
-                        if (!g.tall && t < g.r) {
-                            uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + static_cast<int64_t>(t) * g.ldout + f;
-                            if (f + 8 <= g.cols) {
-                                *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
-                            } else {
-#pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    if (f + u < g.cols) Elt<true>::store_one(o, u, v[u]);
-                            }
-                        }
-                    }
+                    apply_values<EPI>(g, z, t, f, hi[p], lo[p], et[p], v);
                 }
                 if (turned) {
                     reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -521,20 +550,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
                 float v[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v[u] = reg[(tl + u) * S::OUT_LD + fl];
-                if constexpr (SYM) {
-                    *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + row * g.ldo + tj + tl) = pack_h8(v);
-                } else if constexpr (EPI == APPLY) {
-                    *reinterpret_cast<u32x4 *>(g.xt + z * g.tb + row * g.ldt + tj + tl) = pack_h8(v);
-                } else if (row < g.cols) {
-                    uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + row * g.ldout + tj + tl;
-                    if (tj + tl + 8 <= g.r) {
-                        *reinterpret_cast<any16 *>(o) = Elt<true>::pack(v);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            if (tj + tl + u < g.r) Elt<true>::store_one(o, u, v[u]);
-                    }
-                }
+                turned_values<EPI>(g, z, row, tj + tl, v);
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -544,6 +560,114 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     ++tile;
     s0 = 0;
     if (left > 0) __syncthreads();   // the sums are out of LDS before the next tile's operands come in
+    }
+}
+
+// ---- small products ----------------------------------------------------------------------------
+//
+// Where the tiles above are few and short, a launch is their loads, barriers and chained instructions one
+// after the other.  Here a workgroup takes 32 x 32 values, its eight waves an eighth of K each, straight
+// from memory to the registers of the matrix instruction, all of it asked for at once up to K = 1024; the
+// waves' sums meet in LDS and are added in wave order.
+constexpr int kFineWaves = 8;
+
+template <int EPI>
+__global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
+    constexpr bool SYM = EPI == GRAM || EPI == POLY;
+    constexpr int U = 8, LD = 36;   // instructions' operands at once; floats between tokens
+    __shared__ __attribute__((aligned(16))) float sums[kFineWaves][32 * LD];
+    const int w = (blockIdx.x & 7) * g.per_xcd + (blockIdx.x >> 3);
+    if (static_cast<int>(blockIdx.x >> 3) >= g.per_xcd || w >= g.total) return;
+    const int z = w / g.per_batch, mn = w - z * g.per_batch;
+    int ti, fi;
+    if constexpr (SYM) {
+        triangle(mn, ti, fi);
+    } else {
+        ti = mn / g.tiles_f;
+        fi = mn - ti * g.tiles_f;
+    }
+    const int t0 = ti * 32, f0 = fi * 32, th = threadIdx.x, lane = th & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(th >> 6);
+    // the finishing threads' operands: 128 threads, eight features of a token each
+    const int t = t0 + (th >> 2), f = f0 + (th & 3) * 8;
+    u32x4 hi = {0u, 0u, 0u, 0u};
+    uint2 lo = make_uint2(0u, 0u);
+    float et = 0.0f, df[8] = {};
+    if (th < 128 && EPI != GRAM) {
+        const int64_t row = static_cast<int64_t>(z) * g.rows_x;
+        if constexpr (EPI == POLY) {
+            hi = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
+            et = g.d[row + t];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) df[u] = g.d[row + f + u];
+        } else {
+            const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
+            hi = *reinterpret_cast<const u32x4 *>(g.hi + at);
+            lo = *reinterpret_cast<const uint2 *>(g.lo + at);
+            et = g.e[row + t];
+        }
+    }
+    const uint16_t *wrow = g.w + z * g.wb + static_cast<int64_t>(f0 + (lane & 31)) * g.ldw + half * 8;
+    const uint16_t *xrow = g.x + z * g.xb + static_cast<int64_t>(t0 + (lane & 31)) * g.ldx + half * 8;
+    const int total = g.steps * 4;   // of 16 values of K
+    const int beg = static_cast<int>(static_cast<int64_t>(total) * wave / kFineWaves);
+    const int end = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / kFineWaves);
+    auto fetch = [&](int s, h8 (&a)[U], h8 (&b)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u < end) {
+                a[u] = *reinterpret_cast<const h8 *>(wrow + (s + u) * 16);
+                b[u] = *reinterpret_cast<const h8 *>(xrow + (s + u) * 16);
+            }
+        }
+    };
+    f16v acc[2] = {(f16v){}, (f16v){}};   // two chains
+    auto use = [&](int s, h8 (&a)[U], h8 (&b)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u < end) acc[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[u], b[u], acc[u & 1], 0, 0, 0);
+    };
+    h8 a0[U], b0[U], a1[U], b1[U];
+    fetch(beg, a0, b0);
+    for (int s = beg; s < end; s += 2 * U) {
+        fetch(s + U, a1, b1);
+        use(s, a0, b0);
+        fetch(s + 2 * U, a0, b0);
+        use(s + U, a1, b1);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4 *>(&sums[wave][(lane & 31) * LD + (r >> 2) * 8 + half * 4]) =
+            make_float4(acc[0][r] + acc[1][r], acc[0][r + 1] + acc[1][r + 1], acc[0][r + 2] + acc[1][r + 2], acc[0][r + 3] + acc[1][r + 3]);
+    __syncthreads();
+    const bool turned = EPI == APPLY || (SYM && ti != fi) || (EPI == LAST && g.tall);
+    if (th < 128) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        const int at = (th >> 2) * LD + (th & 3) * 8;
+#pragma unroll
+        for (int k = 0; k < kFineWaves; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sums[k][at]), y = *reinterpret_cast<const float4 *>(&sums[k][at + 4]);
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        }
+        if constexpr (SYM) {
+            symmetric_values<EPI>(g, z, t, f, hi, et, df, v);
+            symmetric_store<EPI>(g, z, t, f, v);
+        } else {
+            apply_values<EPI>(g, z, t, f, hi, lo, et, v);
+        }
+        if (turned) {   // each thread's own place of the first wave's sums
+            *reinterpret_cast<float4 *>(&sums[0][at]) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(&sums[0][at + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    if (!turned) return;
+    __syncthreads();
+    if (th < 128) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = sums[0][((th & 3) * 8 + u) * LD + (th >> 2)];
+        turned_values<EPI>(g, z, f0 + (th >> 2), t0 + (th & 3) * 8, v);
     }
 }
 
@@ -605,14 +729,22 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
 
 // ---- plan and launches ---------------------------------------------------------------------------
 
-using Big = linear::Shape<256, 256, 2, 4, 3, 2>;    // one workgroup of eight waves per CU
-using Mid = linear::Shape<128, 128, 2, 2, 2, 2>;    // two of four
-using Small = linear::Shape<64, 64, 2, 2, 4, 4>;    // two of four
-enum { BIG, MID, SMALL, SHAPES };
-constexpr int kSide[SHAPES] = {256, 128, 64}, kThreads[SHAPES] = {512, 256, 256}, kPerCu[SHAPES] = {1, 2, 2};
-static_assert(Big::BF == 256 && Mid::BF == 128 && Small::BF == 64, "sides");
-// us of a step of K with as many workgroups per CU as fit, of a tile's start and end
-constexpr double kStepUs[SHAPES] = {1.25, 0.70, 0.30}, kTileUs[SHAPES] = {9.0, 6.0, 4.0};
+using Big = linear::Shape<256, 256, 2, 4, 3, 2>;        // one workgroup of eight waves per CU
+using Mid = linear::Shape<128, 128, 2, 2, 2, 2>;        // two of four
+using Small = linear::Shape<64, 64, 2, 2, 4, 4>;        // two of four
+using MidDeep = linear::Shape<128, 128, 2, 2, 5, 4>;    // one of four, with more steps in flight
+enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
+constexpr int kSide[SHAPES] = {256, 128, 64, 128, 32}, kPerCu[SHAPES] = {1, 2, 2, 1, 2};
+static_assert(Big::BF == 256 && Mid::BF == 128 && Small::BF == 64 && MidDeep::BF == 128 && Big::PER_CU == 1 && Mid::PER_CU == 2 &&
+              Small::PER_CU == 2 && MidDeep::PER_CU == 1,
+              "the plan's tiles are the kernels'");
+// us of a step of K with one and two workgroups on a compute unit, and of a tile's start and end.  Fitted
+// to the times of all five steps over 260 random shapes (batches of 1 to 16, 32 to 16384 rows and columns)
+// with each shape for each product, replayed from a graph: off by 12% (root mean square), and the choice
+// that the estimates make 3% slower than the fastest measured one on geometric average.
+constexpr double kStepUs[SHAPES][2] = {{1.03, 0}, {0.65, 0.94}, {0.33, 0.33}, {0.45, 0}, {0.27, 0.57}};
+constexpr double kTileUs[SHAPES] = {6.9, 3.4, 2.1, 4.3, 2.1};
+constexpr double kEven = 1.94;   // a step where workgroups are at different places of K and share little in the caches
 constexpr int kCus = 256;
 
 struct Plan {
@@ -631,15 +763,16 @@ Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool 
     double best_us = 1e30;
     for (int i = 0; i < SHAPES; ++i) {
         const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym), total = batch * tiles, slots = static_cast<int64_t>(kCus) * kPerCu[i];
-        const double whole = static_cast<double>(ceil_div(total, slots)) * (static_cast<double>(steps) * kStepUs[i] + kTileUs[i]);
+        double whole = static_cast<double>(total / slots) * (static_cast<double>(steps) * kStepUs[i][kPerCu[i] - 1] + kTileUs[i]);
+        if (total % slots) whole += static_cast<double>(steps) * kStepUs[i][ceil_div(total % slots, kCus) - 1] + kTileUs[i];
         if (whole < best_us - 1e-9) {
             best_us = whole;
             best = {i, static_cast<int>(total), tiles, total};
         }
         const int64_t groups = std::min(slots, total * steps / 4);
-        if (!sym || groups == total || groups < 1) continue;
+        if (!sym || i == FINE || groups == total || groups < 1) continue;
         const double depth = static_cast<double>(ceil_div(total * steps, groups)), pieces = static_cast<double>(std::min(2 * total, total + groups));
-        const double even = depth * kStepUs[i] + 2.0 * kTileUs[i] + 4.0 + pieces * kSide[i] * kSide[i] * 8 / 4e6;
+        const double even = depth * kStepUs[i][ceil_div(groups, kCus) - 1] * kEven + 2.0 * kTileUs[i] + 1.1 + pieces * kSide[i] * kSide[i] * 8 / 25e6;
         if (even < best_us - 1e-9) {
             best_us = even;
             best = {i, static_cast<int>(groups), tiles, total};
@@ -710,6 +843,10 @@ hipError_t launch_product(Args g, const Plan &p, hipStream_t st) {
     switch (p.shape) {
         case BIG: return launch_tiles<Big, EPI>(g, st);
         case MID: return launch_tiles<Mid, EPI>(g, st);
+        case MID_DEEP: return launch_tiles<MidDeep, EPI>(g, st);
+        case FINE:
+            hipLaunchKernelGGL((fine_kernel<EPI>), dim3(static_cast<unsigned>(g.per_xcd) * 8u), dim3(64 * kFineWaves), 0, st, g);
+            return hipGetLastError();
         default: return launch_tiles<Small, EPI>(g, st);
     }
 }
