@@ -58,6 +58,10 @@ __device__ __forceinline__ u32x4 pack_h8(const float (&v)[8]) {
 }
 
 typedef float f2v __attribute__((ext_vector_type(2)));
+// Holds a matrix instruction to its place in the order of the code (blocks_mfma.h).  In the accumulation
+// registers: where a wave has more than 256, the compiler keeps sums there, and copies them both ways for
+// a place in the vector registers (2048 x 2048 in all: 886 us for 380).
+__device__ __forceinline__ void pin(f16v &v) { asm volatile("" : "+a"(v)::"memory"); }
 // What fp16 leaves of eight values, in e4m3 times `up`
 __device__ __forceinline__ uint2 pack_rest(const float (&v)[8], float up) {
     float r[8];
@@ -371,99 +375,106 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     const int fr = min(S::BF, g.rows_w - f0), tr = min(S::BT, g.rows_x - t0);
     const __amdgpu_buffer_rsrc_t rsA = uniform_rsrc(g.w + z * g.wb + f0 * g.ldw, (fr - 1) * ldw + kbytes);
     const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(g.x + z * g.xb + t0 * g.ldx, (tr - 1) * ldx + kbytes);
-    auto load_a = [&](int step, int slot_a) {
-#pragma unroll
-        for (int j = 0; j < LA; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)(lds + slot_a * S::A_BYTES + (j * S::NW + wave) * 1024), 16,
-                                                     voffA[j], step * kStep, 0, 0);
-    };
-    auto load_b = [&](int step, int slot_b) {
-#pragma unroll
-        for (int j = 0; j < LB; ++j)
+    const int last = nsteps - 1;
+    // request q of a step: w of step sw, then x of step sx
+    auto request = [&](int sw, int sx, int slot_a, int slot_b, int q) {
+        if (q < LA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsA, (lds_ptr)(lds + slot_a * S::A_BYTES + (q * S::NW + wave) * 1024), 16,
+                                                     voffA[q < LA ? q : 0], (kbeg + min(sw, last)) * kStep, 0, 0);
+        else if (q < LA + LB)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsB, (lds_ptr)(lds + SA * S::A_BYTES + slot_b * S::B_BYTES + (j * S::NW + wave) * 1024), 16, voffB[j],
-                step * kStep, 0, 0);
+                rsB, (lds_ptr)(lds + SA * S::A_BYTES + slot_b * S::B_BYTES + ((q - LA) * S::NW + wave) * 1024), 16,
+                voffB[q < LA ? 0 : q - LA], (kbeg + min(sx, last)) * kStep, 0, 0);
     };
-    auto read_frags = [&](int slot_a, int slot_b, int kk, h8 *af, h8 *bf) {
-        const unsigned char *At = lds + slot_a * S::A_BYTES, *Bt = lds + SA * S::A_BYTES + slot_b * S::B_BYTES;
-#pragma unroll
-        for (int i = 0; i < FI; ++i) {
-            const int r = (wf * FI + i) * 32 + (lane & 31);
-            af[i] = *reinterpret_cast<const h8 *>(At + r * kStep + ((kk * 2 + half) ^ swz(r)) * 16);
-        }
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const int r = (wt * TJ + j) * 32 + (lane & 31);
-            bf[j] = *reinterpret_cast<const h8 *>(Bt + r * kStep + ((kk * 2 + half) ^ swz(r)) * 16);
-        }
+    auto frag = [&](const unsigned char *tile_at, int q, int kk) {   // 32-row tile q, instruction kk of the step
+        const int r = q * 32 + (lane & 31);
+        return *reinterpret_cast<const h8 *>(tile_at + r * kStep + ((kk * 2 + half) ^ swz(r)) * 16);
     };
-    // Spread the next sub-step's LDS reads, and in sub-step 0 the loads, between the MFMAs.
-    auto interleave = [&](int kk) {
-        constexpr int NM = FI * TJ, NR = FI + TJ, NS = NM > 2 ? NM - 2 : NM;
-        if constexpr (NM >= 4) {
-#pragma unroll
-            for (int q = 0; q < NM; ++q) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // MFMA
-                const int nr = q < NS ? NR / NS + (q < NR % NS ? 1 : 0) : 0;
-                if (nr == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);          // LDS reads
-                else if (nr == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                if (kk == 0 && q < LA + LB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // VMEM read
-            }
-        }
-    };
-
+    // The schedule of blocks_kernel (blocks_mfma.h): requests run ahead by as many steps as LDS holds and are
+    // spread over a step; past the last step they ask for the last one again.  With two or more tiles of
+    // features to a wave, x of step s + SB takes the place of step s's once every wave has that in registers.
+    constexpr bool EARLY = FI >= 2;
+    static_assert(SA == SB + (EARLY ? 1 : 0), "both operands' requests of a step are for the same wait");
+    constexpr int AHEAD = EARLY ? SB : SB - 1;   // steps
+    constexpr int PER = (LA + LB + FI - 1) / FI, FIRST_X = LA / PER > 0 ? LA / PER : 1;
+    constexpr int BEFORE = (FI - 1) * PER < LA + LB ? (FI - 1) * PER : LA + LB;
+    // when a step ends, what it (its first groups) and the AHEAD - 2 before it asked for may be outstanding
+    // while the next is whole
+    constexpr int LEFT = EARLY ? (AHEAD - 2) * (LA + LB) + BEFORE : (AHEAD - 1) * (LA + LB);
+    static_assert((!EARLY || FIRST_X * PER <= LA) && LEFT < 64 && LEFT >= 0, "requests");
     f16v acc[FI][TJ];
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = (f16v){};
-    h8 a0[FI], b0[TJ], a1[FI], b1[TJ];
-    // The order of requests, and how many may be outstanding when a step ends, are linear_kernel's.
-    constexpr int LEFT = (SB - 2) * (LA + LB) + (SA > SB ? LA : 0);
-    static_assert(LEFT < 64, "vmcnt");
-    for (int s = 1 - SA; s < 0; ++s) {
-        const int tb = s + SB - 1, ta = s + SA - 1;
-        if (tb >= 0 && tb < nsteps) load_b(kbeg + tb, tb % SB);
-        if (ta < nsteps) load_a(kbeg + ta, ta % SA);
+    h8 b[TJ][KK], a[2][KK];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+#pragma unroll
+        for (int q = 0; q < LA + LB; ++q) request(s, s, s, s, q);
+    auto hand_over = [&]() {   // the next step is whole in LDS, for every wave
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+    };
+    if constexpr (EARLY) {   // all of the first requests but the last step's
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((AHEAD - 1) * (LA + LB)) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+    } else {
+        hand_over();
     }
-    if (nsteps >= SA) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    asm volatile("s_barrier" ::: "memory");
-    read_frags(0, 0, 0, a0, b0);
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    int sa = 0, sb = 0;
-    auto one_step = [&](int s) {
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) b[j][kk] = frag(lds + SA * S::A_BYTES, wt * TJ + j, kk);
+        a[0][kk] = frag(lds, wf * FI, kk);
+    }
+    int sa = 0, sb = 0;   // slots of the present step
+    for (int s = 0; s < nsteps; ++s) {
         const int na = sa + 1 == SA ? 0 : sa + 1, nb = sb + 1 == SB ? 0 : sb + 1;
+        const int fa = sa == 0 ? SA - 1 : sa - 1, fb = EARLY ? sb : sb == 0 ? SB - 1 : sb - 1;   // free, or about to be
+        const unsigned char *At = lds + sa * S::A_BYTES;
+        const unsigned char *An = lds + na * S::A_BYTES, *Bn = lds + SA * S::A_BYTES + nb * S::B_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            const bool odd = kk & 1;
-            h8 *ac = odd ? a1 : a0, *bc = odd ? b1 : b0;
-            h8 *an = odd ? a0 : a1, *bn = odd ? b0 : b1;
+        for (int i = 0; i < FI; ++i) {
             __builtin_amdgcn_sched_barrier(0);
-            if (kk == 0) {
-                if (s + SB - 1 < nsteps) load_b(kbeg + s + SB - 1, sb == 0 ? SB - 1 : sb - 1);
-                if (s + SA - 1 < nsteps) load_a(kbeg + s + SA - 1, sa == 0 ? SA - 1 : sa - 1);
-            }
-            if (kk + 1 < KK) {
-                read_frags(sa, sb, kk + 1, an, bn);
-            } else {
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                if (s + SA - 1 < nsteps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
-                else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (EARLY && i == FIRST_X) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // b, which the first products have used
                 asm volatile("s_barrier" ::: "memory");
-                read_frags(na, nb, 0, an, bn);
+            }
+            if (i + 1 < FI) {
+#pragma unroll
+                for (int q = i * PER; q < (i + 1) * PER; ++q) request(s + SA - 1, s + AHEAD, fa, fb, q);
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) a[(i + 1) & 1][kk] = frag(At, wf * FI + i + 1, kk);
+            } else {
+                if constexpr (!EARLY) {
+#pragma unroll
+                    for (int q = 0; q < LA + LB; ++q) request(s + AHEAD, s + AHEAD, fa, fb, q);
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                hand_over();
+                if constexpr (EARLY) {
+#pragma unroll
+                    for (int q = i * PER; q < LA + LB; ++q) request(s + SA - 1, s + AHEAD, fa, fb, q);
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) a[FI & 1][kk] = frag(An, wf * FI, kk);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < FI; ++i)
+            for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ac[i], bc[j], acc[i][j], 0, 0, 0);
-            interleave(kk);
+                for (int j = 0; j < TJ; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i & 1][kk], b[j][kk], acc[i][j], 0, 0, 0);
+                    pin(acc[i][j]);
+                    if (i + 1 == FI) b[j][kk] = frag(Bn, wt * TJ + j, kk);
+                }
+                if (i + 1 == FI && !EARLY) a[0][kk] = frag(An, wf * FI, kk);
+            }
         }
         sa = na;
         sb = nb;
-    };
-    for (int s = 0; s < nsteps; ++s) one_step(s);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // epilogue: a wave's own LDS region, 32 tokens at a time, eight features of a token per lane; what it
     // reads of X or O for them is asked for all at once
@@ -730,7 +741,7 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
 // ---- plan and launches ---------------------------------------------------------------------------
 
 using Big = linear::Shape<256, 256, 2, 4, 3, 2>;        // one workgroup of eight waves per CU
-using Mid = linear::Shape<128, 128, 2, 2, 2, 2>;        // two of four
+using Mid = linear::Shape<128, 128, 2, 2, 3, 2>;        // two of four
 using Small = linear::Shape<64, 64, 2, 2, 4, 4>;        // two of four
 using MidDeep = linear::Shape<128, 128, 2, 2, 5, 4>;    // one of four, with more steps in flight
 enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
