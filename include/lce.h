@@ -585,6 +585,31 @@ lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, in
 size_t lce_linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M);
 
 /*
+ * Forward of the training form: quantises x (row blocks) and weight (tiles) from bf16 and
+ * takes their product,
+ *   out = Q(x) Q(weight)^T + bias + residual,
+ * as lce_quantize_blocks and lce_linear_blocks do one after the other.
+ *   x, weight     device bf16 [n, ldx], [M, ldw].
+ *   bias, residual, out  as for lce_linear_blocks.
+ *   xt, scale_xt  what lce_linear_blocks_backward reads for grad_weight: device e4m3 [K,
+ *                 ldxt] and e8m0 [ceil(K / 128), ceil(n / 128)] contiguous, or both NULL.
+ *   wt, scale_wt  the same for grad_x: [K, ldwt], [ceil(K / 128), ceil(M / 128)].
+ *   workspace     device, 256-byte aligned, lce_linear_blocks_forward_workspace_bytes(n,
+ *                 K, M) bytes.  Clobbered; calls that share it must not run at the same
+ *                 time.
+ * Sizes and alignments as for lce_linear_blocks_backward; outputs must not be an input or
+ * one another (LCE_ERR_INVALID_ARG), but out may be residual.  n == 0 is valid and writes
+ * wt.
+ */
+lce_status lce_linear_blocks_forward(const void *x, int64_t ldx, const void *weight, int64_t ldw, const void *bias,
+                                     lce_dtype bias_dtype, const void *residual, int64_t ldr, int64_t n, int64_t K,
+                                     int64_t M, void *out, int64_t ldo, void *xt, int64_t ldxt, void *scale_xt,
+                                     void *wt, int64_t ldwt, void *scale_wt, void *workspace, size_t workspace_bytes,
+                                     hipStream_t stream);
+
+size_t lce_linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M);
+
+/*
  * Backward of a product whose operands were quantised from x [n, K] (row blocks) and
  * weight [M, K] (tiles), straight through their rounding.  With Q the quantiser in row
  * blocks (e8m0 scales):

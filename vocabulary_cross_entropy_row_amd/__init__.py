@@ -108,6 +108,11 @@ def lib() -> ctypes.CDLL:
                                     i64, p, i64, p, sz, p]
     L.lce_linear_blocks_workspace_bytes.restype = sz
     L.lce_linear_blocks_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lce_linear_blocks_forward.restype = ci
+    L.lce_linear_blocks_forward.argtypes = [p, i64, p, i64, p, ci, p, i64, i64, i64, i64, p, i64, p, i64, p, p, i64, p, p, sz,
+                                            p]
+    L.lce_linear_blocks_forward_workspace_bytes.restype = sz
+    L.lce_linear_blocks_forward_workspace_bytes.argtypes = [i64, i64, i64]
     L.lce_linear_blocks_backward.restype = ci
     L.lce_linear_blocks_backward.argtypes = [p, i64, ci, p, i64, p, i64, i64, p, i64, p, i64, i64, i64, i64, i64, p, i64, p,
                                              p, ci, p, sz, p]

@@ -28,6 +28,8 @@ struct QuantizeArgs {
     float *part;             // column sums of each 128 rows, [ceil(n / 128)][K], or NULL
 };
 hipError_t launch_quantize_blocks(const QuantizeArgs &a, bool is_bf16, hipStream_t st);
+// Two bf16 matrices in one launch
+hipError_t launch_quantize_pair(const QuantizeArgs &a, const QuantizeArgs &b, hipStream_t st);
 
 // ---- product -------------------------------------------------------------------------
 
@@ -53,6 +55,23 @@ struct BlocksArgs {
 };
 size_t linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M);
 hipError_t launch_linear_blocks(const BlocksArgs &a, hipStream_t st);
+
+struct BlocksForwardArgs {
+    const void *x, *weight;  // bf16 [n, K], [M, K]
+    int64_t ldx, ldw, n, K, M;
+    const void *bias;        // [M] or NULL
+    bool bias_bf16;
+    const void *residual;    // [n, M] bf16, row stride ldr, or NULL
+    int64_t ldr;
+    void *out;               // [n, M] bf16, row stride ldo
+    int64_t ldo;
+    void *xt, *wt;           // e4m3 [K, n] and [K, M] in tiles, for the backward, or NULL
+    int64_t ldxt, ldwt;
+    void *scale_xt, *scale_wt;   // e8m0, contiguous
+    void *workspace;
+};
+size_t linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M);
+hipError_t launch_linear_blocks_forward(const BlocksForwardArgs &a, hipStream_t st);
 
 struct BlocksGradArgs {
     const void *grad_out;    // [n, M] bf16 or fp32, row stride ldg

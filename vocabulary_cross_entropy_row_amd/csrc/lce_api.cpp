@@ -953,6 +953,15 @@ lce_status check_blocks_sizes(const char *fn, int64_t n, int64_t K, int64_t M) {
     return LCE_OK;
 }
 
+lce_status check_training_sizes(const char *fn, int64_t n, int64_t K, int64_t M) {
+    const lce_status st = check_blocks_sizes(fn, n, K, M);
+    if (st != LCE_OK) return st;
+    if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
+    if (n > (1 << 23) - 1024 || M > (1 << 23) - 1024)   // row lengths of what the products read
+        return fail(LCE_ERR_UNSUPPORTED, "%s: n and M must be <= 2^23 - 1024 (got %lld, %lld)", fn, (long long)n, (long long)M);
+    return LCE_OK;
+}
+
 // whether 128 x 128 blocks of [n, K] number fewer than 2^24
 bool few_blocks(int64_t n, int64_t K) {
     const int64_t rows = n / 128 + 1, cols = K / 128 + 1;
@@ -1066,6 +1075,74 @@ lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, in
     return hip_status(lce::launch_linear_blocks(a, stream), "lce_linear_blocks launch");
 }
 
+size_t lce_linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
+    if (n < 0 || K < 1 || M < 1) return 0;
+    return lce::linear_blocks_forward_workspace_bytes(n, K, M);
+}
+
+lce_status lce_linear_blocks_forward(const void *x, int64_t ldx, const void *weight, int64_t ldw, const void *bias,
+                                     lce_dtype bias_dtype, const void *residual, int64_t ldr, int64_t n, int64_t K,
+                                     int64_t M, void *out, int64_t ldo, void *xt, int64_t ldxt, void *scale_xt,
+                                     void *wt, int64_t ldwt, void *scale_wt, void *workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+    const char *fn = "lce_linear_blocks_forward";
+    lce_status st = check_training_sizes(fn, n, K, M);
+    if (st != LCE_OK) return st;
+    // both matrices are quantised in one launch
+    if (!few_blocks(n, K) || !few_blocks(M, K) || ((n + 127) / 128 + (M + 127) / 128) * ((K + 127) / 128) >= (int64_t(1) << 24))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: 2^24 or more blocks of 128 x 128 in x and weight", fn);
+    if (bias && !f32_or_bf16(bias_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown bias dtype %d", fn, (int)bias_dtype);
+    if (bias && !is_aligned(bias, dtype_bytes(bias_dtype)))
+        return fail(LCE_ERR_INVALID_ARG, "%s: bias must be %zu-byte aligned", fn, dtype_bytes(bias_dtype));
+    if (K > lce::kLinearMaxStride - 16) return fail(LCE_ERR_UNSUPPORTED, "%s: 256 rows of K values exceed 4 GiB", fn);
+    if ((st = check_matrix(fn, "x", x, ldx, K, LCE_BF16, n > 0)) != LCE_OK ||
+        (st = check_matrix(fn, "weight", weight, ldw, K, LCE_BF16, true)) != LCE_OK ||
+        (st = check_matrix(fn, "residual", residual, ldr, M, LCE_BF16, false)) != LCE_OK ||
+        (st = check_matrix(fn, "out", out, ldo, M, LCE_BF16, n > 0)) != LCE_OK)
+        return st;
+    if (n == 0) xt = out = nullptr;   // nothing of them is written
+    if ((xt && ((st = check_blocked(fn, "xt", xt, ldxt, n)) != LCE_OK ||
+                (st = check_scale(fn, "scale_xt", scale_xt, 1, 1, 1, 1, LCE_E8M0, true)) != LCE_OK)) ||
+        (wt && ((st = check_blocked(fn, "wt", wt, ldwt, M)) != LCE_OK ||
+                (st = check_scale(fn, "scale_wt", scale_wt, 1, 1, 1, 1, LCE_E8M0, true)) != LCE_OK)))
+        return st;
+    const size_t need = lce::linear_blocks_forward_workspace_bytes(n, K, M);
+    if (!workspace || workspace_bytes < need)
+        return fail(LCE_ERR_INVALID_ARG, "%s: workspace_bytes %zu < minimum %zu", fn, workspace_bytes, need);
+    if (!is_aligned(workspace, 256)) return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    const void *ins[4] = {x, weight, bias, residual};
+    const void *outs[5] = {out, xt, xt ? scale_xt : nullptr, wt, wt ? scale_wt : nullptr};
+    for (int i = 0; i < 5; ++i) {
+        for (const void *in : ins)
+            if (outs[i] && outs[i] == in && !(i == 0 && in == residual))
+                return fail(LCE_ERR_INVALID_ARG, "%s: an output must not be an operand", fn);
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return fail(LCE_ERR_INVALID_ARG, "%s: two outputs are the same buffer", fn);
+    }
+    lce::BlocksForwardArgs a{};
+    a.x = x;
+    a.weight = weight;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.n = n;
+    a.K = K;
+    a.M = M;
+    a.bias = bias;
+    a.bias_bf16 = bias_dtype == LCE_BF16;
+    a.residual = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    a.xt = xt;
+    a.wt = wt;
+    a.ldxt = ldxt;
+    a.ldwt = ldwt;
+    a.scale_xt = scale_xt;
+    a.scale_wt = scale_wt;
+    a.workspace = workspace;
+    return hip_status(lce::launch_linear_blocks_forward(a, stream), "lce_linear_blocks_forward launch");
+}
+
 size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
     if (n < 0 || K < 1 || M < 1) return 0;
     return lce::linear_blocks_backward_workspace_bytes(n, K, M);
@@ -1078,11 +1155,8 @@ lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dty
                                       void *grad_weight, void *grad_bias, lce_dtype grad_bias_dtype, void *workspace,
                                       size_t workspace_bytes, hipStream_t stream) {
     const char *fn = "lce_linear_blocks_backward";
-    lce_status st = check_blocks_sizes(fn, n, K, M);
+    lce_status st = check_training_sizes(fn, n, K, M);
     if (st != LCE_OK) return st;
-    if (K > 0x7fffffffLL / 256) return fail(LCE_ERR_UNSUPPORTED, "%s: K >= 2^23", fn);
-    if (n > (1 << 23) - 1024 || M > (1 << 23) - 1024)   // row lengths of what the products read
-        return fail(LCE_ERR_UNSUPPORTED, "%s: n and M must be <= 2^23 - 1024 (got %lld, %lld)", fn, (long long)n, (long long)M);
     if (!few_blocks(n, M)) return fail(LCE_ERR_UNSUPPORTED, "%s: 2^24 or more blocks of 128 x 128 in grad_out", fn);
     if (!f32_or_bf16(grad_dtype)) return fail(LCE_ERR_INVALID_ARG, "%s: unknown grad_out dtype %d", fn, (int)grad_dtype);
     if (grad_bias && !f32_or_bf16(grad_bias_dtype))

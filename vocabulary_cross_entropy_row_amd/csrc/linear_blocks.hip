@@ -57,6 +57,27 @@ __global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t values) 
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < values; i += static_cast<int64_t>(gridDim.x) * 256) p[i] = 0;
 }
 
+// Workspace of the forward: x and weight quantised, and the product's own
+struct ForwardLayout {
+    int64_t ld, bk, bm;
+    size_t off_x, off_sx, off_w, off_sw, off_part, bytes;
+};
+ForwardLayout forward_layout(int64_t n, int64_t K, int64_t M) {
+    ForwardLayout L;
+    L.ld = round_up(K, 16);
+    L.bk = ceil_div(K, kBlock);
+    L.bm = ceil_div(M, kBlock);
+    size_t o = 0;
+    L.off_x = o;     o += align256(static_cast<size_t>(n) * L.ld);
+    L.off_sx = o;    o += align256(static_cast<size_t>(n) * L.bk);
+    L.off_w = o;     o += align256(static_cast<size_t>(M) * L.ld);
+    L.off_sw = o;    o += align256(static_cast<size_t>(L.bm) * L.bk);
+    L.off_part = o;
+    o += align256(linear_blocks_workspace_bytes(n, K, M));
+    L.bytes = o;
+    return L;
+}
+
 // Workspace of the backward: the two quantised forms of grad_out with their scales, the bias's partial
 // sums, and the products' own
 struct GradLayout {
@@ -141,6 +162,47 @@ hipError_t launch_linear_blocks(const BlocksArgs &a, hipStream_t st) {
     hipLaunchKernelGGL(linear::linear_fold_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16384))),
                        dim3(256), 0, st, a.part, g.ldpart, p.splits, e);
     return hipGetLastError();
+}
+
+size_t linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M) { return forward_layout(n, K, M).bytes; }
+
+hipError_t launch_linear_blocks_forward(const BlocksForwardArgs &a, hipStream_t st) {
+    const ForwardLayout L = forward_layout(a.n, a.K, a.M);
+    char *ws = static_cast<char *>(a.workspace);
+    auto bytes = [&](size_t off) { return reinterpret_cast<unsigned char *>(ws + off); };
+    const int64_t bn = ceil_div(a.n, kBlock);
+    QuantizeArgs x{}, w{};
+    x.x = a.x;
+    x.ldx = a.ldx;
+    x.n = a.n;
+    x.K = a.K;
+    x.q = {bytes(L.off_x), L.ld, ws + L.off_sx, 1, a.n, false, true};
+    if (a.xt) x.qt = {static_cast<unsigned char *>(a.xt), a.ldxt, a.scale_xt, bn, 1, true, true};
+    w.x = a.weight;
+    w.ldx = a.ldw;
+    w.n = a.M;
+    w.K = a.K;
+    w.q = {bytes(L.off_w), L.ld, ws + L.off_sw, L.bk, 1, true, true};
+    if (a.wt) w.qt = {static_cast<unsigned char *>(a.wt), a.ldwt, a.scale_wt, L.bm, 1, true, true};
+    hipError_t e = launch_quantize_pair(x, w, st);
+    if (e != hipSuccess || a.n == 0) return e;
+    BlocksArgs g{};
+    g.x = ws + L.off_x;
+    g.weight = ws + L.off_w;
+    g.ldx = g.ldw = L.ld;
+    g.n = a.n;
+    g.K = a.K;
+    g.M = a.M;
+    g.sx = {ws + L.off_sx, 1, a.n, true};
+    g.sw = {ws + L.off_sw, L.bk, 1, true};
+    g.bias = a.bias;
+    g.bias_bf16 = a.bias_bf16;
+    g.residual = a.residual;
+    g.ldr = a.ldr;
+    g.out = a.out;
+    g.ldo = a.ldo;
+    g.part = reinterpret_cast<float *>(ws + L.off_part);
+    return launch_linear_blocks(g, st);
 }
 
 size_t linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) { return grad_layout(n, K, M).bytes; }

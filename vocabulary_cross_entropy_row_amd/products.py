@@ -37,23 +37,18 @@ def _up(v: int, unit: int) -> int:
     return -(-v // unit) * unit
 
 
-def _new_values(n: int, K: int, device):
-    """[n, K] whose rows start on 16 bytes, as the product reads them; returns (tensor, row stride)."""
-    ld = _up(K, 16)
-    t = torch.empty((n, ld), dtype=E4M3, device=device)
-    return (t if ld == K else t[:, :K]), ld
-
-
 def _scale_shape(n: int, K: int, tile: bool):
     return (-(-n // 128) if tile else n), -(-K // 128)
 
 
-def _new_scale(n: int, K: int, tile: bool, dtype, device):
-    """Scales of row blocks lie block by block: the product reads those of 16 rows together."""
-    rows, cols = _scale_shape(n, K, tile)
-    if tile:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
-    return torch.empty((cols, rows), dtype=dtype, device=device).t()
+def _new(n: int, K: int, tile: bool, dtype, device):
+    """(values [n, K], their row stride, scales, their strides): rows on 16 bytes, and scales of row blocks
+    block by block, for the product reads those of 16 rows together."""
+    ld = _up(K, 16)
+    rows, cols = shape = _scale_shape(n, K, tile)
+    order = (cols, 1) if tile else (1, rows)
+    return (torch.empty_strided((n, K), (ld, 1), dtype=E4M3, device=device), ld,
+            torch.empty_strided(shape, order, dtype=dtype, device=device), *order)
 
 
 def _scale(t, name: str, n: int, K: int, tile: bool, device):
@@ -70,6 +65,23 @@ def _scale(t, name: str, n: int, K: int, tile: bool, device):
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     row, col = t.stride()
     return row, col, code
+
+
+def _given(values, scale, names, n: int, K: int, tile: bool, dtype, device):
+    """What _new gives, with the outputs that the caller brought."""
+    new = _new(n, K, tile, dtype, device)
+    ld, order = new[1], new[3:]
+    if values is None:
+        values = new[0]
+    else:
+        ld = _rows(values, names[0], E4M3, n, K, device)
+    if scale is None:
+        scale = new[2]
+    else:
+        *order, code = _scale(scale, names[1], n, K, tile, device)
+        if code != _SCALES[dtype]:
+            raise TypeError(f"{names[1]} must be {dtype} (got {scale.dtype})")
+    return (values, ld, scale, *order)
 
 
 @_call_stream
@@ -98,31 +110,22 @@ def lce_quantize_blocks(x, *, blocks: str | None = "row", transposed: str | None
     if scale_dtype not in _SCALES:
         raise TypeError(f"scale_dtype must be float8_e8m0fnu or float32 (got {scale_dtype})")
     kind = kind_t = ldv = ldvt = s_row = s_col = st_row = st_col = 0
+    scode = _SCALES[scale_dtype]
     if blocks is not None:
         kind = _blocks(blocks, "blocks")
-        if values is None:
-            values, ldv = _new_values(n, K, dev)
+        if values is None and scale is None:
+            values, ldv, scale, s_row, s_col = _new(n, K, kind == 1, scale_dtype, dev)
         else:
-            ldv = _rows(values, "values", E4M3, n, K, dev)
-        if scale is None:
-            scale = _new_scale(n, K, kind == 1, scale_dtype, dev)
-        s_row, s_col, scode = _scale(scale, "scale", n, K, kind == 1, dev)
-        if scode != _SCALES[scale_dtype]:
-            raise TypeError(f"scale must be {scale_dtype} (got {scale.dtype})")
+            values, ldv, scale, s_row, s_col = _given(values, scale, ("values", "scale"), n, K, kind == 1, scale_dtype, dev)
     if transposed is not None:
         kind_t = _blocks(transposed, "transposed")
-        if values_t is None:
-            values_t, ldvt = _new_values(K, n, dev)
+        if values_t is None and scale_t is None:
+            values_t, ldvt, scale_t, st_row, st_col = _new(K, n, kind_t == 1, scale_dtype, dev)
         else:
-            ldvt = _rows(values_t, "values_t", E4M3, K, n, dev)
-        if scale_t is None:
-            scale_t = _new_scale(K, n, kind_t == 1, scale_dtype, dev)
-        st_row, st_col, scode = _scale(scale_t, "scale_t", K, n, kind_t == 1, dev)
-        if scode != _SCALES[scale_dtype]:
-            raise TypeError(f"scale_t must be {scale_dtype} (got {scale_t.dtype})")
+            values_t, ldvt, scale_t, st_row, st_col = _given(values_t, scale_t, ("values_t", "scale_t"), K, n, kind_t == 1,
+                                                             scale_dtype, dev)
     _check(lib().lce_quantize_blocks(x.data_ptr(), ldx, code, n, K, _ptr(values), ldv, kind, _ptr(scale), s_row, s_col,
-                                     _ptr(values_t), ldvt, kind_t, _ptr(scale_t), st_row, st_col, _SCALES[scale_dtype],
-                                     stream))
+                                     _ptr(values_t), ldvt, kind_t, _ptr(scale_t), st_row, st_col, scode, stream))
     return BlocksResult(values, scale, values_t, scale_t)
 
 
@@ -253,29 +256,51 @@ def _blocks_backward(g, ldg, gcode, x_args, w_args, n, K, M, gx, ldgx, gw, gb, b
                                             _ptr(gb), bcode, workspace.data_ptr(), bytes_, stream))
 
 
+def _kept(need: bool, K: int, width: int, at: int):
+    """Where a transposed operand [K, width] and its scales lie in what the forward keeps: (row stride, offset of
+    the scales, end), all bytes, from ``at`` on."""
+    if not need:
+        return 0, at, at
+    ld = _up(width, 16)
+    scales = _up(at + K * ld, 256)
+    return ld, scales, _up(scales + -(-K // 128) * -(-width // 128), 256)
+
+
 class _LinearBlocks(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, differentiate):
-        _on_gpu(x, "x")
+        dev = _on_gpu(x, "x")
         if x.dim() < 1 or not torch.is_tensor(weight) or weight.dim() != 2:
             raise ValueError("x must have at least one dimension, and weight two")
-        for t, name in ((x, "x"), (weight, "weight")):
-            if t.dtype != torch.bfloat16:
+        for t, name in ((x, "x"), (weight, "weight"), (residual, "residual")):
+            if t is not None and t.dtype != torch.bfloat16:
                 raise TypeError(f"{name} must be torch.bfloat16 (got {t.dtype})")
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name} must be on {dev} (got {t.device})")
         M, K = weight.shape
         if x.shape[-1] != K:
             raise ValueError(f"weight must be [{M}, {x.shape[-1]}] (got {list(weight.shape)})")
         shape = (*x.shape[:-1], M)
         if residual is not None and residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)} (got {list(residual.shape)})")
-        need_x, need_w = (differentiate and need for need in ctx.needs_input_grad[:2])
-        qx = lce_quantize_blocks(_rows_of(x, K), transposed="tile" if need_w else None)
-        qw = lce_quantize_blocks(_rows_of(weight, K), blocks="tile", transposed="tile" if need_x else None)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        lce_linear_blocks(qx.values, qx.scale, qw.values, qw.scale, bias=bias,
-                          residual=None if residual is None else _rows_of(residual, M), out=_rows_of(out, M))
-        ctx.save_for_backward(qx.values_t, qx.scale_t, qw.values_t, qw.scale_t)
-        ctx.sizes, ctx.x_shape, ctx.bias_dtype = (M, K), x.shape, None if bias is None else bias.dtype
+        bcode = LCE_F32
+        if bias is not None:
+            bcode = _float_code(bias, "bias")
+            if bias.dim() != 1 or bias.shape[0] != M:
+                raise ValueError(f"bias must be [{M}] (got {list(bias.shape)})")
+            _buf(bias, "bias", bias.dtype, M, dev)
+        x2, w2 = _rows_of(x, K), _rows_of(weight, K)
+        r2 = None if residual is None else _rows_of(residual, M)
+        n = x2.shape[0]
+        keep_x, keep_w = (differentiate and need for need in (ctx.needs_input_grad[1], ctx.needs_input_grad[0]))
+        ldxt, sxt, wt = _kept(keep_x, K, n, 0)
+        ldwt, swt, end = _kept(keep_w, K, M, wt)
+        _forward(x2, w2, bias, bcode, r2, out := torch.empty(shape, dtype=torch.bfloat16, device=dev),
+                 kept := torch.empty(end, dtype=torch.uint8, device=dev), n, K, M, (ldxt, 0, sxt) if keep_x else None,
+                 (ldwt, wt, swt) if keep_w else None, stream=None)
+        ctx.save_for_backward(kept)
+        ctx.sizes, ctx.places, ctx.x_shape = (n, K, M), (ldxt, 0, sxt, ldwt, wt, swt), x.shape
+        ctx.bias_dtype = None if bias is None else bias.dtype
         return out
 
     @staticmethod
@@ -283,12 +308,28 @@ class _LinearBlocks(torch.autograd.Function):
         return (_blocks_backward_twice if torch.is_grad_enabled() else _blocks_backward_once)(ctx, g)
 
 
+@_call_stream
+def _forward(x, w, bias, bcode, residual, out, kept, n, K, M, xt, wt, stream):
+    """The call, its operands checked; ``xt`` and ``wt``: (row stride, offset, offset of the scales) in ``kept``."""
+    bytes_ = lib().lce_linear_blocks_forward_workspace_bytes(n, K, M)
+    workspace = torch.empty(max(bytes_, 1), dtype=torch.uint8, device=x.device)
+    base = kept.data_ptr()
+
+    def place(p):
+        return (None, 0, None) if p is None else (base + p[1], p[0], base + p[2])
+
+    _check(lib().lce_linear_blocks_forward(x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), _ptr(bias), bcode, _ptr(residual),
+                                           M if residual is None else _ld(residual), n, K, M, out.data_ptr(), M, *place(xt),
+                                           *place(wt), workspace.data_ptr(), bytes_, stream))
+
+
 def _blocks_backward_once(ctx, g):   # on autograd's thread, as the norm's in head.py
-    xt, scale_xt, wt, scale_wt = ctx.saved_tensors
+    kept, = ctx.saved_tensors
     need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
     gx = gw = gb = None
     if need_x or need_w or need_b:
-        M, K = ctx.sizes
+        n, K, M = ctx.sizes
+        ldxt, xt, sxt, ldwt, wt, swt = ctx.places
         dev = g.device
         bcode = LCE_F32
         if need_x:
@@ -299,14 +340,11 @@ def _blocks_backward_once(ctx, g):   # on autograd's thread, as the norm's in he
             gb = torch.empty(M, dtype=ctx.bias_dtype, device=dev)
             bcode = _CODES[ctx.bias_dtype]
         g2 = _rows_of(g, M)
+        base = kept.data_ptr()
         none = (None, 0, None, 0, 0)
-
-        def args(t, scale, width):
-            return t.data_ptr(), _up(width, 16), scale.data_ptr(), *scale.stride()
-
-        n = g2.shape[0]
-        _blocks_backward(g2, _ld(g2), LCE_BF16, args(xt, scale_xt, n) if need_w else none,
-                         args(wt, scale_wt, M) if need_x else none, n, K, M, gx, K, gw, gb, bcode, None,
+        x_args = (base + xt, ldxt, base + sxt, -(-n // 128), 1) if need_w else none
+        w_args = (base + wt, ldwt, base + swt, -(-M // 128), 1) if need_x else none
+        _blocks_backward(g2, _ld(g2), LCE_BF16, x_args, w_args, n, K, M, gx, K, gw, gb, bcode, None,
                          _current_stream(dev.index))
     return gx, gw, gb, (g if need_r else None), None
 
