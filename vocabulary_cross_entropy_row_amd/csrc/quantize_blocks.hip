@@ -61,38 +61,114 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t m) {
     return umax(m, static_cast<uint32_t>(dev::dpp_i<dev::kDppMirror>(static_cast<int>(m))));
 }
 
-// Eight values of a row from column c on, zeros from K on.  A cut piece takes the row's last eight values and
-// moves them up: one wide load, where a load for each value is a wait for each.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Eight values of a row as they are stored.  A cut piece takes the row's last eight values and moves them
+// up, zeros behind them: one wide load, where a load for each value is a wait for each.
+template <bool BF16> struct Eight;
+template <> struct Eight<true> {
+    u32x4 q;
+    __device__ __forceinline__ void clear() { q = (u32x4){0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ void load(const void *x, int64_t at) {
+        q = *reinterpret_cast<const linear::any16 *>(static_cast<const uint16_t *>(x) + at);
+    }
+    __device__ __forceinline__ void shift(int up) {
+        if (up & 4) q = (u32x4){q.z, q.w, 0u, 0u};
+        if (up & 2) q = (u32x4){q.y, q.z, q.w, 0u};
+        if (up & 1) q = (u32x4){(q.x >> 16) | (q.y << 16), (q.y >> 16) | (q.z << 16), (q.z >> 16) | (q.w << 16), q.w >> 16};
+    }
+    __device__ __forceinline__ void set(int e, const void *x, int64_t at) {   // onto zeros
+        const uint32_t b = static_cast<const uint16_t *>(x)[at];
+        q[e >> 1] |= b << (16 * (e & 1));
+    }
+    __device__ __forceinline__ float get(int e) const { return Elt<true>::get(q, e); }
+    // magnitudes of values 2 w and 2 w + 1
+    __device__ __forceinline__ u16x2 pair(int w) const { return __builtin_bit_cast(u16x2, q[w] & 0x7fff7fffu); }
+};
+template <> struct Eight<false> {
+    u32x4 p, s;
+    __device__ __forceinline__ void clear() { p = s = (u32x4){0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ void load(const void *x, int64_t at) {
+        const linear::any16 *v = reinterpret_cast<const linear::any16 *>(static_cast<const float *>(x) + at);
+        p = v[0];
+        s = v[1];
+    }
+    __device__ __forceinline__ void shift(int up) {
+        if (up & 4) {
+            p = s;
+            s = (u32x4){0u, 0u, 0u, 0u};
+        }
+        if (up & 2) {
+            p = (u32x4){p.z, p.w, s.x, s.y};
+            s = (u32x4){s.z, s.w, 0u, 0u};
+        }
+        if (up & 1) {
+            p = (u32x4){p.y, p.z, p.w, s.x};
+            s = (u32x4){s.y, s.z, s.w, 0u};
+        }
+    }
+    __device__ __forceinline__ void set(int e, const void *x, int64_t at) {
+        (e < 4 ? p : s)[e & 3] = __float_as_uint(static_cast<const float *>(x)[at]);
+    }
+    __device__ __forceinline__ float get(int e) const { return Elt<false>::get(e < 4 ? p : s, e & 3); }
+};
 template <bool BF16>
-__device__ __forceinline__ void load_row(const void *x, int64_t row, int64_t c, int64_t K, float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+__device__ __forceinline__ void load_row(const void *x, int64_t row, int64_t c, int64_t K, Eight<BF16> &v) {
+    v.clear();
     if (c >= K) return;
-    const int64_t from = c + 8 <= K ? c : K - 8;
-    if (from < 0) {   // a row of fewer than eight
+    if (c + 8 <= K) {
+        v.load(x, row + c);
+    } else if (K >= 8) {
+        v.load(x, row + K - 8);
+        v.shift(static_cast<int>(c - (K - 8)));
+    } else {   // c is 0
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = Elt<BF16>::load_one(x, row + (c + e < K ? c + e : K - 1));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < K ? v[e] : 0.0f;
-        return;
+        for (int e = 0; e < 7; ++e)
+            if (e < K) v.set(e, x, row + e);
     }
-    if constexpr (BF16) {
-        const u32x4 q = *reinterpret_cast<const linear::any16 *>(static_cast<const uint16_t *>(x) + row + from);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = Elt<true>::get(q, e);
-    } else {
-        const linear::any16 *q = reinterpret_cast<const linear::any16 *>(static_cast<const float *>(x) + row + from);
-        const u32x4 p = q[0], s = q[1];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = Elt<false>::get(e < 4 ? p : s, e & 3);
-    }
-    const int up = static_cast<int>(c - from);
-    if (up == 0) return;
-#pragma unroll
-    for (int step = 4; step; step >>= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = up & step ? (e + step < 8 ? v[e + step] : 0.0f) : v[e];
 }
+
+__device__ __forceinline__ u16x2 max2(u16x2 a, u16x2 b) { return __builtin_elementwise_max(a, b); }
+__device__ __forceinline__ uint32_t widen(uint16_t b) { return static_cast<uint32_t>(b) << 16; }
+
+// Bits of the largest magnitude of eight rows (of eight values each) and of their columns
+__device__ __forceinline__ void maxima(const Eight<true> (&v)[8], uint32_t (&rows)[8], uint32_t (&cols)[8]) {
+    u16x2 c[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        u16x2 r = {};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const u16x2 p = v[i].pair(w);
+            r = max2(r, p);
+            c[w] = max2(c[w], p);
+        }
+        rows[i] = umax(widen(r.x), widen(r.y));
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        cols[2 * w] = widen(c[w].x);
+        cols[2 * w + 1] = widen(c[w].y);
+    }
+}
+__device__ __forceinline__ void maxima(const Eight<false> (&v)[8], uint32_t (&rows)[8], uint32_t (&cols)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rows[i] = cols[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(v[i].get(e)) & 0x7fffffffu;
+            rows[i] = umax(rows[i], b);
+            cols[e] = umax(cols[e], b);
+        }
+}
+// Keeps the widened values of one use from staying in registers for the next
+__device__ __forceinline__ void stay_packed(Eight<true> (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i].q));
+}
+__device__ __forceinline__ void stay_packed(Eight<false> (&)[8]) {}
 
 // `count` of the bytes of `w`, from the lowest on
 __device__ __forceinline__ void put_bytes(unsigned char *o, uint64_t w, int count) {
@@ -110,7 +186,7 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int bk, uint32_t total) {
     const int ch = threadIdx.x & 15;
     const uint32_t first = blockIdx.x * (16u * kRowBlocks) + (threadIdx.x >> 4);
-    float v[kRowBlocks][8];
+    Eight<BF16> v[kRowBlocks];
     uint32_t row[kRowBlocks], b[kRowBlocks];
 #pragma unroll
     for (int i = 0; i < kRowBlocks; ++i) {
@@ -124,14 +200,14 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int 
         if (first + i * 16u >= total) break;   // the 16 lanes of a block alike
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = umax(m, __float_as_uint(v[i][e]) & 0x7fffffffu);
+        for (int e = 0; e < 8; ++e) m = umax(m, __float_as_uint(v[i].get(e)) & 0x7fffffffu);
         const uint32_t ex = scale_exponent(row16_max(m));
         if (ch == 0) put_scale(a.q, row[i], b[i], ex);
         const float inv = inverse_scale(ex);
         const int64_t c = b[i] * 128ll + ch * 8;
         if (c < a.K)
-            put8(a.q.values + row[i] * a.q.ld + c, four(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                 four(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv), a.K - c);
+            put8(a.q.values + row[i] * a.q.ld + c, four(v[i].get(0) * inv, v[i].get(1) * inv, v[i].get(2) * inv, v[i].get(3) * inv),
+                 four(v[i].get(4) * inv, v[i].get(5) * inv, v[i].get(6) * inv, v[i].get(7) * inv), a.K - c);
     }
 }
 
@@ -154,20 +230,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJobs jobs) {
     const int64_t r0 = br * 128ll, c0 = bc * 128ll;
     const int t = threadIdx.x, ch = t & 15, g = t >> 4, lane = t & 63, wave = t >> 6;
     const int64_t gr = r0 + g * 8, gc = c0 + ch * 8;
-    float v[8][8];   // rows gr .. gr + 7, columns gc .. gc + 7
+    Eight<BF16> v[8];   // rows gr .. gr + 7, columns gc .. gc + 7
 #pragma unroll
     for (int i = 0; i < 8; ++i) load_row<BF16>(a.x, (gr + i) * a.ldx, gr + i < a.n ? gc : a.K, a.K, v[i]);
     uint32_t rmax[8], cmax[8], all = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rmax[i] = cmax[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t b = __float_as_uint(v[i][e]) & 0x7fffffffu;
-            rmax[i] = umax(rmax[i], b);
-            cmax[e] = umax(cmax[e], b);
-        }
+    maxima(v, rmax, cmax);
     const bool want_tile = (a.q.values && a.q.tile) || (a.qt.values && a.qt.tile);
     if (want_tile) {
 #pragma unroll
@@ -191,12 +258,13 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJobs jobs) {
         for (int e = 0; e < 8; ++e) {
             float c = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c += v[i][e];
+            for (int i = 0; i < 8; ++i) c += v[i].get(e);
             c += __shfl_xor(c, 16);
             c += __shfl_xor(c, 32);
             if (lane < 16) col_sum[wave][ch * 8 + e] = c;
         }
     }
+    stay_packed(v);
     __syncthreads();
     uint32_t tile_e = 0;
     if (want_tile) {
@@ -216,12 +284,13 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJobs jobs) {
                 if (ch == 0 && gr + i < a.n) put_scale(a.q, gr + i, bc, e);
             }
             const float inv = inverse_scale(e);
-            const uint32_t lo = four(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-            const uint32_t hi = four(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+            const uint32_t lo = four(v[i].get(0) * inv, v[i].get(1) * inv, v[i].get(2) * inv, v[i].get(3) * inv);
+            const uint32_t hi = four(v[i].get(4) * inv, v[i].get(5) * inv, v[i].get(6) * inv, v[i].get(7) * inv);
             if (gr + i < a.n && gc < a.K) put8(a.q.values + (gr + i) * a.q.ld + gc, lo, hi, a.K - gc);
         }
     }
     if (!a.qt.values) return;
+    stay_packed(v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int c = ch * 8 + e;
@@ -231,8 +300,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJobs jobs) {
             if (g == 0 && c0 + c < a.K) put_scale(a.qt, c0 + c, br, ex);
         }
         const float inv = inverse_scale(ex);
-        const uint2 w = make_uint2(four(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv),
-                                   four(v[4][e] * inv, v[5][e] * inv, v[6][e] * inv, v[7][e] * inv));
+        const uint2 w = make_uint2(four(v[0].get(e) * inv, v[1].get(e) * inv, v[2].get(e) * inv, v[3].get(e) * inv),
+                                   four(v[4].get(e) * inv, v[5].get(e) * inv, v[6].get(e) * inv, v[7].get(e) * inv));
         *reinterpret_cast<uint2 *>(flat + c * 128 + (((g >> 1) ^ (ch & 7)) * 16) + (g & 1) * 8) = w;
     }
     __syncthreads();
