@@ -63,8 +63,7 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t m) {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// Eight values of a row as they are stored.  A cut piece takes the row's last eight values and moves them
-// up, zeros behind them: one wide load, where a load for each value is a wait for each.
+// Eight values of a row as they are stored.
 template <bool BF16> struct Eight;
 template <> struct Eight<true> {
     u32x4 q;
@@ -112,20 +111,35 @@ template <> struct Eight<false> {
     }
     __device__ __forceinline__ float get(int e) const { return Elt<false>::get(e < 4 ? p : s, e & 3); }
 };
-template <bool BF16>
-__device__ __forceinline__ void load_row(const void *x, int64_t row, int64_t c, int64_t K, Eight<BF16> &v) {
-    v.clear();
-    if (c >= K) return;
-    if (c + 8 <= K) {
-        v.load(x, row + c);
-    } else if (K >= 8) {
-        v.load(x, row + K - 8);
-        v.shift(static_cast<int>(c - (K - 8)));
-    } else {   // c is 0
+// Values c .. c + 7 of N rows, zeros where there are none.  Every lane loads eight values of rows that there are
+// and without a branch, so that all loads are under way at once: where c .. c + 7 reach past K, the row's last
+// eight, which are then moved up.
+template <bool BF16, int N, class Row, class There>
+__device__ __forceinline__ void load_rows(const void *x, int64_t c, int64_t K, Row row, There there, Eight<BF16> (&v)[N]) {
+    if (K >= 8) {
+        const int64_t from = c + 8 <= K ? c : K - 8;
 #pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < K) v.set(e, x, row + e);
+        for (int i = 0; i < N; ++i) v[i].load(x, row(i) + from);
+        const int up = static_cast<int>(c - from < 8 ? c - from : 8);
+        if (up) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i].shift(up);
+                if (up >= 8) v[i].clear();
+            }
+        }
+    } else {   // c is 0, or past K
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i].clear();
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + e < K) v[i].set(e, x, row(i) + e);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (!there(i)) v[i].clear();
 }
 
 __device__ __forceinline__ u16x2 max2(u16x2 a, u16x2 b) { return __builtin_elementwise_max(a, b); }
@@ -186,28 +200,28 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int bk, uint32_t total) {
     const int ch = threadIdx.x & 15;
     const uint32_t first = blockIdx.x * (16u * kRowBlocks) + (threadIdx.x >> 4);
-    Eight<BF16> v[kRowBlocks];
+    Eight<BF16> v[kRowBlocks][1];
     uint32_t row[kRowBlocks], b[kRowBlocks];
 #pragma unroll
     for (int i = 0; i < kRowBlocks; ++i) {
-        const uint32_t at = first + i * 16u;
+        const uint32_t at = min(first + i * 16u, total - 1);
         row[i] = at / static_cast<uint32_t>(bk);
         b[i] = at - row[i] * static_cast<uint32_t>(bk);
-        if (at < total) load_row<BF16>(a.x, row[i] * a.ldx, b[i] * 128ll + ch * 8, a.K, v[i]);
+        load_rows<BF16>(a.x, b[i] * 128ll + ch * 8, a.K, [&](int) { return row[i] * a.ldx; }, [](int) { return true; }, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kRowBlocks; ++i) {
         if (first + i * 16u >= total) break;   // the 16 lanes of a block alike
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = umax(m, __float_as_uint(v[i].get(e)) & 0x7fffffffu);
+        for (int e = 0; e < 8; ++e) m = umax(m, __float_as_uint(v[i][0].get(e)) & 0x7fffffffu);
         const uint32_t ex = scale_exponent(row16_max(m));
         if (ch == 0) put_scale(a.q, row[i], b[i], ex);
         const float inv = inverse_scale(ex);
         const int64_t c = b[i] * 128ll + ch * 8;
         if (c < a.K)
-            put8(a.q.values + row[i] * a.q.ld + c, four(v[i].get(0) * inv, v[i].get(1) * inv, v[i].get(2) * inv, v[i].get(3) * inv),
-                 four(v[i].get(4) * inv, v[i].get(5) * inv, v[i].get(6) * inv, v[i].get(7) * inv), a.K - c);
+            put8(a.q.values + row[i] * a.q.ld + c, four(v[i][0].get(0) * inv, v[i][0].get(1) * inv, v[i][0].get(2) * inv, v[i][0].get(3) * inv),
+                 four(v[i][0].get(4) * inv, v[i][0].get(5) * inv, v[i][0].get(6) * inv, v[i][0].get(7) * inv), a.K - c);
     }
 }
 
@@ -231,8 +245,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeJobs jobs) {
     const int t = threadIdx.x, ch = t & 15, g = t >> 4, lane = t & 63, wave = t >> 6;
     const int64_t gr = r0 + g * 8, gc = c0 + ch * 8;
     Eight<BF16> v[8];   // rows gr .. gr + 7, columns gc .. gc + 7
-#pragma unroll
-    for (int i = 0; i < 8; ++i) load_row<BF16>(a.x, (gr + i) * a.ldx, gr + i < a.n ? gc : a.K, a.K, v[i]);
+    load_rows<BF16>(a.x, gc, a.K, [&](int i) { return (gr + i < a.n ? gr + i : a.n - 1) * a.ldx; },
+                    [&](int i) { return gr + i < a.n; }, v);
     uint32_t rmax[8], cmax[8], all = 0;
     maxima(v, rmax, cmax);
     const bool want_tile = (a.q.values && a.q.tile) || (a.qt.values && a.qt.tile);
