@@ -209,7 +209,7 @@ struct Args {
     int groups, per_xcd;              // workgroups; ceil(groups / 8)
     float *part;                      // groups != total: [2 groups][side][side] fp32
     // epilogue
-    float inv;                        // of the products' scale
+    float inv, inv_poly;              // of the products' scale; apply_short_kernel: of O O's
     uint16_t *o;                      // O [rows][ldo]: written by GRAM, read by POLY
     uint16_t *bo;                     // B's off-diagonal part
     int64_t ldo, ob;
@@ -682,6 +682,144 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
     }
 }
 
+// Up to 64 rows, B is little work: every workgroup of B X forms the 32 rows of it that it needs, from O and
+// its diagonal, in LDS, instead of a launch that forms it for all (64 x 64 54 -> 42 us; with 128 rows that
+// takes longer than the launch, 16 x 128 x 512 71 -> 91).  A workgroup takes 32 rows of X and 256
+// columns, 32 to a wave; everything that it reads is asked for at its start.
+constexpr int kShortRows = 64;
+constexpr int kShortCols = 256;
+
+template <int EPI>   // APPLY or LAST
+__global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
+    constexpr int U = kShortRows / 16, LDB = kShortRows + 8, LD = 36;
+    __shared__ __attribute__((aligned(16))) uint16_t b_rows[32 * LDB];
+    __shared__ float diagonal[32];
+    __shared__ __attribute__((aligned(16))) float sums[8][32 * LD];
+    const int z = blockIdx.x / g.per_batch, mn = blockIdx.x - z * g.per_batch, ti = mn / g.tiles_f;
+    const int th = threadIdx.x, lane = th & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(th >> 6);
+    const int t0 = ti * 32, f0 = (mn - ti * g.tiles_f) * kShortCols + wave * 32;
+    const bool there = f0 < g.rows_w;   // of this wave's columns: all or none
+    h8 a[U];
+    u32x4 hi[2];
+    uint2 lo[2];
+    if (there) {
+        const uint16_t *row = g.w + z * g.wb + static_cast<int64_t>(f0 + l32) * g.ldw + half * 8;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            a[u] = *reinterpret_cast<const h8 *>(row + u * 16);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int64_t at = z * g.hb + static_cast<int64_t>(t0 + p * 16 + (lane >> 2)) * g.ldh + f0 + (lane & 3) * 8;
+            hi[p] = *reinterpret_cast<const u32x4 *>(g.hi + at);
+            lo[p] = *reinterpret_cast<const uint2 *>(g.lo + at);
+        }
+    }
+    if (wave * 32 < kShortRows) {   // columns 32 wave .. of B's rows t0 ..
+        const uint16_t *o = g.o + z * g.ob;
+        const float *d = g.d + static_cast<int64_t>(z) * g.rows_x;
+        const int t = t0 + l32;
+        h8 oc[U], ot[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            oc[u] = *reinterpret_cast<const h8 *>(o + static_cast<int64_t>(wave * 32 + l32) * g.ldo + u * 16 + half * 8);
+            ot[u] = *reinterpret_cast<const h8 *>(o + static_cast<int64_t>(t) * g.ldo + u * 16 + half * 8);
+        }
+        const float dt = d[t];
+        uint2 here[4];
+        float4 df[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int c = wave * 32 + r * 8 + half * 4;
+            here[r] = *reinterpret_cast<const uint2 *>(o + static_cast<int64_t>(t) * g.ldo + c);
+            df[r] = *reinterpret_cast<const float4 *>(d + c);
+        }
+        f16v sum = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(oc[u], ot[u], sum, 0, 0, 0);
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int c = wave * 32 + r * 8 + half * 4;
+            const h4 o4 = __builtin_bit_cast(h4, here[r]);
+            const float dc[4] = {df[r].x, df[r].y, df[r].z, df[r].w};
+            h4 b;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {   // symmetric_values<POLY>
+                const float ov = static_cast<float>(o4[u]) * (1.0f / kScaleO);
+                float square = fmaf(dt + dc[u], ov, sum[r * 4 + u] * g.inv_poly);
+                float v = fmaf(g.c, square, g.b * ov) * kScaleB;
+                if (t == c + u) {
+                    square = fmaf(dt, dt, square);
+                    diagonal[l32] = g.a + fmaf(g.c, square, g.b * dt);
+                    v = 0.0f;
+                }
+                b[u] = static_cast<_Float16>(v);
+            }
+            *reinterpret_cast<uint2 *>(b_rows + l32 * LDB + c) = __builtin_bit_cast(uint2, b);
+        }
+    }
+    __syncthreads();
+    if (!there) return;
+    f16v acc = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const h8 b = *reinterpret_cast<const h8 *>(b_rows + l32 * LDB + u * 16 + half * 8);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[u], b, acc, 0, 0, 0);
+    }
+    float *reg = sums[wave];   // this wave's alone
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4 *>(reg + l32 * LD + (r >> 2) * 8 + half * 4) = make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]);
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const bool turned = EPI == APPLY || g.tall;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int tl = p * 16 + (lane >> 2), at = tl * LD + (lane & 3) * 8;
+        const float4 x = *reinterpret_cast<const float4 *>(reg + at), y = *reinterpret_cast<const float4 *>(reg + at + 4);
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        apply_values<EPI>(g, z, t0 + tl, f0 + (lane & 3) * 8, hi[p], lo[p], diagonal[tl], v);
+        if (turned) {
+            *reinterpret_cast<float4 *>(reg + at) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(reg + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    if (!turned) return;
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int fl = q * 16 + (lane >> 2), tl = (lane & 3) * 8;
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = reg[(tl + u) * LD + fl];
+        turned_values<EPI>(g, z, f0 + fl, t0 + tl, v);
+    }
+}
+
+// Adds pieces k .. k + N - 1, up to the last, to v; all of their loads are under way at once.
+template <int N>
+__device__ __forceinline__ int add_pieces(const float *p, int size, int first, int first_slot, int k, int last, float (&v)[8]) {
+    float4 x[N], y[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int i = min(k + u, last);
+        const float4 *q = reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i == first ? first_slot : 2 * i) * size);
+        x[u] = q[0];
+        y[u] = q[1];
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const bool in = k + u <= last;   // a choice and no branch, or each load moves behind one
+        const float q[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = in ? v[e] + q[e] : v[e];
+    }
+    return N;
+}
+
 // The pieces of the tiles that more than one workgroup had, added in the order of their steps, 64 x 64 values
 // a workgroup, stored as they are and, off the diagonal, transposed.
 template <int SIDE, int EPI>
@@ -705,14 +843,10 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
     for (int i = 0; i < 2; ++i) {
         const int tl = i * 32 + (th >> 3), fl = (th & 7) * 8, t = t0 + tl, f = f0 + fl;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, df[8] = {};
-        for (int k = first; k <= last; ++k) {
-            const int64_t slot = k == first ? first_slot : 2 * k;
-            const float4 *p = reinterpret_cast<const float4 *>(
-                g.part + (slot * SIDE + part / PARTS * 64 + tl) * SIDE + part % PARTS * 64 + fl);
-            const float4 x = p[0], y = p[1];
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-        }
+        const float *p = g.part + static_cast<int64_t>(part / PARTS * 64 + tl) * SIDE + part % PARTS * 64 + fl;
+        int k = first;
+        while (last - k >= 4) k += add_pieces<16>(p, SIDE * SIDE, first, first_slot, k, last, v);
+        if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, first_slot, k, last, v);
         u32x4 o = {0u, 0u, 0u, 0u};
         float dt = 0.0f;
         if constexpr (EPI == POLY) {
@@ -943,6 +1077,22 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         g.steps = static_cast<int>(L.cp / kUnit);
         g.inv = 1.0f / (s * s);
         if ((e = launch_product<GRAM>(g, L.gram, st)) != hipSuccess) return e;
+        if (L.rp <= kShortRows) {
+            g.w = half(k & 1 ? L.off_t1 : L.off_t0);
+            g.ldw = L.ldr;
+            g.wb = l.tb;
+            g.xt = half(k & 1 ? L.off_t0 : L.off_t1);
+            g.rows_w = static_cast<int>(L.cp);
+            g.inv = 1.0f / s;
+            g.inv_poly = 1.0f / (kScaleO * kScaleO);
+            g.tiles_f = static_cast<int>(ceil_div(L.cp, kShortCols));
+            g.per_batch = static_cast<int>(L.rp / 32) * g.tiles_f;
+            const dim3 grid(static_cast<unsigned>(g.per_batch * a.batch));
+            if (k + 1 < a.steps) hipLaunchKernelGGL((apply_short_kernel<APPLY>), grid, dim3(512), 0, st, g);
+            else hipLaunchKernelGGL((apply_short_kernel<LAST>), grid, dim3(512), 0, st, g);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            continue;
+        }
         g.w = g.x = g.o;
         g.ldw = g.ldx = L.ldr;
         g.wb = g.xb = g.ob;
