@@ -339,6 +339,36 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void blocks_kern
     }
 }
 
+// The partial sums of the K splits, added in their order, through the epilogue.  All loads of up to SPLITS of
+// them are under way at once; the last one's again where there are fewer.
+template <int SPLITS>
+__global__ __launch_bounds__(256) void blocks_fold_kernel(const float *part, int64_t ldpart, int splits, Epi e) {
+    const int64_t per = ldpart / 8, total = e.n * per;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = i / per, f = (i - t * per) * 8;
+        const float4 *p = reinterpret_cast<const float4 *>(part + t * ldpart + f);
+        const int64_t step = e.n * ldpart / 4;
+        float4 x[SPLITS], y[SPLITS];
+#pragma unroll
+        for (int k = 0; k < SPLITS; ++k) {
+            x[k] = p[min(k, splits - 1) * step];
+            y[k] = p[min(k, splits - 1) * step + 1];
+        }
+        const Cols c = linear::load_cols(e, f);
+        linear::finish<1>(e, c, t, 0, f, [&](float (&s)[1][8]) {
+            float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, y[0].x, y[0].y, y[0].z, y[0].w};
+#pragma unroll
+            for (int k = 1; k < SPLITS; ++k) {
+                const float q[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = k < splits ? v[u] + q[u] : v[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s[0][u] = v[u];
+        });
+    }
+}
+
 // ---- few tokens ------------------------------------------------------------------------
 //
 // Up to 32 tokens, as linear_rows_kernel: a workgroup takes 16 features and its eight waves an eighth of

@@ -159,8 +159,10 @@ hipError_t launch_linear_blocks(const BlocksArgs &a, hipStream_t st) {
     }
     if (err != hipSuccess || p.splits == 1) return err;
     const int64_t items = a.n * (g.ldpart / 8);
-    hipLaunchKernelGGL(linear::linear_fold_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16384))),
-                       dim3(256), 0, st, a.part, g.ldpart, p.splits, e);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16384))), block(256);
+    static_assert(kMaxSplits <= 16, "the fold's loads");
+    if (p.splits <= 4) hipLaunchKernelGGL((blocks::blocks_fold_kernel<4>), grid, block, 0, st, a.part, g.ldpart, p.splits, e);
+    else hipLaunchKernelGGL((blocks::blocks_fold_kernel<16>), grid, block, 0, st, a.part, g.ldpart, p.splits, e);
     return hipGetLastError();
 }
 
