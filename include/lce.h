@@ -646,9 +646,9 @@ size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t 
  *   A = X X^T,   X <- a X + (b A + c A A) X
  * and out the last X, transposed back.  (3.4445, -4.7750, 2.0315) over five steps takes
  * singular values from about 0.002 to 1 to between 0.7 and 1.2.  The products run in fp16
- * with fp32 sums; X is held in two fp16 and the diagonals of A and b A + c A A in fp32, so
- * the result is off by 2e-4 to 7e-4 (2-norm; five steps of those coefficients) before it is
- * rounded to bf16.  Coefficients under which values pass 256 overflow.
+ * with fp32 sums; X is held in fp16 and an 8-bit rest, the diagonals of A and b A + c A A in
+ * fp32, so the result is off by 2e-4 to 8e-4 (2-norm; five steps of those coefficients)
+ * before it is rounded to bf16.  Coefficients under which values pass 256 overflow.
  *   g           device [batch][rows, cols], row stride ldg and g_batch_stride elements
  *               between matrices, dtype F32 or BF16.  A matrix of zeros gives zeros (eps
  *               above 0); one that holds an infinity or a NaN gives NaN, in itself alone.
@@ -657,7 +657,7 @@ size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t 
  *               and its transpose.  Clobbered; calls that share it must not run at the
  *               same time.
  * rows and cols are 1 to 2^20, batch at most 65535, and batch (rows / 64 + 1) (cols / 64 + 1)
- * below 2^23 (LCE_ERR_UNSUPPORTED otherwise); steps is 1 to 100.  The same inputs give the same
+ * below 2^22 (LCE_ERR_UNSUPPORTED otherwise); steps is 1 to 100.  The same inputs give the same
  * bits.  batch == 0 is valid.
  */
 lce_status lce_orthogonalise(const void *g, int64_t ldg, int64_t g_batch_stride, lce_dtype dtype, int64_t batch,

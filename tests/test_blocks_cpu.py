@@ -94,6 +94,32 @@ def test_backward_refuses(over, status, needle):
     assert st == status and needle in msg, msg
 
 
+def forward(**over):
+    a = dict(x=A, ldx=300, w=B, ldw=300, bias=None, bias_t=0, res=None, ldr=500, n=40, K=300, M=500, out=C, ldo=500, xt=D,
+             ldxt=48, sxt=D + 0x8000, wt=E, ldwt=512, swt=E + 0x8000, ws=WS, wsb=1 << 30)
+    a.update(over)
+    return lce.lib().lce_linear_blocks_forward(a["x"], a["ldx"], a["w"], a["ldw"], a["bias"], a["bias_t"], a["res"], a["ldr"],
+                                               a["n"], a["K"], a["M"], a["out"], a["ldo"], a["xt"], a["ldxt"], a["sxt"], a["wt"],
+                                               a["ldwt"], a["swt"], a["ws"], a["wsb"], None), lce.lce_last_error()
+
+
+@pytest.mark.parametrize("over,status,needle", [
+    (dict(n=-1), INVALID, "n must be"), (dict(K=0), INVALID, "K must be"), (dict(M=0), INVALID, "M must be"),
+    (dict(n=(1 << 23) - 1000), UNSUPPORTED, "2^23 - 1024"), (dict(M=1 << 22, K=1 << 22), UNSUPPORTED, "2^24"),
+    (dict(x=None), INVALID, "x is required"), (dict(w=None), INVALID, "weight is required"), (dict(ldx=299), INVALID, "row stride of x"),
+    (dict(ldw=299), INVALID, "row stride of weight"), (dict(x=A + 1), INVALID, "aligned"), (dict(out=None), INVALID, "out is required"),
+    (dict(ldo=499), INVALID, "row stride of out"), (dict(bias=F, bias_t=2), INVALID, "bias dtype"), (dict(bias=F + 2), INVALID, "bias must be"),
+    (dict(res=F, ldr=499), INVALID, "residual"), (dict(ldxt=47), UNSUPPORTED, "16-byte"), (dict(ldwt=496), INVALID, "row stride of wt"),
+    (dict(xt=D + 8), UNSUPPORTED, "16-byte"), (dict(sxt=None), INVALID, "scale_xt"), (dict(swt=None), INVALID, "scale_wt"),
+    (dict(ws=None), INVALID, "workspace"), (dict(wsb=1000), INVALID, "workspace_bytes"), (dict(ws=WS + 16), INVALID, "256-byte"),
+    (dict(out=A), INVALID, "an operand"), (dict(xt=B), INVALID, "an operand"), (dict(wt=D), INVALID, "same buffer"),
+    (dict(swt=C), INVALID, "same buffer"), (dict(bias=C), INVALID, "an operand"), (dict(res=D), INVALID, "an operand"),
+])
+def test_forward_refuses(over, status, needle):
+    st, msg = forward(**over)
+    assert st == status and needle in msg, msg
+
+
 X = torch.zeros((4, 16), dtype=torch.bfloat16)
 Q, S = torch.zeros((4, 16), dtype=torch.uint8).view(torch.float8_e4m3fn), torch.ones((4, 1))
 

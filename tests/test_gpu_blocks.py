@@ -22,6 +22,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible to torch", allow_module_level=True)
 
+import blocks_plans  # noqa: E402
 import vocabulary_cross_entropy_row_amd as lce  # noqa: E402
 
 DEV = torch.device("cuda:0")
@@ -217,6 +218,14 @@ def test_product(n, K, M, power):
         check_product(x, sx, w, lce.lce_quantize_blocks(stands_for(w, sw, True).float(), blocks="tile").scale)
 
 
+@pytest.mark.parametrize("power,n,K,M", [(p, *size) for p in (True, False) for size in blocks_plans.COVER[p]])
+def test_every_kernel_of_the_product(power, n, K, M):
+    x, sx, w, sw = operands(n, K, M, n + K + M, power)
+    r = normal(n * 5 + M)
+    check_product(x, sx, w, sw, act=ACTS[(n + M) % 5], bias=r(M).to(F32 if n % 2 else BF16),
+                  residual=r(n, M).to(BF16) if K % 2 else None)
+
+
 @pytest.mark.parametrize("power", [True, False], ids=["e8m0", "f32"])
 @pytest.mark.parametrize("n", [7, 40, 400])
 def test_what_lies_past_the_width_does_not_matter(n, power):
@@ -392,3 +401,71 @@ def test_same_bits_again():
     x, sx, w, sw = operands(700, 4096, 500, 8, False)
     a = lce.lce_linear_blocks(x, sx, w, sw).out
     assert torch.equal(a, lce.lce_linear_blocks(x, sx, w, sw).out)
+
+
+def test_offsets_past_32_bits():
+    """A matrix of more than 2^32 values, its transpose and the products that read and write as much."""
+    r = normal(41)
+    n, K = 70001, 61504
+    x = torch.empty(n, K, dtype=BF16, device=DEV)
+    for i in range(0, n, 10000):
+        x[i:i + 10000] = r(min(10000, n - i), 1).to(BF16) * r(1, K).to(BF16)
+    got = lce.lce_quantize_blocks(x, blocks="row", transposed="tile")
+    for rows in (slice(0, 128), slice(69888, n)):   # whole blocks of rows
+        qv, qs = quantised(x[rows], False)
+        assert torch.equal(got.scale[rows].double(), qs) and torch.equal(got.values[rows].double(), qv)
+        for cols in (slice(0, 256), slice(61440, K)):
+            qv, qs = quantised(x[rows, cols].t(), True)
+            at = slice(cols.start // 128, -(-cols.stop // 128)), slice(rows.start // 128, -(-rows.stop // 128))
+            assert torch.equal(got.scale_t[at].double(), qs) and torch.equal(got.values_t[cols, rows].double(), qv)
+    # as the weight: [K, n] in tiles, against few rows of x
+    few = lce.lce_quantize_blocks(r(3, n))
+    out = lce.lce_linear_blocks(few.values, few.scale, got.values_t, got.scale_t).out
+    for cols in (slice(0, 128), slice(61440, K)):
+        at = slice(cols.start // 128, -(-cols.stop // 128))
+        a, b = stands_for(few.values, few.scale, False), stands_for(got.values_t[cols], got.scale_t[at], True)
+        z = a @ b.t()
+        within(out[:, cols], z, HALF * z.abs() + (n + 8) * U * (a.abs() @ b.abs().t()) + cut_off(a, b), "weight past 2^32")
+    # as x, and an output of more than 2^32 values
+    M = 61457
+    w = lce.lce_quantize_blocks(r(M, 128), blocks="tile")
+    narrow = torch.as_strided(got.values, (n, 128), got.values.stride()), got.scale[:, :1]
+    out = lce.lce_linear_blocks(*narrow, w.values, w.scale).out
+    for rows in (slice(0, 64), slice(n - 64, n)):
+        a = stands_for(narrow[0][rows], narrow[1][rows], False)
+        b = stands_for(w.values, w.scale, True)
+        z = a @ b.t()
+        within(out[rows], z, HALF * z.abs() + 136 * U * (a.abs() @ b.abs().t()) + cut_off(a, b), "output past 2^32")
+
+
+def test_calls_at_once_with_their_own_workspaces():
+    """Two streams, each with split products, and two captured graphs that share one workspace in turn."""
+    cases = [operands(34, 1286, 72, s, True) for s in (1, 2)]
+    want = [lce.lce_linear_blocks(*c).out for c in cases]
+    assert lce.lce_linear_blocks_workspace_bytes(34, 1286, 72) > 0
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[lce.lce_linear_blocks(*c, stream=st).out for c, st in zip(cases, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(a, b) for a, b in zip(pair, want))
+    ws = torch.empty(lce.lce_linear_blocks_workspace_bytes(34, 1286, 72), dtype=torch.uint8, device=DEV)
+    outs, graphs = [torch.empty_like(w) for w in want], [torch.cuda.CUDAGraph() for _ in cases]
+    for g, c, o in zip(graphs, cases, outs):
+        with torch.cuda.graph(g):
+            lce.lce_linear_blocks(*c, out=o, workspace=ws)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        for o in outs:
+            o.zero_()
+
+
+def test_rows_behind_the_last_are_left():
+    x, sx, w, sw = operands(40, 300, 72, 3, True)
+    out = torch.full((60, 80), 7.0, dtype=BF16, device=DEV)
+    lce.lce_linear_blocks(x, sx, w, sw, out=out[:40, :72])
+    assert bool((out[40:] == 7).all()) and bool((out[:, 72:] == 7).all())
+    assert torch.equal(out[:40, :72], lce.lce_linear_blocks(x, sx, w, sw).out)

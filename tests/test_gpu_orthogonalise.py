@@ -26,6 +26,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible to torch", allow_module_level=True)
 
+import blocks_plans  # noqa: E402
 import vocabulary_cross_entropy_row_amd as lce  # noqa: E402
 
 DEV = torch.device("cuda:0")
@@ -109,6 +110,31 @@ def test_batches(batch, r, c):
     G = torch.stack([matrix(r, c, 7 * k, "signal") * 10.0 ** k for k in range(min(batch, 5))] * -(-batch // 5))[:batch]
     got = lce.lce_orthogonalise(G)
     for k in range(batch):
+        check(G[k], got[k], f"matrix {k}")
+
+
+@pytest.mark.parametrize("batch,r,c", blocks_plans.ORTHO_COVER)
+def test_every_kernel(batch, r, c):
+    G = torch.stack([matrix(r, c, 5 * k, "signal" if k % 2 else "noise") for k in range(batch)])
+    got = lce.lce_orthogonalise(G)
+    for k in range(batch):
+        check(G[k], got[k], f"matrix {k}")
+
+
+@pytest.mark.parametrize("r,c", [(64, 4000), (1, 5000), (40, 70), (33, 65), (2900, 17), (64, 64), (32, 256), (48, 20000)])
+def test_up_to_64_rows(r, c):
+    for kind in ("noise", "signal"):
+        G = matrix(r, c, 3 * r + c, kind)
+        check(G, lce.lce_orthogonalise(G), kind)
+
+
+def test_offsets_past_32_bits():
+    G = torch.empty(33000, 128, 1024, dtype=BF16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    for part in G.split(3000):
+        part.normal_(generator=g)
+    got = lce.lce_orthogonalise(G)
+    for k in (0, 16383, 16384, 32767, 32768, 32999):
         check(G[k], got[k], f"matrix {k}")
 
 

@@ -1221,10 +1221,10 @@ lce_status check_ortho(const char *fn, int64_t batch, int64_t rows, int64_t cols
         return fail(LCE_ERR_INVALID_ARG, "%s: rows and cols must be >= 1 (got %lld, %lld)", fn, (long long)rows, (long long)cols);
     if (rows > (1 << 20) || cols > (1 << 20) || batch > 65535)
         return fail(LCE_ERR_UNSUPPORTED, "%s: rows and cols must be <= 2^20, batch <= 65535", fn);
-    // tiles of 64 x 64 at most: of X, and of A
+    // tiles of 64 x 64 in X; up to 64 rows two workgroups of 512 threads each
     const int64_t r = (rows < cols ? rows : cols) / 64 + 1, c = (rows < cols ? cols : rows) / 64 + 1;
-    if (r * c >= (int64_t(1) << 23) || batch * r * c >= (int64_t(1) << 23))
-        return fail(LCE_ERR_UNSUPPORTED, "%s: 2^23 or more tiles of 64 x 64", fn);
+    if (r * c >= (int64_t(1) << 22) || batch * r * c >= (int64_t(1) << 22))
+        return fail(LCE_ERR_UNSUPPORTED, "%s: 2^22 or more tiles of 64 x 64", fn);
     return LCE_OK;
 }
 

@@ -1,0 +1,62 @@
+// Which tiles the products of an orthogonalised update take (host code alone, so that it can be looked at
+// without a GPU; orthogonalise.hip has the tiles).
+#pragma once
+
+#include <algorithm>
+#include <stdint.h>
+
+namespace lce {
+namespace ortho_plan {
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
+constexpr int kSide[SHAPES] = {256, 128, 64, 128, 32}, kPerCu[SHAPES] = {1, 2, 2, 1, 2};
+// us of a step of 64 of K with one and two workgroups on a compute unit, and of a tile's start and end.
+// Fitted to the times of all five steps over 260 random shapes (batches of 1 to 16, 32 to 16384 rows and
+// columns) with each shape for each product, replayed from a graph: off by 12% (root mean square), and the
+// choice that the estimates make 2% slower than the fastest measured one on geometric average.
+constexpr double kStepUs[SHAPES][2] = {{1.03, 0}, {0.65, 0.94}, {0.33, 0.33}, {0.45, 0}, {0.27, 0.57}};
+constexpr double kTileUs[SHAPES] = {12.0, 3.4, 2.1, 4.3, 2.1};
+constexpr double kEven = 1.94;   // a step where workgroups are at different places of K and share less in the caches
+constexpr double kFoldUs = 3.0, kFoldRate = 10e6;   // the launch that adds pieces up, and its bytes a us
+constexpr int kCus = 256;
+
+struct Plan {
+    int shape, groups;      // groups == total: a workgroup a tile
+    int64_t tiles, total;   // of one matrix, of the batch
+};
+inline int64_t tiles_of(int64_t rows_x, int64_t rows_w, int side, bool sym) {
+    const int64_t t = ceil_div(rows_x, side);
+    return sym ? t * (t + 1) / 2 : t * ceil_div(rows_w, side);
+}
+// The shape with the least estimated time, a workgroup a tile; or, with `ranges` (X X^T, whose K is the longer
+// side), as many workgroups as fit on the card, with equal ranges of all steps, which costs each two ends
+// and the launch that adds the pieces up.
+inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool sym, bool ranges) {
+    Plan best{SMALL, 0, 0, 0};
+    double best_us = 1e30;
+    for (int i = 0; i < SHAPES; ++i) {
+        const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym), total = batch * tiles, slots = static_cast<int64_t>(kCus) * kPerCu[i];
+        double whole = static_cast<double>(total / slots) * (static_cast<double>(steps) * kStepUs[i][kPerCu[i] - 1] + kTileUs[i]);
+        if (total % slots) whole += static_cast<double>(steps) * kStepUs[i][ceil_div(total % slots, kCus) - 1] + kTileUs[i];
+        if (whole < best_us - 1e-9) {
+            best_us = whole;
+            best = {i, static_cast<int>(total), tiles, total};
+        }
+        const int64_t groups = std::min(slots, total * steps / 4);
+        if (!ranges || i == FINE || groups == total || groups < 1) continue;
+        const double depth = static_cast<double>(ceil_div(total * steps, groups)), pieces = static_cast<double>(std::min(2 * total, total + groups));
+        const double even = depth * kStepUs[i][ceil_div(groups, kCus) - 1] * kEven + 2.0 * kTileUs[i] + kFoldUs +
+                            pieces * kSide[i] * kSide[i] * 8 / kFoldRate;
+        if (even < best_us - 1e-9) {
+            best_us = even;
+            best = {i, static_cast<int>(groups), tiles, total};
+        }
+    }
+    return best;
+}
+
+}  // namespace ortho_plan
+}  // namespace lce

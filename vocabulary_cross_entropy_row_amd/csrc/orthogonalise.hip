@@ -4,19 +4,21 @@
 //
 // The three products run on the matrix cores in fp16, whose 11 bits keep eight times what bf16 does at the
 // same rate, with fp32 sums.  What would be lost is kept where it costs nothing:
-//   X      two fp16, hi + lo: the products read hi, the term a X both.  The products' share of X is small
-//          in the directions that a X still has to amplify, so those see no rounding of X.
+//   X      fp16 and what that leaves in e4m3 (15 bits together): the products read the fp16, the term a X
+//          both.  The products' share of X is small in the directions that a X still has to amplify, so
+//          those see little of X's rounding.
 //   A, B   their diagonals in fp32 vectors, the rest in fp16.  X approaches orthogonal rows, so A
 //          approaches its diagonal: A = D + O gives A A = O O + (D_t + D_f) O + D^2, and B X = diag X + rest.
-// Simulated over gaussian, low-rank and power-law spectra (256 to 1024 rows): 2e-4 to 7e-4 of the result
+// Simulated over gaussian, low-rank and power-law spectra (256 to 1024 rows): 2e-4 to 8e-4 of the result
 // (2-norm) where fp16 alone gives 1e-3 to 4e-3 and bf16 1e-2 to 3e-2; the bf16 output rounds at 1.7e-3.
 // Powers of two keep fp16 in range: X is held times S ~ sqrt(c) (|X| is at most about 1.2, its root mean
 // square at most 1.2 / sqrt(c)), O times 2^10, B times 2^8.
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed, and stored a second time
 // transposed.  All operands have K contiguous: X for A, O for O O, and for B X also X^T (hi), which the
-// product that forms X writes beside it.  A step is three launches, r^2 c + r^3 + 2 r^2 c operations.
-// Everything is padded with zeros to multiples of 64, so the products meet no edges.
+// product that forms X writes beside it.  A step is three launches, r^2 c + r^3 + 2 r^2 c operations (two
+// where B, of 64 rows at most, is formed by the workgroups that use it).  Everything is padded with zeros
+// to multiples of 64, so the products meet no edges.
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <math.h>
@@ -25,9 +27,12 @@
 #include "blocks_internal.h"
 #include "ce_device.h"
 #include "linear_mfma.h"
+#include "ortho_plan.h"
 
 namespace lce {
 namespace {
+
+using namespace ortho_plan;
 
 using dev::Elt;
 using dev::u32x4;
@@ -46,8 +51,6 @@ constexpr int64_t kUnit = 64;             // fp16 values of K in a step
 constexpr float kScaleO = 1024.0f, kScaleB = 256.0f;
 constexpr int kNormGroups = 1024;         // partial sums of squares per matrix, at most
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 __device__ __forceinline__ u32x4 pack_h8(const float (&v)[8]) {
@@ -329,7 +332,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     // to memory: slot 2 w for the piece that its range starts with, 2 w + 1 for one that it ends with.
     const int w = (blockIdx.x & 7) * g.per_xcd + (blockIdx.x >> 3);
     if (static_cast<int>(blockIdx.x >> 3) >= g.per_xcd || w >= g.groups) return;
-    const bool whole = !SYM || g.groups == g.total;
+    const bool whole = EPI != GRAM || g.groups == g.total;
     int tile = w, s0 = 0, left = g.steps;   // left: steps of the range
     if (!whole) {
         const int64_t units = static_cast<int64_t>(g.total) * g.steps, from = range_start(units, g.groups, w);
@@ -820,9 +823,9 @@ __device__ __forceinline__ int add_pieces(const float *p, int size, int first, i
     return N;
 }
 
-// The pieces of the tiles that more than one workgroup had, added in the order of their steps, 64 x 64 values
+// The pieces of X X^T's tiles that more than one workgroup had, added in the order of their steps, 64 x 64 values
 // a workgroup, stored as they are and, off the diagonal, transposed.
-template <int SIDE, int EPI>
+template <int SIDE>
 __global__ __launch_bounds__(256) void fold_kernel(Args g) {
     constexpr int PARTS = SIDE / 64;
     __shared__ float turn[64][65];
@@ -837,26 +840,18 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
     triangle(tile - z * g.per_batch, ti, fi);
     const int t0 = ti * SIDE + part / PARTS * 64, f0 = fi * SIDE + part % PARTS * 64;
     if (t0 >= g.rows_x || f0 >= g.rows_w) return;   // rows come in 64s
+    const float none[8] = {};
     const int first_slot = 2 * first + (range_start(units, g.groups, first) <= from ? 1 : 0);
-    const float *dz = g.d + static_cast<int64_t>(z) * g.rows_x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int tl = i * 32 + (th >> 3), fl = (th & 7) * 8, t = t0 + tl, f = f0 + fl;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, df[8] = {};
+        float v[8] = {};
         const float *p = g.part + static_cast<int64_t>(part / PARTS * 64 + tl) * SIDE + part % PARTS * 64 + fl;
         int k = first;
         while (last - k >= 4) k += add_pieces<16>(p, SIDE * SIDE, first, first_slot, k, last, v);
         if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, first_slot, k, last, v);
-        u32x4 o = {0u, 0u, 0u, 0u};
-        float dt = 0.0f;
-        if constexpr (EPI == POLY) {
-            o = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
-            dt = dz[t];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) df[u] = dz[f + u];
-        }
-        symmetric_values<EPI>(g, z, t, f, o, dt, df, v);
-        *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
+        symmetric_values<GRAM>(g, z, t, f, u32x4{}, 0.0f, none, v);
+        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
 #pragma unroll
         for (int u = 0; u < 8; ++u) turn[tl][fl + u] = v[u];
     }
@@ -868,7 +863,7 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
         float v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = turn[tl + u][fl];
-        *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + static_cast<int64_t>(f0 + fl) * g.ldo + t0 + tl) = pack_h8(v);
+        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(f0 + fl) * g.ldo + t0 + tl) = pack_h8(v);
     }
 }
 
@@ -878,53 +873,10 @@ using Big = linear::Shape<256, 256, 2, 4, 3, 2>;        // one workgroup of eigh
 using Mid = linear::Shape<128, 128, 2, 2, 3, 2>;        // two of four
 using Small = linear::Shape<64, 64, 2, 2, 4, 4>;        // two of four
 using MidDeep = linear::Shape<128, 128, 2, 2, 5, 4>;    // one of four, with more steps in flight
-enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
-constexpr int kSide[SHAPES] = {256, 128, 64, 128, 32}, kPerCu[SHAPES] = {1, 2, 2, 1, 2};
-static_assert(Big::BF == 256 && Mid::BF == 128 && Small::BF == 64 && MidDeep::BF == 128 && Big::PER_CU == 1 && Mid::PER_CU == 2 &&
-              Small::PER_CU == 2 && MidDeep::PER_CU == 1,
+static_assert(kSide[BIG] == Big::BF && kSide[MID] == Mid::BF && kSide[SMALL] == Small::BF && kSide[MID_DEEP] == MidDeep::BF &&
+              kPerCu[BIG] == Big::PER_CU && kPerCu[MID] == Mid::PER_CU && kPerCu[SMALL] == Small::PER_CU && kPerCu[MID_DEEP] == MidDeep::PER_CU,
               "the plan's tiles are the kernels'");
-// us of a step of K with one and two workgroups on a compute unit, and of a tile's start and end.  Fitted
-// to the times of all five steps over 260 random shapes (batches of 1 to 16, 32 to 16384 rows and columns)
-// with each shape for each product, replayed from a graph: off by 12% (root mean square), and the choice
-// that the estimates make 3% slower than the fastest measured one on geometric average.
-constexpr double kStepUs[SHAPES][2] = {{1.03, 0}, {0.65, 0.94}, {0.33, 0.33}, {0.45, 0}, {0.27, 0.57}};
-constexpr double kTileUs[SHAPES] = {6.9, 3.4, 2.1, 4.3, 2.1};
-constexpr double kEven = 1.94;   // a step where workgroups are at different places of K and share little in the caches
-constexpr int kCus = 256;
 
-struct Plan {
-    int shape, groups;
-    int64_t tiles, total;   // of one matrix, of the batch
-};
-int64_t tiles_of(int64_t rows_x, int64_t rows_w, int side, bool sym) {
-    const int64_t t = ceil_div(rows_x, side);
-    return sym ? t * (t + 1) / 2 : t * ceil_div(rows_w, side);
-}
-// The shape with the least estimated time, a workgroup a tile; or (symmetric products) as many workgroups as
-// fit on the card, with equal ranges of all steps, which costs each two ends and the launch that adds the
-// pieces up.
-Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool sym) {
-    Plan best{SMALL, 0, 0, 0};
-    double best_us = 1e30;
-    for (int i = 0; i < SHAPES; ++i) {
-        const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym), total = batch * tiles, slots = static_cast<int64_t>(kCus) * kPerCu[i];
-        double whole = static_cast<double>(total / slots) * (static_cast<double>(steps) * kStepUs[i][kPerCu[i] - 1] + kTileUs[i]);
-        if (total % slots) whole += static_cast<double>(steps) * kStepUs[i][ceil_div(total % slots, kCus) - 1] + kTileUs[i];
-        if (whole < best_us - 1e-9) {
-            best_us = whole;
-            best = {i, static_cast<int>(total), tiles, total};
-        }
-        const int64_t groups = std::min(slots, total * steps / 4);
-        if (!sym || i == FINE || groups == total || groups < 1) continue;
-        const double depth = static_cast<double>(ceil_div(total * steps, groups)), pieces = static_cast<double>(std::min(2 * total, total + groups));
-        const double even = depth * kStepUs[i][ceil_div(groups, kCus) - 1] * kEven + 2.0 * kTileUs[i] + 1.1 + pieces * kSide[i] * kSide[i] * 8 / 25e6;
-        if (even < best_us - 1e-9) {
-            best_us = even;
-            best = {i, static_cast<int>(groups), tiles, total};
-        }
-    }
-    return best;
-}
 size_t piece_bytes(const Plan &p) {
     return p.groups == p.total ? 0 : static_cast<size_t>(p.groups) * 2 * kSide[p.shape] * kSide[p.shape] * 4;
 }
@@ -944,9 +896,9 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     L.cp = round_up(L.c, kUnit);
     L.ldx = apart(L.cp);
     L.ldr = apart(L.rp);
-    L.gram = plan_of(batch, L.rp, L.rp, L.cp / kUnit, true);
-    L.poly = plan_of(batch, L.rp, L.rp, L.rp / kUnit, true);
-    L.apply = plan_of(batch, L.rp, L.cp, L.rp / kUnit, false);
+    L.gram = plan_of(batch, L.rp, L.rp, L.cp / kUnit, true, true);
+    L.poly = plan_of(batch, L.rp, L.rp, L.rp / kUnit, true, false);
+    L.apply = plan_of(batch, L.rp, L.cp, L.rp / kUnit, false, false);
     const size_t x = align256(static_cast<size_t>(batch) * L.rp * L.ldx * 2), t = align256(static_cast<size_t>(batch) * L.cp * L.ldr * 2);
     const size_t s = align256(static_cast<size_t>(batch) * L.rp * L.ldr * 2), v = align256(static_cast<size_t>(batch) * L.rp * 4);
     size_t o = 0;
@@ -960,7 +912,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     L.off_e = o;     o += v;
     L.off_norm = o;  o += align256(static_cast<size_t>(batch) * kNormGroups * 8);
     L.off_part = o;
-    o += std::max(piece_bytes(L.gram), piece_bytes(L.poly));
+    o += piece_bytes(L.gram);
     L.bytes = o;
     return L;
 }
@@ -968,12 +920,12 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
 template <class S, int EPI>
 hipError_t launch_tiles(const Args &g, hipStream_t st) {
     hipLaunchKernelGGL((ortho_kernel<S, EPI>), dim3(static_cast<unsigned>(g.per_xcd) * 8u), dim3(64 * S::NW), 0, st, g);
-    if constexpr (EPI == GRAM || EPI == POLY) {
+    if constexpr (EPI == GRAM) {
         if (g.groups != g.total) {
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
             constexpr int parts = S::BF / 64 * (S::BF / 64);
-            hipLaunchKernelGGL((fold_kernel<S::BF, EPI>), dim3(static_cast<unsigned>(g.total) * parts), dim3(256), 0, st, g);
+            hipLaunchKernelGGL((fold_kernel<S::BF>), dim3(static_cast<unsigned>(g.total) * parts), dim3(256), 0, st, g);
         }
     }
     return hipGetLastError();
