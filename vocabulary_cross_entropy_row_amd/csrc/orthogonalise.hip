@@ -60,6 +60,11 @@ __device__ __forceinline__ u32x4 pack_h8(const float (&v)[8]) {
     return __builtin_bit_cast(u32x4, h);
 }
 
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 pack_h4(const float (&v)[4]) {
+    return __builtin_bit_cast(uint2, (h4){static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]), static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])});
+}
+
 typedef float f2v __attribute__((ext_vector_type(2)));
 // Holds a matrix instruction to its place in the order of the code (blocks_mfma.h).  In the accumulation
 // registers: where a wave has more than 256, the compiler keeps sums there, and copies them both ways for
@@ -236,20 +241,24 @@ __device__ __forceinline__ void triangle(int mn, int &ti, int &fi) {
     fi = mn - ti * (ti + 1) / 2;
 }
 
-// GRAM: values v of A to O and its diagonal.  POLY: values of O O to B, from O there, the diagonal at t and
-// at f .. f + 7.
+// Values v of A, N of row t from column f on, to O and its diagonal
+template <int N>
+__device__ __forceinline__ void gram_values(const Args &g, int z, int t, int f, float (&v)[N]) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        v[u] *= g.inv;
+        if (t == f + u) {
+            g.d[static_cast<int64_t>(z) * g.rows_x + t] = v[u];
+            v[u] = 0.0f;
+        }
+        v[u] *= kScaleO;
+    }
+}
+// The same, or (POLY) values of O O to B, from O there, the diagonal at t and at f .. f + 7
 template <int EPI>
 __device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, int f, u32x4 oq, float dt, const float (&df)[8], float (&v)[8]) {
     if constexpr (EPI == GRAM) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            v[u] *= g.inv;
-            if (t == f + u) {
-                g.d[static_cast<int64_t>(z) * g.rows_x + t] = v[u];
-                v[u] = 0.0f;
-            }
-            v[u] *= kScaleO;
-        }
+        gram_values(g, z, t, f, v);
     } else {
         const h8 o = __builtin_bit_cast(h8, oq);
 #pragma unroll
@@ -804,32 +813,32 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
 
 // Adds pieces k .. k + N - 1, up to the last, to v; all of their loads are under way at once.
 template <int N>
-__device__ __forceinline__ int add_pieces(const float *p, int size, int first, int first_slot, int k, int last, float (&v)[8]) {
-    float4 x[N], y[N];
+__device__ __forceinline__ int add_pieces(const float *p, int size, int first, int first_slot, int k, int last, float (&v)[4]) {
+    float4 x[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const int i = min(k + u, last);
-        const float4 *q = reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i == first ? first_slot : 2 * i) * size);
-        x[u] = q[0];
-        y[u] = q[1];
+        x[u] = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i == first ? first_slot : 2 * i) * size);
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const bool in = k + u <= last;   // a choice and no branch, or each load moves behind one
-        const float q[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+        const float q[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = in ? v[e] + q[e] : v[e];
+        for (int e = 0; e < 4; ++e) v[e] = in ? v[e] + q[e] : v[e];
     }
     return N;
 }
 
-// The pieces of X X^T's tiles that more than one workgroup had, added in the order of their steps, 64 x 64 values
-// a workgroup, stored as they are and, off the diagonal, transposed.
+// The pieces of X X^T's tiles that more than one workgroup had, added in the order of their steps, 16 x 64
+// values a workgroup (few tiles have many pieces each, and a thread's chain of loads is the launch's time: 64 x
+// 12000 with its 47 pieces of one tile FOLDPERF), stored as they are and, off the diagonal, transposed.
+constexpr int kFoldRows = 16;
 template <int SIDE>
 __global__ __launch_bounds__(256) void fold_kernel(Args g) {
-    constexpr int PARTS = SIDE / 64;
-    __shared__ float turn[64][65];
-    const int tile = blockIdx.x / (PARTS * PARTS), part = blockIdx.x % (PARTS * PARTS), th = threadIdx.x;
+    constexpr int ACROSS = SIDE / 64, PARTS = ACROSS * (SIDE / kFoldRows);
+    __shared__ float turn[kFoldRows][65];
+    const int tile = blockIdx.x / PARTS, part = blockIdx.x % PARTS, th = threadIdx.x;
     const int64_t units = static_cast<int64_t>(g.total) * g.steps, from = static_cast<int64_t>(tile) * g.steps;
     // the last range that starts at or before a unit u is ceil((u + 1) groups / units) - 1
     auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * g.groups + units - 1) / units) - 1; };
@@ -838,33 +847,26 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
     const int z = tile / g.per_batch;
     int ti, fi;
     triangle(tile - z * g.per_batch, ti, fi);
-    const int t0 = ti * SIDE + part / PARTS * 64, f0 = fi * SIDE + part % PARTS * 64;
+    const int tp = part / ACROSS * kFoldRows, fp = part % ACROSS * 64, t0 = ti * SIDE + tp, f0 = fi * SIDE + fp;
     if (t0 >= g.rows_x || f0 >= g.rows_w) return;   // rows come in 64s
-    const float none[8] = {};
     const int first_slot = 2 * first + (range_start(units, g.groups, first) <= from ? 1 : 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int tl = i * 32 + (th >> 3), fl = (th & 7) * 8, t = t0 + tl, f = f0 + fl;
-        float v[8] = {};
-        const float *p = g.part + static_cast<int64_t>(part / PARTS * 64 + tl) * SIDE + part % PARTS * 64 + fl;
-        int k = first;
-        while (last - k >= 4) k += add_pieces<16>(p, SIDE * SIDE, first, first_slot, k, last, v);
-        if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, first_slot, k, last, v);
-        symmetric_values<GRAM>(g, z, t, f, u32x4{}, 0.0f, none, v);
-        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h8(v);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) turn[tl][fl + u] = v[u];
-    }
+    const int tl = th >> 4, fl = (th & 15) * 4, t = t0 + tl, f = f0 + fl;
+    float v[4] = {};
+    const float *p = g.part + static_cast<int64_t>(tp + tl) * SIDE + fp + fl;
+    int k = first;
+    while (last - k >= 4) k += add_pieces<24>(p, SIDE * SIDE, first, first_slot, k, last, v);
+    if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, first_slot, k, last, v);
+    gram_values(g, z, t, f, v);
+    *reinterpret_cast<uint2 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h4(v);
     if (ti == fi) return;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) turn[tl][fl + u] = v[u];
     __syncthreads();
+    const int row = th >> 2, from_t = (th & 3) * 4;
+    float w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int fl = i * 32 + (th >> 3), tl = (th & 7) * 8;
-        float v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = turn[tl + u][fl];
-        *reinterpret_cast<u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(f0 + fl) * g.ldo + t0 + tl) = pack_h8(v);
-    }
+    for (int u = 0; u < 4; ++u) w[u] = turn[from_t + u][row];
+    *reinterpret_cast<uint2 *>(g.o + z * g.ob + static_cast<int64_t>(f0 + row) * g.ldo + t0 + from_t) = pack_h4(w);
 }
 
 // ---- plan and launches ---------------------------------------------------------------------------
@@ -924,7 +926,7 @@ hipError_t launch_tiles(const Args &g, hipStream_t st) {
         if (g.groups != g.total) {
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            constexpr int parts = S::BF / 64 * (S::BF / 64);
+            constexpr int parts = S::BF / 64 * (S::BF / kFoldRows);
             hipLaunchKernelGGL((fold_kernel<S::BF>), dim3(static_cast<unsigned>(g.total) * parts), dim3(256), 0, st, g);
         }
     }
