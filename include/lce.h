@@ -561,7 +561,9 @@ lce_status lce_quantize_blocks(const void *x, int64_t ldx, lce_dtype dtype, int6
  *   x, weight     device e4m3 [n, ldx], [M, ldw].
  *   scale_x       device, LCE_F32 (any numbers) or LCE_E8M0, strides sx_row, sx_col.
  *   scale_w       the same for weight, sw_row per 128 rows.  Scales that are e8m0 on
- *                 both sides are applied by the matrix instructions.
+ *                 both sides are applied by the matrix instructions; of others the
+ *                 product scale_x scale_w is formed first, in fp32 (below 2^-126 it has
+ *                 fewer bits).
  *   bias          device [M] F32 or BF16, or NULL.
  *   residual      device bf16 [n, ldr], or NULL; may be `out` itself.
  *   out           device bf16 [n, ldo].

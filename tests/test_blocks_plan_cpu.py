@@ -46,4 +46,5 @@ def test_product_plans_are_within_their_limits(plans):
 def test_every_update_has_a_size(plans):
     taken = {(k, *p) for size in blocks_plans.ORTHO_COVER for k, p in enumerate(plans[1](*size))}
     shapes = set(blocks_plans.ORTHO_SHAPES)
-    assert taken == {(k, s, False) for k in range(3) for s in shapes} | {(0, s, True) for s in shapes - {"32"}}
+    tiles = shapes - {"32"}
+    assert taken == {(k, s, False) for k in range(3) for s in (shapes if k else tiles)} | {(0, s, True) for s in tiles}

@@ -241,6 +241,19 @@ def test_what_lies_past_the_width_does_not_matter(n, power):
         assert torch.equal(lce.lce_linear_blocks(px, other, pw, sw.t().contiguous().t()).out, want)
 
 
+@pytest.mark.parametrize("power", [True, False], ids=["e8m0", "f32"])
+@pytest.mark.parametrize("n", [9, 40, 300])
+def test_scales_far_from_one(n, power):
+    """Each pair's product near 1, the scales themselves 2^100 and 2^-100; and pairs whose products differ by 2^60."""
+    x, sx, w, sw = operands(n, 300, 260, n, power)
+    for up in (100, -100):
+        bx, bw = (t.float() * 2.0 ** e for t, e in ((sx, up), (sw, -up)))
+        check_product(x, bx.to(sx.dtype), w, bw.to(sw.dtype))
+    steps = torch.tensor([0.0, 60.0, -60.0], device=DEV)
+    check_product(x, (sx.float() * torch.exp2(steps)).to(sx.dtype), w, sw)
+    check_product(x, sx, w, (sw.float() * torch.exp2(-steps)).to(sw.dtype))
+
+
 def test_a_nan_scale_reaches_its_rows_alone():
     for power in (True, False):
         for n in (9, 200):

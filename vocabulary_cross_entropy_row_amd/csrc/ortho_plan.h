@@ -33,11 +33,13 @@ inline int64_t tiles_of(int64_t rows_x, int64_t rows_w, int side, bool sym) {
 }
 // The shape with the least estimated time, a workgroup a tile; or, with `ranges` (X X^T, whose K is the longer
 // side), as many workgroups as fit on the card, with equal ranges of all steps, which costs each two ends
-// and the launch that adds the pieces up.
+// and the launch that adds the pieces up.  FINE is no faster for X X^T (K is not short: 256 x 1024 92 us, with
+// tiles of 64 89) and is not built for it.
 inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps, bool sym, bool ranges) {
     Plan best{SMALL, 0, 0, 0};
     double best_us = 1e30;
     for (int i = 0; i < SHAPES; ++i) {
+        if (i == FINE && ranges) continue;
         const int64_t tiles = tiles_of(rows_x, rows_w, kSide[i], sym), total = batch * tiles, slots = static_cast<int64_t>(kCus) * kPerCu[i];
         double whole = static_cast<double>(total / slots) * (static_cast<double>(steps) * kStepUs[i][kPerCu[i] - 1] + kTileUs[i]);
         if (total % slots) whole += static_cast<double>(steps) * kStepUs[i][ceil_div(total % slots, kCus) - 1] + kTileUs[i];
@@ -46,7 +48,7 @@ inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps
             best = {i, static_cast<int>(total), tiles, total};
         }
         const int64_t groups = std::min(slots, total * steps / 4);
-        if (!ranges || i == FINE || groups == total || groups < 1) continue;
+        if (!ranges || groups == total || groups < 1) continue;
         const double depth = static_cast<double>(ceil_div(total * steps, groups)), pieces = static_cast<double>(std::min(2 * total, total + groups));
         const double even = depth * kStepUs[i][ceil_div(groups, kCus) - 1] * kEven + 2.0 * kTileUs[i] + kFoldUs +
                             pieces * kSide[i] * kSide[i] * 8 / kFoldRate;

@@ -19,6 +19,14 @@
 // product that forms X writes beside it.  A step is three launches, r^2 c + r^3 + 2 r^2 c operations (two
 // where B, of 64 rows at most, is formed by the workgroups that use it).  Everything is padded with zeros
 // to multiples of 64, so the products meet no edges.
+//
+// 4096 x 16384 in five steps takes 4.8 to 5.2 ms, 0.86 to 0.93 PFLOP/s where a library fp16 product reaches
+// 1.4 to 1.5: a step is X X^T (323 to 338 us, 136 tiles on 256 compute units, whose matrix units are busy 41% of the time),
+// A A (105, the same tiles and a quarter of the depth) and B X (545 to 580; busy 54% at the 1.65 GHz that
+// their power leaves; 440 of it the main loop, the rest its ends, which read and write 0.5 GB of X).  Small
+// ones are their launches: 256 x 1024, 17 launches, 89 us from a graph.
+// The steps from two fp16 for X (4096 x 16384): the lower half in 8 bits and tiles chosen for each product,
+// instructions held in place between LDS reads (1003 x 517 x 4 161 -> 149 us, 2048 x 2048 886 -> 380).
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <math.h>
@@ -128,7 +136,7 @@ struct LoadArgs {
 };
 
 // Sums of squares in fp64, a fixed share of the rows' 2048-value pieces per workgroup: no square of a
-// finite fp32 value overflows, and the order is fixed.
+// finite fp32 value overflows, and the order is fixed.  (4096 x 16384 bf16: 35 us, 3.8 TB/s.)
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_kernel(LoadArgs a) {
     __shared__ double sums[4];
@@ -152,7 +160,8 @@ __global__ __launch_bounds__(256) void norm_kernel(LoadArgs a) {
     if (threadIdx.x == 0) a.part[blockIdx.y * kNormGroups + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
-// A workgroup takes 64 x 64 of X: hi, lo and the transposed hi, zeros in the padding.
+// A workgroup takes 64 x 64 of X: hi, lo and the transposed hi, zeros in the padding (4096 x 16384 bf16: 97 us,
+// 4.8 TB/s of what it reads and writes).
 template <bool BF16>
 __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
     __shared__ float tile[64][65];
@@ -591,12 +600,13 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
 // Where the tiles above are few and short, a launch is their loads, barriers and chained instructions one
 // after the other.  Here a workgroup takes 32 x 32 values, its eight waves an eighth of K each, straight
 // from memory to the registers of the matrix instruction, all of it asked for at once up to K = 1024; the
-// waves' sums meet in LDS and are added in wave order.
+// waves' sums meet in LDS and are added in wave order.  Over 221 random shapes it is the fastest for A A of 131
+// (3 us of a call's five on average) and for B X of 35 (3 us).
 constexpr int kFineWaves = 8;
 
-template <int EPI>
+template <int EPI>   // all but GRAM
 __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
-    constexpr bool SYM = EPI == GRAM || EPI == POLY;
+    constexpr bool SYM = EPI == POLY;
     constexpr int U = 8, LD = 36;   // instructions' operands at once; floats between tokens
     __shared__ __attribute__((aligned(16))) float sums[kFineWaves][32 * LD];
     const int w = (blockIdx.x & 7) * g.per_xcd + (blockIdx.x >> 3);
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
     u32x4 hi = {0u, 0u, 0u, 0u};
     uint2 lo = make_uint2(0u, 0u);
     float et = 0.0f, df[8] = {};
-    if (th < 128 && EPI != GRAM) {
+    if (th < 128) {
         const int64_t row = static_cast<int64_t>(z) * g.rows_x;
         if constexpr (EPI == POLY) {
             hi = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
@@ -832,7 +842,7 @@ __device__ __forceinline__ int add_pieces(const float *p, int size, int first, i
 
 // The pieces of X X^T's tiles that more than one workgroup had, added in the order of their steps, 16 x 64
 // values a workgroup (few tiles have many pieces each, and a thread's chain of loads is the launch's time: 64 x
-// 12000 with its 47 pieces of one tile FOLDPERF), stored as they are and, off the diagonal, transposed.
+// 12000, with 47 pieces of its one tile, 11.3 us with 64 x 64 a workgroup, 4.6 so), stored as they are and, off the diagonal, transposed.
 constexpr int kFoldRows = 16;
 template <int SIDE>
 __global__ __launch_bounds__(256) void fold_kernel(Args g) {
@@ -944,7 +954,8 @@ hipError_t launch_product(Args g, const Plan &p, hipStream_t st) {
         case MID: return launch_tiles<Mid, EPI>(g, st);
         case MID_DEEP: return launch_tiles<MidDeep, EPI>(g, st);
         case FINE:
-            hipLaunchKernelGGL((fine_kernel<EPI>), dim3(static_cast<unsigned>(g.per_xcd) * 8u), dim3(64 * kFineWaves), 0, st, g);
+            if constexpr (EPI == GRAM) return hipErrorInvalidValue;   // not planned
+            else hipLaunchKernelGGL((fine_kernel<EPI>), dim3(static_cast<unsigned>(g.per_xcd) * 8u), dim3(64 * kFineWaves), 0, st, g);
             return hipGetLastError();
         default: return launch_tiles<Small, EPI>(g, st);
     }

@@ -14,6 +14,11 @@
 // of them: a row's 128 lie in 16 neighbouring lanes, a column's in 16 lanes of four waves, and the eight
 // rows of a column make eight neighbouring bytes of the transpose, which goes out through LDS in whole
 // 128-byte rows.
+//
+// Bound by memory: 8192 x 6656 bf16 both ways 41 us, 5.3 TB/s of the 218 MB that it has to move (a copy of
+// 1 GiB reaches 5.1); 16384 x 4096 fp32 in tiles both ways 74 to 79 us, 5.1 to 5.4 TB/s.  What got it there
+// (8192 x 6656): loads of a whole 8 x 8 without branches (54 -> 41 us with values kept as stored and the
+// largest magnitudes taken by pairs; 66 -> 54 with rows that a block ends inside of in one load).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
