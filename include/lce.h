@@ -630,8 +630,8 @@ size_t lce_linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M
  *                 n, K, M) bytes.  Clobbered; calls that share it must not run at the
  *                 same time.
  * Sizes and alignments as for lce_linear_blocks, K below 2^23, n and M at most 2^23 -
- * 1024 and fewer than 2^24 blocks in grad_out.  Outputs must not be an operand
- * (LCE_ERR_INVALID_ARG).  n == 0 writes zeros to grad_weight and grad_bias.
+ * 1024 and fewer than 2^24 blocks in grad_out.  Outputs must not be an operand or one
+ * another (LCE_ERR_INVALID_ARG).  n == 0 writes zeros to grad_weight and grad_bias.
  */
 lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dtype grad_dtype, const void *xt,
                                       int64_t ldxt, const void *scale_xt, int64_t sxt_row, int64_t sxt_col,

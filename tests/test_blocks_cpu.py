@@ -87,7 +87,7 @@ def backward(**over):
     (dict(ldxt=47), UNSUPPORTED, "16-byte"), (dict(ldwt=496), INVALID, "row stride of wt"), (dict(sxt=None), INVALID, "scale_xt"),
     (dict(swt=None), INVALID, "scale_wt"), (dict(wsb=100), INVALID, "workspace_bytes"), (dict(ws=WS + 16), INVALID, "256-byte"),
     (dict(gx=A), INVALID, "an operand"), (dict(gw=D), INVALID, "an operand"), (dict(gb=C), INVALID, "an operand"),
-    (dict(gw=F + 1), INVALID, "aligned"), (dict(ldgx=299), INVALID, "grad_x"),
+    (dict(gw=F + 1), INVALID, "aligned"), (dict(ldgx=299), INVALID, "grad_x"), (dict(gw=F), INVALID, "same buffer"),
 ])
 def test_backward_refuses(over, status, needle):
     st, msg = backward(**over)

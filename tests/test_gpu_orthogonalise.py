@@ -176,7 +176,7 @@ def test_zeros_and_values_that_are_no_numbers():
     assert torch.equal(got[0], clean[0]) and torch.equal(got[4], clean[4])
 
 
-@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e30])
+@pytest.mark.parametrize("scale", [1e-40, 1e-30, 1e-12, 1e30, 5e37])
 def test_scale_of_the_gradient(scale):
     G = matrix(80, 100, 4).double() * scale * 1e3
     G = G.float()

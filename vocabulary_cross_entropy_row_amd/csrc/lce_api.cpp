@@ -1184,9 +1184,12 @@ lce_status lce_linear_blocks_backward(const void *grad_out, int64_t ldg, lce_dty
         return fail(LCE_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
     const void *ins[5] = {grad_out, xt, scale_xt, wt, scale_wt};
     const void *outs[3] = {grad_x, grad_weight, grad_bias};
-    for (const void *o : outs)
-        for (const void *i : ins)
-            if (o && o == i) return fail(LCE_ERR_INVALID_ARG, "%s: an output must not be an operand", fn);
+    for (int i = 0; i < 3; ++i) {
+        for (const void *in : ins)
+            if (outs[i] && outs[i] == in) return fail(LCE_ERR_INVALID_ARG, "%s: an output must not be an operand", fn);
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return fail(LCE_ERR_INVALID_ARG, "%s: two outputs are the same buffer", fn);
+    }
     lce::BlocksGradArgs a{};
     a.grad_out = grad_out;
     a.ldg = ldg;

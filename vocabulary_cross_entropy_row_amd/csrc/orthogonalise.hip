@@ -182,11 +182,12 @@ __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
     if ((t & 63) == 0) sums[t >> 6] = s;
     __syncthreads();
     s = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    const float factor = static_cast<float>(static_cast<double>(a.s) / (sqrt(s) + static_cast<double>(a.eps)));
+    // fp64: of the smallest and the largest fp32 values the factor is no normal fp32 number
+    const double factor = static_cast<double>(a.s) / (sqrt(s) + static_cast<double>(a.eps));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tile[i * 32 + (t >> 3)][(t & 7) * 8 + e] = v[i][e] * factor;
+        for (int e = 0; e < 8; ++e) tile[i * 32 + (t >> 3)][(t & 7) * 8 + e] = static_cast<float>(v[i][e] * factor);
     __syncthreads();
     // eight values along a row of X, and along a row of X^T
 #pragma unroll
