@@ -482,3 +482,25 @@ def test_rows_behind_the_last_are_left():
     lce.lce_linear_blocks(x, sx, w, sw, out=out[:40, :72])
     assert bool((out[40:] == 7).all()) and bool((out[:, 72:] == 7).all())
     assert torch.equal(out[:40, :72], lce.lce_linear_blocks(x, sx, w, sw).out)
+
+
+def test_no_rows():
+    x = torch.empty(0, 300, device=DEV)
+    got = lce.lce_quantize_blocks(x, blocks="row", transposed="tile")
+    assert got.values.shape == (0, 300) and got.scale.shape == (0, 3) and got.values_t.shape == (300, 0) and got.scale_t.shape == (3, 0)
+    w = lce.lce_quantize_blocks(normal(1)(40, 300), blocks="tile")
+    assert lce.lce_linear_blocks(got.values, got.scale, w.values, w.scale).out.shape == (0, 40)
+    assert lce.lce_orthogonalise(torch.empty(0, 8, 8, device=DEV)).shape == (0, 8, 8)
+
+
+@pytest.mark.parametrize("n,K", [(1, 130), (130, 1), (1, 1)])
+def test_single_rows_and_columns_with_odd_strides(n, K):
+    """A single row or column may have any stride; the operands that come of it are read as they lie."""
+    x = torch.as_strided(normal(6)(4000), (n, K), (1 if n == 1 else 7 + K, 1 if K > 1 else 3))
+    got = check_quantiser(x, "row", "tile")
+    w = lce.lce_quantize_blocks(normal(7)(20, K), blocks="tile")
+    check_product(got.values, got.scale, w.values, w.scale)
+    wide = torch.zeros(n, 256, dtype=torch.uint8, device=DEV).view(E4M3)[:, :K]
+    wide.view(torch.uint8).copy_(got.values.view(torch.uint8))
+    assert torch.equal(lce.lce_linear_blocks(wide, got.scale, w.values, w.scale).out,
+                       lce.lce_linear_blocks(got.values, got.scale, w.values, w.scale).out)
