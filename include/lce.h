@@ -648,9 +648,10 @@ size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t 
  *   A = X X^T,   X <- a X + (b A + c A A) X
  * and out the last X, transposed back.  (3.4445, -4.7750, 2.0315) over five steps takes
  * singular values from about 0.002 to 1 to between 0.7 and 1.2.  The products run in fp16
- * with fp32 sums; X is held in fp16 and an 8-bit rest, the diagonals of A and b A + c A A in
- * fp32, so the result is off by 2e-4 to 8e-4 (2-norm; five steps of those coefficients)
- * before it is rounded to bf16.  Coefficients under which values pass 256 overflow.
+ * with fp32 sums; X is held in two fp16 (22 bits), the diagonals of A and b A + c A A in
+ * fp32.  With five steps of those coefficients the result is off by up to 1.0e-3 of it
+ * (Frobenius norm; 2-norm 1.9e-3) before it is rounded to bf16, matrices of few directions
+ * included, and by up to 6e-3 below 64 rows.  Coefficients under which values pass 256 overflow.
  *   g           device [batch][rows, cols], row stride ldg and g_batch_stride elements
  *               between matrices, dtype F32 or BF16.  A matrix of zeros gives zeros (eps
  *               above 0); one that holds an infinity or a NaN gives NaN, in itself alone.

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <stdint.h>
 
 namespace lce {
@@ -58,6 +59,19 @@ inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps
         }
     }
     return best;
+}
+
+// Whether B X takes what fp16 leaves of X too, with rows and |a| of the update.
+//
+// a X + B X is (a + B) X, whose rows stay in the space of X's, if both terms have the same X.  With fp16's X in
+// the product alone, what fp16 leaves makes directions that X did not have, of the second order in fp16's
+// step, and the steps multiply them by `a` each: about 9e-4 |a|^steps / r of the result (Frobenius norm) where G has
+// one direction, as the definition with the kernel's roundings shows (five default steps: 64 x 64 5.4e-3, 512 x 1024
+// 8.6e-4; eight: 1.4e-1, 2.2e-2).  Where that could reach half of the bf16 output's rounding, 1.7e-3, the product takes
+// both (6.0e-4; eight: 2.1e-3, 2.7e-3, where products in fp32 give 1.7e-3, 2.6e-3), for twice its instructions.
+// Up to 64 rows they cost nothing.
+inline bool takes_rest(int64_t r, int steps, double a) {
+    return r <= 64 || steps * std::log(std::fabs(a)) > std::log(static_cast<double>(r));
 }
 
 }  // namespace ortho_plan

@@ -4,29 +4,31 @@
 //
 // The three products run on the matrix cores in fp16, whose 11 bits keep eight times what bf16 does at the
 // same rate, with fp32 sums.  What would be lost is kept where it costs nothing:
-//   X      fp16 and what that leaves in e4m3 (15 bits together): the products read the fp16, the term a X
-//          both.  The products' share of X is small in the directions that a X still has to amplify, so
-//          those see little of X's rounding.
+//   X      fp16 and what that leaves in fp16, 22 bits together.  X X^T reads the first, a X both, and B X both
+//          where that shows (ortho_plan.h).  What the steps make of a gradient of few directions hangs on it: held
+//          in 15 bits and with fp16's X in B X, X picked up directions that grow by a step each (64 x 64 of one
+//          direction 6.0e-3 of the result in five steps, 1.6e-1 in eight; now 6.0e-4 and 2.1e-3).
 //   A, B   their diagonals in fp32 vectors, the rest in fp16.  X approaches orthogonal rows, so A
 //          approaches its diagonal: A = D + O gives A A = O O + (D_t + D_f) O + D^2, and B X = diag X + rest.
-// Simulated over gaussian, low-rank and power-law spectra (256 to 1024 rows): 2e-4 to 8e-4 of the result
-// (2-norm) where fp16 alone gives 1e-3 to 4e-3 and bf16 1e-2 to 3e-2; the bf16 output rounds at 1.7e-3.
-// Powers of two keep fp16 in range: X is held times S ~ sqrt(c) (|X| is at most about 1.2, its root mean
-// square at most 1.2 / sqrt(c)), O times 2^10, B times 2^8.
+// With these roundings put into the definition (gaussian matrices with even and uneven rows, of 1 to 16
+// directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.0e-3 of the result in the
+// Frobenius norm and 1.9e-3 in the 2-norm from 64 rows on, and by up to 5e-3 and 6e-3 below; the bf16 output rounds at 1.7e-3.
+// Powers of two keep fp16 in range: X is held times 2^14 (its values are at most 1.21), O times 2^10, B times 2^8.
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed, and stored a second time
-// transposed.  All operands have K contiguous: X for A, O for O O, and for B X also X^T (hi), which the
-// product that forms X writes beside it.  A step is three launches, r^2 c + r^3 + 2 r^2 c operations (two
-// where B, of 64 rows at most, is formed by the workgroups that use it).  Everything is padded with zeros
-// to multiples of 64, so the products meet no edges.
+// transposed.  All operands have K contiguous: X for A, O for O O, and for B X also X^T, which the
+// product that forms X writes beside it (its rest behind it in each row, B's rows starting again there).
+// A step is three launches, r^2 c + r^3 + 2 r^2 c operations, another 2 r^2 c with the rest (two launches where
+// B, of 64 rows at most, is formed by the workgroups that use it).  Everything is padded with zeros to multiples
+// of 64, so the products meet no edges.
 //
-// 4096 x 16384 in five steps takes 4.8 to 5.2 ms, 0.86 to 0.93 PFLOP/s where a library fp16 product reaches
-// 1.4 to 1.5: a step is X X^T (323 to 338 us, 136 tiles on 256 compute units, whose matrix units are busy 41% of the time),
-// A A (105, the same tiles and a quarter of the depth) and B X (545 to 580; busy 54% at the 1.65 GHz that
-// their power leaves; 440 of it the main loop, the rest its ends, which read and write 0.5 GB of X).  Small
-// ones are their launches: 256 x 1024, 17 launches, 89 us from a graph.
-// The steps from two fp16 for X (4096 x 16384): the lower half in 8 bits and tiles chosen for each product,
-// instructions held in place between LDS reads (1003 x 517 x 4 161 -> 149 us, 2048 x 2048 886 -> 380).
+// 4096 x 16384 in five steps takes 4.9 to 5.2 ms, 0.86 to 0.92 PFLOP/s where a library fp16 product reaches
+// 1.4 to 1.5: a step is X X^T (327 us, 136 tiles on 256 compute units, whose matrix units are busy 40% of the time),
+// A A (92, the same tiles and a quarter of the depth) and B X (554; busy 53% at the 1.77 GHz that
+// their power leaves; 440 of it the main loop, the rest its ends, which read and write 0.7 GB of X).  Small
+// ones are their launches: 256 x 1024, 17 launches, 98 us from a graph, 9 of them for the rest in B X.
+// The steps: tiles chosen for each product, instructions held in place between LDS reads (1003 x 517 x 4 161 ->
+// 149 us, 2048 x 2048 886 -> 380).
 #include <hip/hip_runtime.h>
 #include <algorithm>
 #include <math.h>
@@ -56,7 +58,7 @@ using linear::uniform_rsrc;
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kUnit = 64;             // fp16 values of K in a step
-constexpr float kScaleO = 1024.0f, kScaleB = 256.0f;
+constexpr float kScaleX = 16384.0f, kScaleO = 1024.0f, kScaleB = 256.0f;
 constexpr int kNormGroups = 1024;         // partial sums of squares per matrix, at most
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -73,30 +75,21 @@ __device__ __forceinline__ uint2 pack_h4(const float (&v)[4]) {
     return __builtin_bit_cast(uint2, (h4){static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]), static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])});
 }
 
-typedef float f2v __attribute__((ext_vector_type(2)));
 // Holds a matrix instruction to its place in the order of the code (blocks_mfma.h).  In the accumulation
 // registers: where a wave has more than 256, the compiler keeps sums there, and copies them both ways for
 // a place in the vector registers (2048 x 2048 in all: 886 us for 380).
 __device__ __forceinline__ void pin(f16v &v) { asm volatile("" : "+a"(v)::"memory"); }
-// What fp16 leaves of eight values, in e4m3 times `up`
-__device__ __forceinline__ uint2 pack_rest(const float (&v)[8], float up) {
-    float r[8];
+// What fp16 leaves of eight values, in fp16
+__device__ __forceinline__ u32x4 pack_rest(const float (&v)[8]) {
+    h8 h;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        r[e] = fminf(fmaxf((v[e] - static_cast<float>(static_cast<_Float16>(v[e]))) * up, -448.0f), 448.0f);
-    int a = 0, b = 0;
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], a, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], a, true);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], b, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], b, true);
-    return make_uint2(static_cast<uint32_t>(a), static_cast<uint32_t>(b));
+    for (int e = 0; e < 8; ++e) h[e] = static_cast<_Float16>(v[e] - static_cast<float>(static_cast<_Float16>(v[e])));
+    return __builtin_bit_cast(u32x4, h);
 }
-__device__ __forceinline__ void unpack(u32x4 hi, uint2 lo, float down, float (&v)[8]) {
-    const h8 h = __builtin_bit_cast(h8, hi);
-    const f2v r[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.x), false), __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.x), true),
-                      __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.y), false), __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo.y), true)};
+__device__ __forceinline__ void unpack(u32x4 hi, u32x4 lo, float (&v)[8]) {   // exact: 22 bits
+    const h8 h = __builtin_bit_cast(h8, hi), l = __builtin_bit_cast(h8, lo);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(r[e >> 1][e & 1], down, static_cast<float>(h[e]));
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(h[e]) + static_cast<float>(l[e]);
 }
 
 // eight values of a row from column c on, zeros from `cols` on
@@ -127,12 +120,12 @@ struct LoadArgs {
     int64_t rows, cols;               // of G
     double *part;                     // [batch][kNormGroups], the first `groups` used
     int groups;
-    uint16_t *hi, *xt;                // X [rp][ldx], X^T [cp][ldt]
-    unsigned char *lo;                // as X
+    uint16_t *hi, *lo, *xt;           // X and its rest [rp][ldx], X^T [cp][ldt]
     int64_t ldx, ldt, xb, tb;         // row and batch strides (elements)
     int rp, cp;                       // padded rows and columns of X
+    int rest_at;                      // X^T: where in a row the rest's starts, 0: not wanted
     int tall;                         // X is G^T
-    float s, up, eps;
+    float s, eps;
 };
 
 // Sums of squares in fp64, a fixed share of the rows' 2048-value pieces per workgroup: no square of a
@@ -209,8 +202,10 @@ __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
         }
         const int64_t x_at = z * a.xb + static_cast<int64_t>(r0 + line) * a.ldx + c0 + at;
         *reinterpret_cast<u32x4 *>(a.hi + x_at) = pack_h8(p);
-        *reinterpret_cast<uint2 *>(a.lo + x_at) = pack_rest(p, a.up);
-        *reinterpret_cast<u32x4 *>(a.xt + z * a.tb + static_cast<int64_t>(c0 + line) * a.ldt + r0 + at) = pack_h8(q);
+        *reinterpret_cast<u32x4 *>(a.lo + x_at) = pack_rest(p);
+        uint16_t *xt = a.xt + z * a.tb + static_cast<int64_t>(c0 + line) * a.ldt + r0 + at;
+        *reinterpret_cast<u32x4 *>(xt) = pack_h8(q);
+        if (a.rest_at) *reinterpret_cast<u32x4 *>(xt + a.rest_at) = pack_rest(q);
     }
 }
 
@@ -222,7 +217,7 @@ struct Args {
     const uint16_t *w, *x;            // K contiguous: features [rows_w][ldw], tokens [rows_x][ldx]
     int64_t ldw, ldx, wb, xb;         // row and batch strides (elements)
     int rows_w, rows_x;               // multiples of 64
-    int steps;                        // of K
+    int steps, steps_x;               // of K; of x's, which starts again at its end (APPLY, LAST)
     int tiles_f, per_batch, total;    // tiles: per row of them, of one matrix, of all
     int groups, per_xcd;              // workgroups; ceil(groups / 8)
     float *part;                      // groups != total: [2 groups][side][side] fp32
@@ -233,9 +228,8 @@ struct Args {
     int64_t ldo, ob;
     float *d, *e;                     // diagonals of A, and a + that of B: [batch][rows]
     float a, b, c;
-    uint16_t *hi, *xt;                // X and the next X^T
-    unsigned char *lo;
-    float up, down;                   // of lo
+    uint16_t *hi, *lo, *xt;           // X, its rest and the next X^T
+    int rest_at;                      // of X^T
     int64_t ldh, hb, ldt, tb;
     void *out;                        // LAST: bf16
     int64_t ldout, outb;
@@ -289,15 +283,15 @@ __device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, in
 // APPLY and LAST: the product's values v of eight features of a token to X' in all its forms, but for the
 // transposed one.  LAST leaves what the output's transpose holds in v.
 template <int EPI>
-__device__ __forceinline__ void apply_values(const Args &g, int z, int t, int f, u32x4 hi, uint2 lo, float et, float (&v)[8]) {
+__device__ __forceinline__ void apply_values(const Args &g, int z, int t, int f, u32x4 hi, u32x4 lo, float et, float (&v)[8]) {
     float was[8];
-    unpack(hi, lo, g.down, was);
+    unpack(hi, lo, was);
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] = fmaf(et, was[u], v[u] * (1.0f / kScaleB));
     if constexpr (EPI == APPLY) {
         const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
         *reinterpret_cast<u32x4 *>(g.hi + at) = pack_h8(v);
-        *reinterpret_cast<uint2 *>(g.lo + at) = pack_rest(v, g.up);
+        *reinterpret_cast<u32x4 *>(g.lo + at) = pack_rest(v);
     } else {
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] *= g.inv;
@@ -319,7 +313,9 @@ __device__ __forceinline__ void turned_values(const Args &g, int z, int64_t row,
     if constexpr (EPI == GRAM || EPI == POLY) {
         *reinterpret_cast<u32x4 *>((EPI == GRAM ? g.o : g.bo) + z * g.ob + row * g.ldo + t) = pack_h8(v);
     } else if constexpr (EPI == APPLY) {
-        *reinterpret_cast<u32x4 *>(g.xt + z * g.tb + row * g.ldt + t) = pack_h8(v);
+        uint16_t *o = g.xt + z * g.tb + row * g.ldt + t;
+        *reinterpret_cast<u32x4 *>(o) = pack_h8(v);
+        if (g.rest_at) *reinterpret_cast<u32x4 *>(o + g.rest_at) = pack_rest(v);
     } else if (row < g.cols) {
         uint16_t *o = static_cast<uint16_t *>(g.out) + z * g.outb + row * g.ldout + t;
         if (t + 8 <= g.r) {
@@ -363,7 +359,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wf = wave / S::WT, wt = wave % S::WT;
-    const uint32_t ldw = static_cast<uint32_t>(g.ldw * 2), ldx = static_cast<uint32_t>(g.ldx * 2), kbytes = g.steps * kStep;
+    const uint32_t ldw = static_cast<uint32_t>(g.ldw * 2), ldx = static_cast<uint32_t>(g.ldx * 2);
     constexpr int kMaxLoads = 8;
     static_assert(LA <= kMaxLoads && LB <= kMaxLoads, "load slots");
     uint32_t voffA[kMaxLoads], voffB[kMaxLoads];
@@ -393,10 +389,10 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
         fi = within / gt;
     }
     const int t0 = __builtin_amdgcn_readfirstlane(ti * S::BT), f0 = __builtin_amdgcn_readfirstlane(fi * S::BF);
-    const int kbeg = s0, nsteps = min(left, g.steps - s0);
+    const int kbeg = s0, nsteps = min(left, g.steps - s0), steps_x = SYM ? g.steps : g.steps_x;
     const int fr = min(S::BF, g.rows_w - f0), tr = min(S::BT, g.rows_x - t0);
-    const __amdgpu_buffer_rsrc_t rsA = uniform_rsrc(g.w + z * g.wb + f0 * g.ldw, (fr - 1) * ldw + kbytes);
-    const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(g.x + z * g.xb + t0 * g.ldx, (tr - 1) * ldx + kbytes);
+    const __amdgpu_buffer_rsrc_t rsA = uniform_rsrc(g.w + z * g.wb + f0 * g.ldw, (fr - 1) * ldw + g.steps * kStep);
+    const __amdgpu_buffer_rsrc_t rsB = uniform_rsrc(g.x + z * g.xb + t0 * g.ldx, (tr - 1) * ldx + steps_x * kStep);
     const int last = nsteps - 1;
     // request q of a step: w of step sw, then x of step sx
     auto request = [&](int sw, int sx, int slot_a, int slot_b, int q) {
@@ -406,7 +402,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
         else if (q < LA + LB)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsB, (lds_ptr)(lds + SA * S::A_BYTES + slot_b * S::B_BYTES + ((q - LA) * S::NW + wave) * 1024), 16,
-                voffB[q < LA ? 0 : q - LA], (kbeg + min(sx, last)) * kStep, 0, 0);
+                voffB[q < LA ? 0 : q - LA], (kbeg + min(sx, last) - (SYM || kbeg + min(sx, last) < steps_x ? 0 : steps_x)) * kStep, 0, 0);
     };
     auto frag = [&](const unsigned char *tile_at, int q, int kk) {   // 32-row tile q, instruction kk of the step
         const int r = q * 32 + (lane & 31);
@@ -502,7 +498,7 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
     // reads of X or O for them is asked for all at once
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();
-    constexpr int LPT = FI * 4, TPP = 64 / LPT, PASSES = 32 / TPP;
+    constexpr int LPT = FI * 4, TPP = 64 / LPT, PASSES = 32 / TPP, AT_ONCE = PASSES < 4 ? PASSES : 4;
     float *reg = reinterpret_cast<float *>(lds) + wave * 32 * S::OUT_LD;
     const int lf = (lane % LPT) * 8;
     const int f = f0 + wf * FI * 32 + lf;
@@ -527,48 +523,51 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
                 *reinterpret_cast<float4 *>(reg + (lane & 31) * S::OUT_LD + i * 32 + (r >> 2) * 8 + half * 4) =
                     make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
         asm volatile("" ::: "memory");   // the accumulators' registers are free for what follows
-        u32x4 hi[PASSES];   // of X, or O
-        uint2 lo[PASSES];
-        float et[PASSES];   // the diagonal at the token
-        if (there && EPI != GRAM && !piece) {
+        // four passes' operands at once: eight took registers that went to memory (B X of 4096 x 16384 643 -> 554 us)
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int t = tj + p * TPP + lane / LPT;
-                if constexpr (EPI == POLY) {
-                    hi[p] = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
-                } else {
-                    const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
-                    hi[p] = *reinterpret_cast<const u32x4 *>(g.hi + at);
-                    lo[p] = *reinterpret_cast<const uint2 *>(g.lo + at);
-                }
-                et[p] = (EPI == POLY ? g.d : g.e)[static_cast<int64_t>(z) * g.rows_x + t];
-            }
-        }
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (there) {
+        for (int p0 = 0; p0 < PASSES; p0 += AT_ONCE) {
+            u32x4 hi[AT_ONCE], lo[AT_ONCE];   // of X, or O
+            float et[AT_ONCE];                // the diagonal at the token
+            if (there && EPI != GRAM && !piece) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int tl = p * TPP + lane / LPT, t = tj + tl;
-                float *at = reg + tl * S::OUT_LD + lf;
-                const float4 x = reinterpret_cast<const float4 *>(at)[0], y = reinterpret_cast<const float4 *>(at)[1];
-                float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                if constexpr (SYM) {
-                    if (piece) {
-                        float4 *o = reinterpret_cast<float4 *>(
-                            g.part + ((2ll * w + (kbeg == 0 ? 1 : 0)) * S::BT + (t - t0)) * S::BF + (f - f0));
-                        o[0] = x;
-                        o[1] = y;
-                        continue;
+                for (int p = 0; p < AT_ONCE; ++p) {
+                    const int t = tj + (p0 + p) * TPP + lane / LPT;
+                    if constexpr (EPI == POLY) {
+                        hi[p] = *reinterpret_cast<const u32x4 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f);
+                    } else {
+                        const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
+                        hi[p] = *reinterpret_cast<const u32x4 *>(g.hi + at);
+                        lo[p] = *reinterpret_cast<const u32x4 *>(g.lo + at);
                     }
-                    symmetric_values<EPI>(g, z, t, f, hi[p], et[p], df, v);
-                    symmetric_store<EPI>(g, z, t, f, v);
-                } else {
-                    apply_values<EPI>(g, z, t, f, hi[p], lo[p], et[p], v);
+                    et[p] = (EPI == POLY ? g.d : g.e)[static_cast<int64_t>(z) * g.rows_x + t];
                 }
-                if (turned) {
-                    reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            __builtin_amdgcn_wave_barrier();
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (there) {
+#pragma unroll
+                for (int p = 0; p < AT_ONCE; ++p) {
+                    const int tl = (p0 + p) * TPP + lane / LPT, t = tj + tl;
+                    float *at = reg + tl * S::OUT_LD + lf;
+                    const float4 x = reinterpret_cast<const float4 *>(at)[0], y = reinterpret_cast<const float4 *>(at)[1];
+                    float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    if constexpr (SYM) {
+                        if (piece) {
+                            float4 *o = reinterpret_cast<float4 *>(
+                                g.part + ((2ll * w + (kbeg == 0 ? 1 : 0)) * S::BT + (t - t0)) * S::BF + (f - f0));
+                            o[0] = x;
+                            o[1] = y;
+                            continue;
+                        }
+                        symmetric_values<EPI>(g, z, t, f, hi[p], et[p], df, v);
+                        symmetric_store<EPI>(g, z, t, f, v);
+                    } else {
+                        apply_values<EPI>(g, z, t, f, hi[p], lo[p], et[p], v);
+                    }
+                    if (turned) {
+                        reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
                 }
             }
         }
@@ -625,7 +624,7 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
     // the finishing threads' operands: 128 threads, eight features of a token each
     const int t = t0 + (th >> 2), f = f0 + (th & 3) * 8;
     u32x4 hi = {0u, 0u, 0u, 0u};
-    uint2 lo = make_uint2(0u, 0u);
+    u32x4 lo = {0u, 0u, 0u, 0u};
     float et = 0.0f, df[8] = {};
     if (th < 128) {
         const int64_t row = static_cast<int64_t>(z) * g.rows_x;
@@ -637,13 +636,13 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
         } else {
             const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
             hi = *reinterpret_cast<const u32x4 *>(g.hi + at);
-            lo = *reinterpret_cast<const uint2 *>(g.lo + at);
+            lo = *reinterpret_cast<const u32x4 *>(g.lo + at);
             et = g.e[row + t];
         }
     }
     const uint16_t *wrow = g.w + z * g.wb + static_cast<int64_t>(f0 + (lane & 31)) * g.ldw + half * 8;
     const uint16_t *xrow = g.x + z * g.xb + static_cast<int64_t>(t0 + (lane & 31)) * g.ldx + half * 8;
-    const int total = g.steps * 4;   // of 16 values of K
+    const int total = g.steps * 4, total_x = SYM ? total : g.steps_x * 4;   // of 16 values of K
     const int beg = static_cast<int>(static_cast<int64_t>(total) * wave / kFineWaves);
     const int end = static_cast<int>(static_cast<int64_t>(total) * (wave + 1) / kFineWaves);
     auto fetch = [&](int s, h8 (&a)[U], h8 (&b)[U]) {
@@ -651,7 +650,7 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
         for (int u = 0; u < U; ++u) {
             if (s + u < end) {
                 a[u] = *reinterpret_cast<const h8 *>(wrow + (s + u) * 16);
-                b[u] = *reinterpret_cast<const h8 *>(xrow + (s + u) * 16);
+                b[u] = *reinterpret_cast<const h8 *>(xrow + (SYM || s + u < total_x ? s + u : s + u - total_x) * 16);
             }
         }
     };
@@ -723,19 +722,20 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
     const int wave = __builtin_amdgcn_readfirstlane(th >> 6);
     const int t0 = ti * 32, f0 = (mn - ti * g.tiles_f) * kShortCols + wave * 32;
     const bool there = f0 < g.rows_w;   // of this wave's columns: all or none
-    h8 a[U];
-    u32x4 hi[2];
-    uint2 lo[2];
+    h8 a[U], rest[U];
+    u32x4 hi[2], lo[2];
     if (there) {
         const uint16_t *row = g.w + z * g.wb + static_cast<int64_t>(f0 + l32) * g.ldw + half * 8;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
             a[u] = *reinterpret_cast<const h8 *>(row + u * 16);
+            rest[u] = *reinterpret_cast<const h8 *>(row + g.rest_at + u * 16);
+        }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int64_t at = z * g.hb + static_cast<int64_t>(t0 + p * 16 + (lane >> 2)) * g.ldh + f0 + (lane & 3) * 8;
             hi[p] = *reinterpret_cast<const u32x4 *>(g.hi + at);
-            lo[p] = *reinterpret_cast<const uint2 *>(g.lo + at);
+            lo[p] = *reinterpret_cast<const u32x4 *>(g.lo + at);
         }
     }
     if (wave * 32 < kShortRows) {   // columns 32 wave .. of B's rows t0 ..
@@ -790,6 +790,7 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
     for (int u = 0; u < U; ++u) {
         const h8 b = *reinterpret_cast<const h8 *>(b_rows + l32 * LDB + u * 16 + half * 8);
         acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[u], b, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(rest[u], b, acc, 0, 0, 0);
     }
     float *reg = sums[wave];   // this wave's alone
 #pragma unroll
@@ -895,28 +896,29 @@ size_t piece_bytes(const Plan &p) {
 }
 
 struct Layout {
-    int64_t r, c, rp, cp, ldx, ldr;   // ldx: of X; ldr: of X^T, O, B
+    int64_t r, c, rp, cp, ldx, ldt, ldr;   // ldx: of X; ldt: of X^T; ldr: of O, B
     Plan gram, poly, apply;
     size_t off_hi, off_lo, off_t0, off_t1, off_o, off_b, off_d, off_e, off_norm, off_part, bytes;
 };
 // Rows that lie a multiple of 4 KB apart meet in few of the caches' sets (8% of a product): 128 bytes more.
 int64_t apart(int64_t padded) { return padded * 2 % 4096 == 0 ? padded + kUnit : padded; }
-Layout layout(int64_t batch, int64_t rows, int64_t cols) {
+Layout layout(int64_t batch, int64_t rows, int64_t cols, bool rest) {
     Layout L;
     L.r = std::min(rows, cols);
     L.c = std::max(rows, cols);
     L.rp = round_up(L.r, kUnit);
     L.cp = round_up(L.c, kUnit);
     L.ldx = apart(L.cp);
+    L.ldt = apart(rest ? 2 * L.rp : L.rp);
     L.ldr = apart(L.rp);
     L.gram = plan_of(batch, L.rp, L.rp, L.cp / kUnit, true, true);
     L.poly = plan_of(batch, L.rp, L.rp, L.rp / kUnit, true, false);
-    L.apply = plan_of(batch, L.rp, L.cp, L.rp / kUnit, false, false);
-    const size_t x = align256(static_cast<size_t>(batch) * L.rp * L.ldx * 2), t = align256(static_cast<size_t>(batch) * L.cp * L.ldr * 2);
+    L.apply = plan_of(batch, L.rp, L.cp, (rest ? 2 : 1) * L.rp / kUnit, false, false);
+    const size_t x = align256(static_cast<size_t>(batch) * L.rp * L.ldx * 2), t = align256(static_cast<size_t>(batch) * L.cp * L.ldt * 2);
     const size_t s = align256(static_cast<size_t>(batch) * L.rp * L.ldr * 2), v = align256(static_cast<size_t>(batch) * L.rp * 4);
     size_t o = 0;
     L.off_hi = o;    o += x;
-    L.off_lo = o;    o += x / 2;
+    L.off_lo = o;    o += x;
     L.off_t0 = o;    o += t;
     L.off_t1 = o;    o += t;
     L.off_o = o;     o += s;
@@ -965,16 +967,17 @@ hipError_t launch_product(Args g, const Plan &p, hipStream_t st) {
 }  // namespace
 
 size_t orthogonalise_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
-    return batch > 0 ? layout(batch, rows, cols).bytes : 0;
+    return batch > 0 ? layout(batch, rows, cols, true).bytes : 0;   // whatever the steps and coefficients
 }
 
 hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     if (a.batch <= 0) return hipSuccess;
-    const Layout L = layout(a.batch, a.rows, a.cols);
+    const bool rest = takes_rest(std::min(a.rows, a.cols), a.steps, a.a);
+    const Layout L = layout(a.batch, a.rows, a.cols, rest);
     char *ws = static_cast<char *>(a.workspace);
     auto half = [&](size_t off) { return reinterpret_cast<uint16_t *>(ws + off); };
     const int tall = a.rows > a.cols;
-    const float s = ldexpf(1.0f, static_cast<int>(lrint(0.5 * log2(static_cast<double>(L.c)))));
+    const float s = kScaleX;
 
     LoadArgs l{};
     l.g = a.g;
@@ -984,17 +987,17 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     l.cols = a.cols;
     l.part = reinterpret_cast<double *>(ws + L.off_norm);
     l.hi = half(L.off_hi);
-    l.lo = reinterpret_cast<unsigned char *>(ws + L.off_lo);
+    l.lo = half(L.off_lo);
     l.xt = half(L.off_t0);
     l.ldx = L.ldx;
-    l.ldt = L.ldr;
+    l.ldt = L.ldt;
     l.xb = L.rp * L.ldx;
-    l.tb = L.cp * L.ldr;
+    l.tb = L.cp * L.ldt;
+    l.rest_at = rest ? static_cast<int>(L.rp) : 0;
     l.rp = static_cast<int>(L.rp);
     l.cp = static_cast<int>(L.cp);
     l.tall = tall;
     l.s = s;
-    l.up = ldexpf(1.0f, 19) / s;   // |X| up to 1.3: the rest, half a step of fp16, stays below 448
     l.eps = a.eps;
     // a workgroup a piece of 2048 values, up to 1024 of them a matrix and about as many for a batch
     const int64_t pieces = a.rows * ceil_div(a.cols, 2048);
@@ -1023,11 +1026,10 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     g.c = a.c;
     g.hi = l.hi;
     g.lo = l.lo;
-    g.up = l.up;
-    g.down = 1.0f / l.up;
+    g.rest_at = l.rest_at;
     g.ldh = L.ldx;
     g.hb = l.xb;
-    g.ldt = L.ldr;
+    g.ldt = L.ldt;
     g.tb = l.tb;
     g.out = a.out;
     g.ldout = a.ldo;
@@ -1045,7 +1047,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         if ((e = launch_product<GRAM>(g, L.gram, st)) != hipSuccess) return e;
         if (L.rp <= kShortRows) {
             g.w = half(k & 1 ? L.off_t1 : L.off_t0);
-            g.ldw = L.ldr;
+            g.ldw = L.ldt;
             g.wb = l.tb;
             g.xt = half(k & 1 ? L.off_t0 : L.off_t1);
             g.rows_w = static_cast<int>(L.cp);
@@ -1068,8 +1070,11 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         g.x = g.bo;
         g.w = half(k & 1 ? L.off_t1 : L.off_t0);
         g.xt = half(k & 1 ? L.off_t0 : L.off_t1);
+        g.ldw = L.ldt;
         g.wb = l.tb;
         g.rows_w = static_cast<int>(L.cp);
+        g.steps_x = g.steps;
+        if (rest) g.steps *= 2;
         g.inv = 1.0f / s;
         e = k + 1 < a.steps ? launch_product<APPLY>(g, L.apply, st) : launch_product<LAST>(g, L.apply, st);
         if (e != hipSuccess) return e;
