@@ -2,7 +2,10 @@
 test can make coarser to see whether it would notice."""
 from __future__ import annotations
 
+import ctypes
 import math
+import os
+import subprocess
 
 import torch
 
@@ -47,6 +50,16 @@ def scales(steps, abc):
         return 2.0 ** (most if v == 0 else min(most, math.floor(15 - math.log2(v))))
 
     return power(x, 14), power(o, 10), power(p, 8)
+
+
+def values(steps, abc):
+    """The largest |X|, |A| and |B| before each step, of singular values from 0 to 1 in exact arithmetic."""
+    a, b, c = abc
+    s = torch.linspace(0, 1, 100001, dtype=torch.float64)
+    for _ in range(steps):
+        t = s * s
+        yield float(s.abs().max()), float(t.max()), float((t * (b + c * t)).abs().max())
+        s = s * (a + t * (b + c * t))
 
 
 def takes_rest(r, steps, abc):
@@ -122,3 +135,34 @@ def share_of(got, G, steps, mutation):
     d = rounded(G, steps, mutation=mutation) - like
     size = float((d * d).sum())
     return float(((got - like) * d).sum()) / size if size else None
+
+
+HEADER = """#include "ortho_plan.h"
+extern "C" int scales(long r, int steps, float a, float b, float c, float *out) {
+    const auto s = lce::ortho_plan::powers_of(r, steps, a, b, c);
+    out[0] = s.x;
+    out[1] = s.o;
+    out[2] = s.b;
+    return s.fit * 2 + s.rest;
+}
+"""
+
+
+def load(directory: str):
+    """(rows, steps, coefficients) -> (x, o, b, B X takes the rest), or None where they are refused: the kernel's own
+    choice, csrc/ortho_plan.h, compiled into ``directory``."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, so = os.path.join(directory, "scales.cpp"), os.path.join(directory, "scales.so")
+    with open(src, "w") as f:
+        f.write(HEADER)
+    csrc = os.path.join(root, "vocabulary_cross_entropy_row_amd", "csrc")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", f"-I{csrc}", src, "-o", so], check=True)
+    lib = ctypes.CDLL(so)
+    lib.scales.argtypes = [ctypes.c_long, ctypes.c_int] + [ctypes.c_float] * 3 + [ctypes.c_void_p]
+
+    def of(r, steps, abc):
+        out = (ctypes.c_float * 3)()
+        v = lib.scales(r, steps, *abc, ctypes.addressof(out))
+        return (*out, bool(v & 1)) if v & 2 else None
+
+    return of

@@ -1,7 +1,8 @@
 """What the orthogonalised update keeps beyond fp16, on the GPU.
 
 Gradients of few directions show it.  The other singular values are 0 and stay 0 by the definition; whatever the
-roundings put there grows by 3.4445 a step, 485 times in five steps and 19800 times in eight.
+roundings put there grows by 3.4445 a step, 485 times in five steps and 19800 times in eight.  Coefficients under which
+values grow show that no step leaves fp16's range.
 
 Tolerances.  ``ortho_model.rounded`` has the kernel's roundings (fp32 sums among them, in another order than the
 kernel's) and is off from the definition by some dev; the kernel's deviation is of the same size and held to three
@@ -50,3 +51,34 @@ def test_every_rounding_is_as_fine_as_stated(case, mutation):
     if share is None:
         pytest.skip("the product does not take the rest at this size")
     assert abs(share) < 0.5, f"{share:.2f} of what {mutation!r} would change"
+
+
+# (gradient, steps, coefficients), and the most that singular values make of X, A and B before the last step: 12, 144, 0;
+# 16, 256, 0; 16, 256, 3.6e3; 150, 2.3e4, 0; 1, 1, 2e6; 6, 36, 1.4e3 (twice); 238, 5.7e4, 0; 238, 5.7e4, 2.2e6
+GROWTH = [("ones 2 3", 2, (12.0, 0.0, 0.0)), ("ones 2 2", 3, (4.0, 0.0, 0.0)), ("ones 100 70", 2, (2.0, 14.0, 0.0)),
+          ("directions 200 300", 5, (3.5, 0.0, 0.0)), ("directions 70 90", 1, (1e6, 1e6, 1e6)), ("directions 70 90", 2, (3.0, 2.0, 1.0)),
+          ("noise 70 90", 2, (3.0, 2.0, 1.0)), ("noise 300 90", 4, (6.2, 0.0, 0.0)), ("diagonal 130 200", 2, (200.0, 38.0, 0.0))]
+
+
+def growing(kind):
+    name, r, c = kind.split()
+    r, c = int(r), int(c)
+    if name == "ones":
+        return torch.ones(r, c, device=DEV)
+    if name == "diagonal":   # one entry far above the others
+        G = 1e-3 * torch.eye(r, c, device=DEV)
+        G[3, 5] = 1.0
+        return G
+    return model.matrix(r, c, 9, 2 if name == "directions" else 0, device=DEV)
+
+
+@pytest.mark.parametrize("kind,steps,abc", GROWTH)
+def test_values_that_grow(kind, steps, abc):
+    """Each value off by half a step of bf16 and three times the largest of the model's deviations; by 2^-20 of it
+    besides, for a value next to the middle of a step that fp32's roundings move (two of each step's, 2^-24 each)."""
+    G = growing(kind)
+    got = lce.lce_orthogonalise(G, steps=steps, coefficients=abc).double()
+    want, like = model.defined(G, steps, abc), model.rounded(G, steps, abc)
+    limit = want.abs() * (2.0 ** -8 + 2.0 ** -20) + 3 * (like - want).abs().max()
+    off = (got - want).abs()
+    assert bool((off <= limit).all()), f"worst {float(off.max()):.3g} of {float(want.abs().max()):.3g}, limit {float(limit.max()):.3g}"

@@ -14,6 +14,7 @@
 #include "blocks_internal.h"
 #include "head_internal.h"
 #include "lce_internal.h"
+#include "ortho_plan.h"
 
 // The workspace of lce_ce_fwd_bwd_noalloc: room for the row kernel's workspace
 // at any n (its per-workgroup part stops growing at kMaxRowGroups workgroups),
@@ -1253,6 +1254,9 @@ lce_status lce_orthogonalise(const void *g, int64_t ldg, int64_t g_batch_stride,
         return fail(LCE_ERR_INVALID_ARG, "%s: the coefficients must be finite (got %g, %g, %g)", fn, (double)a, (double)b, (double)c);
     if (!(eps >= 0.0f) || isinf(eps))
         return fail(LCE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0 (got %g)", fn, (double)eps);
+    if (!lce::ortho_plan::powers_of(1, steps, a, b, c).fit)
+        return fail(LCE_ERR_UNSUPPORTED, "%s: the coefficients (%g, %g, %g) can take singular values past 256 before the last of %d steps",
+                    fn, (double)a, (double)b, (double)c, steps);
     if (batch == 0) return ok();
     if ((st = check_matrix(fn, "g", g, ldg, cols, dtype, true)) != LCE_OK ||
         (st = check_matrix(fn, "out", out, ldo, cols, LCE_BF16, true)) != LCE_OK)

@@ -61,7 +61,43 @@ inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps
     return best;
 }
 
-// Whether B X takes what fp16 leaves of X too, with rows and |a| of the update.
+// ---- what fp16 holds X and the off-diagonal parts of A and B times -------------------------------
+//
+// X = G / ||G|| has singular values up to 1, and p(s) = a s + b s^3 + c s^5 of them after a step.  With m the most
+// that they can be, |X| <= m, |A| <= m^2 and |B| <= the largest |b t + c t^2| up to t = m^2, and so is every
+// value of theirs: powers of two that leave these below 2^15 never overflow fp16.
+
+// the largest |p(s)| for s from 0 to m: at m, or where p' is 0
+inline double peak(double a, double b, double c, double m) {
+    auto p = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + c * t))); };
+    double top = p(m * m);
+    auto at = [&](double t) {
+        if (t > 0.0 && t < m * m) top = std::max(top, p(t));   // false of NaN
+    };
+    const double d = 9.0 * b * b - 20.0 * a * c;   // of a + 3 b t + 5 c t^2
+    if (d >= 0.0) {
+        const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));
+        at(q / (5.0 * c));
+        at(a / q);
+    }
+    return top;
+}
+// the largest |b t + c t^2| for t from 0 to u
+inline double peak_b(double b, double c, double u) {
+    double top = std::fabs(u * (b + c * u));
+    const double t = -b / (2.0 * c);
+    if (t > 0.0 && t < u) top = std::max(top, std::fabs(t * (b + c * t)));
+    return top;
+}
+// Past a value of 256 the powers would leave small values of A few bits; terms past 2^100 leave fp32.
+constexpr double kMaxValue = 256.0, kMaxTerm = 0x1p100;   // of X before a step; of a, b m^2 and c m^4
+
+struct Powers {
+    bool fit;          // nothing passes kMaxValue or kMaxTerm; the others mean nothing if not
+    float x, o, b;
+    bool rest;         // whether B X takes what fp16 leaves of X too
+};
+// The powers are at most 2^14, 2^10 and 2^8, which the default coefficients (m = 1.21) have.
 //
 // a X + B X is (a + B) X, whose rows stay in the space of X's, if both terms have the same X.  With fp16's X in
 // the product alone, what fp16 leaves makes directions that X did not have, of the second order in fp16's
@@ -70,8 +106,24 @@ inline Plan plan_of(int64_t batch, int64_t rows_x, int64_t rows_w, int64_t steps
 // 8.6e-4; eight: 1.4e-1, 2.2e-2).  Where that could reach half of the bf16 output's rounding, 1.7e-3, the product takes
 // both (6.0e-4; eight: 2.1e-3, 2.7e-3, where products in fp32 give 1.7e-3, 2.6e-3), for twice its instructions.
 // Up to 64 rows they cost nothing.
-inline bool takes_rest(int64_t r, int steps, double a) {
-    return r <= 64 || steps * std::log(std::fabs(a)) > std::log(static_cast<double>(r));
+inline Powers powers_of(int64_t r, int steps, double a, double b, double c) {
+    double m = 1.0, x = 0.0, o = 0.0, p = 0.0;
+    Powers s{true, 0, 0, 0, r <= 64};
+    for (int k = 0; k < steps && s.fit; ++k) {
+        x = std::max(x, m);
+        o = std::max(o, m * m);
+        p = std::max(p, peak_b(b, c, m * m));
+        s.fit = m <= kMaxValue && std::fabs(a) <= kMaxTerm && std::fabs(b) * m * m <= kMaxTerm && std::fabs(c) * m * m * m * m <= kMaxTerm;
+        m = peak(a, b, c, m) * (1.0 + 0x1p-8);   // and what the roundings add
+    }
+    auto power = [](double v, int most) {
+        return std::ldexp(1.0f, v > 0.0 ? static_cast<int>(std::min<double>(most, std::floor(15.0 - std::log2(v)))) : most);
+    };
+    s.x = power(x, 14);
+    s.o = power(o, 10);
+    s.b = power(p, 8);
+    s.rest = s.rest || steps * std::log(std::fabs(a)) > std::log(static_cast<double>(r));
+    return s;
 }
 
 }  // namespace ortho_plan

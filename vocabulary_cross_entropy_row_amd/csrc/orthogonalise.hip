@@ -13,7 +13,8 @@
 // With these roundings put into the definition (gaussian matrices with even and uneven rows, of 1 to 16
 // directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.0e-3 of the result in the
 // Frobenius norm and 1.9e-3 in the 2-norm from 64 rows on, and by up to 5e-3 and 6e-3 below; the bf16 output rounds at 1.7e-3.
-// Powers of two keep fp16 in range: X is held times 2^14 (its values are at most 1.21), O times 2^10, B times 2^8.
+// Powers of two keep fp16 in range, for the default coefficients X times 2^14 (its values are at most 1.21), O times
+// 2^10 and B times 2^8 (ortho_plan.h).
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed, and stored a second time
 // transposed.  All operands have K contiguous: X for A, O for O O, and for B X also X^T, which the
@@ -58,7 +59,6 @@ using linear::uniform_rsrc;
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kUnit = 64;             // fp16 values of K in a step
-constexpr float kScaleX = 16384.0f, kScaleO = 1024.0f, kScaleB = 256.0f;
 constexpr int kNormGroups = 1024;         // partial sums of squares per matrix, at most
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -223,6 +223,7 @@ struct Args {
     float *part;                      // groups != total: [2 groups][side][side] fp32
     // epilogue
     float inv, inv_poly;              // of the products' scale; apply_short_kernel: of O O's
+    float so, sb, inv_o, inv_b;       // what O and B are held times, and their inverses
     uint16_t *o;                      // O [rows][ldo]: written by GRAM, read by POLY
     uint16_t *bo;                     // B's off-diagonal part
     int64_t ldo, ob;
@@ -255,7 +256,7 @@ __device__ __forceinline__ void gram_values(const Args &g, int z, int t, int f, 
             g.d[static_cast<int64_t>(z) * g.rows_x + t] = v[u];
             v[u] = 0.0f;
         }
-        v[u] *= kScaleO;
+        v[u] *= g.so;
     }
 }
 // The same, or (POLY) values of O O to B, from O there, the diagonal at t and at f .. f + 7
@@ -267,14 +268,14 @@ __device__ __forceinline__ void symmetric_values(const Args &g, int z, int t, in
         const h8 o = __builtin_bit_cast(h8, oq);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float ov = static_cast<float>(o[u]) * (1.0f / kScaleO);
+            const float ov = static_cast<float>(o[u]) * g.inv_o;
             float square = fmaf(dt + df[u], ov, v[u] * g.inv);
             if (t == f + u) {
                 square = fmaf(dt, dt, square);   // O is 0 there
                 g.e[static_cast<int64_t>(z) * g.rows_x + t] = g.a + fmaf(g.c, square, g.b * dt);
                 v[u] = 0.0f;
             } else {
-                v[u] = fmaf(g.c, square, g.b * ov) * kScaleB;
+                v[u] = fmaf(g.c, square, g.b * ov) * g.sb;
             }
         }
     }
@@ -287,7 +288,7 @@ __device__ __forceinline__ void apply_values(const Args &g, int z, int t, int f,
     float was[8];
     unpack(hi, lo, was);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = fmaf(et, was[u], v[u] * (1.0f / kScaleB));
+    for (int u = 0; u < 8; ++u) v[u] = fmaf(et, was[u], v[u] * g.inv_b);
     if constexpr (EPI == APPLY) {
         const int64_t at = z * g.hb + static_cast<int64_t>(t) * g.ldh + f;
         *reinterpret_cast<u32x4 *>(g.hi + at) = pack_h8(v);
@@ -770,9 +771,9 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
             h4 b;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {   // symmetric_values<POLY>
-                const float ov = static_cast<float>(o4[u]) * (1.0f / kScaleO);
+                const float ov = static_cast<float>(o4[u]) * g.inv_o;
                 float square = fmaf(dt + dc[u], ov, sum[r * 4 + u] * g.inv_poly);
-                float v = fmaf(g.c, square, g.b * ov) * kScaleB;
+                float v = fmaf(g.c, square, g.b * ov) * g.sb;
                 if (t == c + u) {
                     square = fmaf(dt, dt, square);
                     diagonal[l32] = g.a + fmaf(g.c, square, g.b * dt);
@@ -972,12 +973,13 @@ size_t orthogonalise_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) 
 
 hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     if (a.batch <= 0) return hipSuccess;
-    const bool rest = takes_rest(std::min(a.rows, a.cols), a.steps, a.a);
-    const Layout L = layout(a.batch, a.rows, a.cols, rest);
+    const Powers sc = powers_of(std::min(a.rows, a.cols), a.steps, a.a, a.b, a.c);
+    if (!sc.fit) return hipErrorInvalidValue;
+    const Layout L = layout(a.batch, a.rows, a.cols, sc.rest);
     char *ws = static_cast<char *>(a.workspace);
     auto half = [&](size_t off) { return reinterpret_cast<uint16_t *>(ws + off); };
     const int tall = a.rows > a.cols;
-    const float s = kScaleX;
+    const float s = sc.x;
 
     LoadArgs l{};
     l.g = a.g;
@@ -993,7 +995,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     l.ldt = L.ldt;
     l.xb = L.rp * L.ldx;
     l.tb = L.cp * L.ldt;
-    l.rest_at = rest ? static_cast<int>(L.rp) : 0;
+    l.rest_at = sc.rest ? static_cast<int>(L.rp) : 0;
     l.rp = static_cast<int>(L.rp);
     l.cp = static_cast<int>(L.cp);
     l.tall = tall;
@@ -1027,6 +1029,10 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
     g.hi = l.hi;
     g.lo = l.lo;
     g.rest_at = l.rest_at;
+    g.so = sc.o;
+    g.sb = sc.b;
+    g.inv_o = 1.0f / sc.o;
+    g.inv_b = 1.0f / sc.b;
     g.ldh = L.ldx;
     g.hb = l.xb;
     g.ldt = L.ldt;
@@ -1052,7 +1058,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
             g.xt = half(k & 1 ? L.off_t0 : L.off_t1);
             g.rows_w = static_cast<int>(L.cp);
             g.inv = 1.0f / s;
-            g.inv_poly = 1.0f / (kScaleO * kScaleO);
+            g.inv_poly = g.inv_o * g.inv_o;
             g.tiles_f = static_cast<int>(ceil_div(L.cp, kShortCols));
             g.per_batch = static_cast<int>(L.rp / 32) * g.tiles_f;
             const dim3 grid(static_cast<unsigned>(g.per_batch * a.batch));
@@ -1065,7 +1071,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         g.ldw = g.ldx = L.ldr;
         g.wb = g.xb = g.ob;
         g.steps = static_cast<int>(L.rp / kUnit);
-        g.inv = 1.0f / (kScaleO * kScaleO);
+        g.inv = g.inv_o * g.inv_o;
         if ((e = launch_product<POLY>(g, L.poly, st)) != hipSuccess) return e;
         g.x = g.bo;
         g.w = half(k & 1 ? L.off_t1 : L.off_t0);
@@ -1074,7 +1080,7 @@ hipError_t launch_orthogonalise(const OrthoArgs &a, hipStream_t st) {
         g.wb = l.tb;
         g.rows_w = static_cast<int>(L.cp);
         g.steps_x = g.steps;
-        if (rest) g.steps *= 2;
+        if (sc.rest) g.steps *= 2;
         g.inv = 1.0f / s;
         e = k + 1 < a.steps ? launch_product<APPLY>(g, L.apply, st) : launch_product<LAST>(g, L.apply, st);
         if (e != hipSuccess) return e;

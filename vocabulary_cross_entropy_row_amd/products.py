@@ -393,7 +393,8 @@ def lce_orthogonalise(g, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.031
     """The orthogonalised update of a matrix ``g`` [rows, cols], or of each of a batch [batch, rows, cols]
     (bfloat16 or float32, unit column stride): X = g / (its norm + eps), then ``steps`` times
     X <- a X + (b A + c A A) X with A = X X^T (X^T X of a matrix taller than wide) and ``coefficients``
-    (a, b, c).  Returns bfloat16 of g's shape, ``out`` if it is given."""
+    (a, b, c), refused where they can take singular values of 0 to 1 past 256 before the last step.
+    Returns bfloat16 of g's shape, ``out`` if it is given."""
     dev = _on_gpu(g, "g")
     if g.dim() not in (2, 3):
         raise ValueError(f"g must be [rows, cols] or [batch, rows, cols] (got {list(g.shape)})")
