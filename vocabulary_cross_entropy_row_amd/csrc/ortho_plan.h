@@ -105,7 +105,7 @@ struct Powers {
 // one direction, as the definition with the kernel's roundings shows (five default steps: 64 x 64 5.4e-3, 512 x 1024
 // 8.6e-4; eight: 1.4e-1, 2.2e-2).  Where that could reach half of the bf16 output's rounding, 1.7e-3, the product takes
 // both (6.0e-4; eight: 2.1e-3, 2.7e-3, where products in fp32 give 1.7e-3, 2.6e-3), for twice its instructions.
-// Up to 64 rows they cost nothing.
+// Up to 64 rows always: the kernel for them has one form.
 inline Powers powers_of(int64_t r, int steps, double a, double b, double c) {
     double m = 1.0, x = 0.0, o = 0.0, p = 0.0;
     Powers s{true, 0, 0, 0, r <= 64};

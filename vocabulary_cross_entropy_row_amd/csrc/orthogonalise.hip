@@ -11,7 +11,7 @@
 //   A, B   their diagonals in fp32 vectors, the rest in fp16.  X approaches orthogonal rows, so A
 //          approaches its diagonal: A = D + O gives A A = O O + (D_t + D_f) O + D^2, and B X = diag X + rest.
 // With these roundings put into the definition (gaussian matrices with even and uneven rows, of 1 to 16
-// directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.0e-3 of the result in the
+// directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.4e-3 of the result in the
 // Frobenius norm and 1.9e-3 in the 2-norm from 64 rows on, and by up to 5e-3 and 6e-3 below; the bf16 output rounds at 1.7e-3.
 // Powers of two keep fp16 in range, for the default coefficients X times 2^14 (its values are at most 1.21), O times
 // 2^10 and B times 2^8 (ortho_plan.h).
