@@ -145,12 +145,15 @@ extern "C" int scales(long r, int steps, float a, float b, float c, float *out) 
     out[2] = s.b;
     return s.fit * 2 + s.rest;
 }
+extern "C" int shape(long batch, long rows_x, long rows_w, long steps) {
+    return lce::ortho_plan::plan_of(batch, rows_x, rows_w, steps, false, false).shape;
+}
 """
 
 
 def load(directory: str):
-    """(rows, steps, coefficients) -> (x, o, b, B X takes the rest), or None where they are refused: the kernel's own
-    choice, csrc/ortho_plan.h, compiled into ``directory``."""
+    """(rows, steps, coefficients) -> (x, o, b, B X takes the rest), or None where they are refused, and (batch, rows,
+    columns, rest) -> which tiles B X takes: the kernel's own choice, csrc/ortho_plan.h, compiled into ``directory``."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     src, so = os.path.join(directory, "scales.cpp"), os.path.join(directory, "scales.so")
     with open(src, "w") as f:
@@ -165,4 +168,10 @@ def load(directory: str):
         v = lib.scales(r, steps, *abc, ctypes.addressof(out))
         return (*out, bool(v & 1)) if v & 2 else None
 
-    return of
+    lib.shape.argtypes = [ctypes.c_long] * 4
+
+    def shape(batch, rows, cols, rest):
+        rp, cp = (-(-v // 64) * 64 for v in (min(rows, cols), max(rows, cols)))
+        return lib.shape(batch, rp, cp, rp // 64 * (2 if rest else 1))
+
+    return of, shape

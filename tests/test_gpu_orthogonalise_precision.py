@@ -21,6 +21,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible to torch", allow_module_level=True)
 
+import blocks_plans  # noqa: E402
 import ortho_model as model  # noqa: E402
 import vocabulary_cross_entropy_row_amd as lce  # noqa: E402
 
@@ -82,3 +83,17 @@ def test_values_that_grow(kind, steps, abc):
     limit = want.abs() * (2.0 ** -8 + 2.0 ** -20) + 3 * (like - want).abs().max()
     off = (got - want).abs()
     assert bool((off <= limit).all()), f"worst {float(off.max()):.3g} of {float(want.abs().max()):.3g}, limit {float(limit.max()):.3g}"
+
+
+@pytest.mark.parametrize("steps", [2, 8])
+@pytest.mark.parametrize("batch,r,c", blocks_plans.ORTHO_COVER)
+def test_every_kernel_without_and_with_the_rest(batch, r, c, steps):
+    """Two steps take fp16's X alone in B X from 65 rows on, eight the rest too."""
+    assert not model.takes_rest(65, 2, model.ABC) and model.takes_rest(2007, 8, model.ABC)
+    G = torch.stack([model.matrix(r, c, k, 3 * (k % 2), device=DEV) for k in range(batch)])
+    got = lce.lce_orthogonalise(G, steps=steps).double()
+    for k in {0, 1 % batch, batch - 1}:
+        want, like = model.defined(G[k], steps), model.rounded(G[k], steps)
+        limit = math.hypot(1.1 * 2.0 ** -8 / math.sqrt(3) * float(want.norm()), 3 * float((like - want).norm()))
+        off = float((got[k] - want).norm())
+        assert off <= limit, f"matrix {k}: {off:.3g} of {limit:.3g}"

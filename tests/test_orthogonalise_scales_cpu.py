@@ -5,15 +5,21 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import blocks_plans  # noqa: E402
 import ortho_model as model  # noqa: E402
 import vocabulary_cross_entropy_row_amd as lce  # noqa: E402
 
 
 @pytest.fixture(scope="module")
-def chosen(tmp_path_factory):
+def plans(tmp_path_factory):
     if shutil.which("g++") is None:
         pytest.skip("g++ not available")
     return model.load(str(tmp_path_factory.mktemp("scales")))
+
+
+@pytest.fixture(scope="module")
+def chosen(plans):
+    return plans[0]
 
 
 COEFFICIENTS = [model.ABC, (1.5, -0.5, 0.0), (2.0, -1.5, 0.5), (3.0, -3.2, 1.2), (4.0, 0.0, 0.0), (12.0, 0.0, 0.0), (0.0, 1.0, 0.0),
@@ -62,3 +68,12 @@ def test_growth_past_the_limit_is_refused(steps, abc):
                                        (100, (1.0, 0.0, 0.0)), (3, (15.0, 0.0, 0.0)), (50, (0.0, 0.0, 0.0))])
 def test_other_coefficients_are_not(steps, abc):
     assert call(steps, abc)[0] == lce.LCE_OK
+
+
+def test_sizes_of_the_gpu_test_take_every_kernel(plans):
+    """B X without the rest (two steps) and with it (eight) in every shape of tile."""
+    sizes = [size for size in blocks_plans.ORTHO_COVER if min(size[1:]) > 64]
+    for rest in (False, True):
+        assert {plans[1](*size, rest) for size in sizes} == set(range(len(blocks_plans.ORTHO_SHAPES)))
+    for size in sizes:
+        assert [plans[0](min(size[1:]), steps, model.ABC)[3] for steps in (2, 8)] == [False, True]
