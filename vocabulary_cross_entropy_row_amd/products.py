@@ -41,14 +41,17 @@ def _scale_shape(n: int, K: int, tile: bool):
     return (-(-n // 128) if tile else n), -(-K // 128)
 
 
-def _new(n: int, K: int, tile: bool, dtype, device):
-    """(values [n, K], their row stride, scales, their strides): rows on 16 bytes, and scales of row blocks
-    block by block, for the product reads those of 16 rows together."""
+def _new_values(n: int, K: int, device):
+    """(values [n, K], their row stride): rows on 16 bytes."""
     ld = _up(K, 16)
+    return torch.empty_strided((n, K), (ld, 1), dtype=E4M3, device=device), ld
+
+
+def _new_scale(n: int, K: int, tile: bool, dtype, device):
+    """(scales, their strides): those of row blocks block by block, for the product reads those of 16 rows together."""
     rows, cols = shape = _scale_shape(n, K, tile)
     order = (cols, 1) if tile else (1, rows)
-    return (torch.empty_strided((n, K), (ld, 1), dtype=E4M3, device=device), ld,
-            torch.empty_strided(shape, order, dtype=dtype, device=device), *order)
+    return torch.empty_strided(shape, order, dtype=dtype, device=device), *order
 
 
 def _scale(t, name: str, n: int, K: int, tile: bool, device):
@@ -67,21 +70,18 @@ def _scale(t, name: str, n: int, K: int, tile: bool, device):
     return row, col, code
 
 
-def _given(values, scale, names, n: int, K: int, tile: bool, dtype, device):
-    """What _new gives, with the outputs that the caller brought."""
-    new = _new(n, K, tile, dtype, device)
-    ld, order = new[1], new[3:]
+def _outputs(values, scale, names, n: int, K: int, tile: bool, dtype, device):
+    """(values, their row stride, scales, their strides): those that the caller brought, checked, and new ones."""
     if values is None:
-        values = new[0]
+        values, ld = _new_values(n, K, device)
     else:
         ld = _rows(values, names[0], E4M3, n, K, device)
     if scale is None:
-        scale = new[2]
-    else:
-        *order, code = _scale(scale, names[1], n, K, tile, device)
-        if code != _SCALES[dtype]:
-            raise TypeError(f"{names[1]} must be {dtype} (got {scale.dtype})")
-    return (values, ld, scale, *order)
+        return values, ld, *_new_scale(n, K, tile, dtype, device)
+    *order, code = _scale(scale, names[1], n, K, tile, device)
+    if code != _SCALES[dtype]:
+        raise TypeError(f"{names[1]} must be {dtype} (got {scale.dtype})")
+    return values, ld, scale, *order
 
 
 @_call_stream
@@ -113,17 +113,11 @@ def lce_quantize_blocks(x, *, blocks: str | None = "row", transposed: str | None
     scode = _SCALES[scale_dtype]
     if blocks is not None:
         kind = _blocks(blocks, "blocks")
-        if values is None and scale is None:
-            values, ldv, scale, s_row, s_col = _new(n, K, kind == 1, scale_dtype, dev)
-        else:
-            values, ldv, scale, s_row, s_col = _given(values, scale, ("values", "scale"), n, K, kind == 1, scale_dtype, dev)
+        values, ldv, scale, s_row, s_col = _outputs(values, scale, ("values", "scale"), n, K, kind == 1, scale_dtype, dev)
     if transposed is not None:
         kind_t = _blocks(transposed, "transposed")
-        if values_t is None and scale_t is None:
-            values_t, ldvt, scale_t, st_row, st_col = _new(K, n, kind_t == 1, scale_dtype, dev)
-        else:
-            values_t, ldvt, scale_t, st_row, st_col = _given(values_t, scale_t, ("values_t", "scale_t"), K, n, kind_t == 1,
-                                                             scale_dtype, dev)
+        values_t, ldvt, scale_t, st_row, st_col = _outputs(values_t, scale_t, ("values_t", "scale_t"), K, n, kind_t == 1,
+                                                           scale_dtype, dev)
     _check(lib().lce_quantize_blocks(x.data_ptr(), ldx, code, n, K, _ptr(values), ldv, kind, _ptr(scale), s_row, s_col,
                                      _ptr(values_t), ldvt, kind_t, _ptr(scale_t), st_row, st_col, scode, stream))
     return BlocksResult(values, scale, values_t, scale_t)
