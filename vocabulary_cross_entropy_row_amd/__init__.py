@@ -43,9 +43,21 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m vocabulary_cross_entropy_row_amd.build` (there is no CPU fallback)")
     L = ctypes.CDLL(LIB_PATH)
+    try:   # the version before any other entry point: an older library lacks some
+        L.lce_abi_version.restype = ctypes.c_int
+        L.lce_abi_version.argtypes = []
+        if L.lce_abi_version() != ABI_VERSION:
+            raise ImportError("liblce.so ABI version mismatch; rebuild it")
+        _declare(L)
+    except AttributeError as e:
+        raise ImportError(f"liblce.so lacks an entry point of this binding ({e}); rebuild it") from None
+    _lib = L
+    return L
+
+
+def _declare(L) -> None:
+    """Types of the entry points' arguments and results."""
     p, i64, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
-    L.lce_abi_version.restype = ctypes.c_int
-    L.lce_abi_version.argtypes = []
     L.lce_last_error.restype = ctypes.c_char_p
     L.lce_last_error.argtypes = []
     L.lce_ce_workspace_bytes.restype = ctypes.c_size_t
@@ -122,10 +134,6 @@ def lib() -> ctypes.CDLL:
     L.lce_orthogonalise.argtypes = [p, i64, i64, ci, i64, i64, i64, ci, f32, f32, f32, f32, p, i64, i64, p, sz, p]
     L.lce_orthogonalise_workspace_bytes.restype = sz
     L.lce_orthogonalise_workspace_bytes.argtypes = [i64, i64, i64]
-    if L.lce_abi_version() != ABI_VERSION:
-        raise ImportError("liblce.so ABI version mismatch; rebuild it")
-    _lib = L
-    return L
 
 
 def lce_last_error() -> str:
