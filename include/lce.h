@@ -468,7 +468,8 @@ lce_status lce_logits_process(const void *logits, int64_t ldx, lce_dtype dtype, 
  *                 e4m3 output of lce_rms_norm is such an x).  Either scale may be
  *                 NULL (ones); both must be NULL for BF16.
  *   bias          device [M] F32 or BF16 (bias_dtype), or NULL.
- *   residual      device [n, ldr], out_dtype, or NULL; may be `out` itself.
+ *   residual      device [n, ldr], out_dtype, or NULL; may be `out` itself, with its
+ *                 row stride.
  *   out           device [n, ldo], out_dtype: BF16, or F32 with BF16 operands.  (The
  *                 8-bit matrix instructions cut each group of eight products to
  *                 2^-13 of its largest before the fp32 sum: 2^4 finer than a bf16
@@ -565,7 +566,8 @@ lce_status lce_quantize_blocks(const void *x, int64_t ldx, lce_dtype dtype, int6
  *                 product scale_x scale_w is formed first, in fp32 (below 2^-126 it has
  *                 fewer bits).
  *   bias          device [M] F32 or BF16, or NULL.
- *   residual      device bf16 [n, ldr], or NULL; may be `out` itself.
+ *   residual      device bf16 [n, ldr], or NULL; may be `out` itself, with its
+ *                 row stride.
  *   out           device bf16 [n, ldo].
  *   preact        device bf16 [n, ldp], or NULL: z rounded.
  *   workspace     device, 16-byte aligned, lce_linear_blocks_workspace_bytes(...)

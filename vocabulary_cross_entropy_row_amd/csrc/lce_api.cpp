@@ -535,6 +535,14 @@ lce_status check_apart(const char *fn, const char *out_name, const void *out, co
     return out && out == in ? fail(LCE_ERR_INVALID_ARG, "%s: %s must not be %s", fn, out_name, in_name) : LCE_OK;
 }
 
+// A residual in the place of the output: each value is read where it is written, if the rows are the same.
+lce_status check_residual(const char *fn, const void *residual, int64_t ldr, const void *out, int64_t ldo, int64_t n) {
+    return residual && residual == out && n > 1 && ldr != ldo
+               ? fail(LCE_ERR_INVALID_ARG, "%s: a residual in the place of out must have its row stride (%lld, got %lld)", fn,
+                      (long long)ldo, (long long)ldr)
+               : LCE_OK;
+}
+
 lce_status check_norm_sizes(const char *fn, int64_t n, int64_t H, lce_dtype dtype, const void *weight,
                             lce_dtype weight_dtype, float weight_offset) {
     if (n < 0) return fail(LCE_ERR_INVALID_ARG, "%s: n must be >= 0 (got %lld)", fn, (long long)n);
@@ -813,7 +821,8 @@ lce_status lce_linear(const void *x, int64_t ldx, const void *weight, int64_t ld
     if (preact && (preact == residual || preact == out))
         return fail(LCE_ERR_INVALID_ARG, "%s: preact must not be residual or out", fn);
     if ((st = check_apart(fn, "out", out, "bias", bias)) != LCE_OK ||
-        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK)
+        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK ||
+        (st = check_residual(fn, residual, ldr, out, ldo, n)) != LCE_OK)
         return st;
     lce::LinearArgs a{};
     a.x = x;
@@ -1051,7 +1060,8 @@ lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, in
     if (preact && (preact == residual || preact == out))
         return fail(LCE_ERR_INVALID_ARG, "%s: preact must not be residual or out", fn);
     if ((st = check_apart(fn, "out", out, "bias", bias)) != LCE_OK ||
-        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK)
+        (st = check_apart(fn, "preact", preact, "bias", bias)) != LCE_OK ||
+        (st = check_residual(fn, residual, ldr, out, ldo, n)) != LCE_OK)
         return st;
     lce::BlocksArgs a{};
     a.x = x;
@@ -1120,6 +1130,7 @@ lce_status lce_linear_blocks_forward(const void *x, int64_t ldx, const void *wei
         for (int j = 0; j < i; ++j)
             if (outs[i] && outs[i] == outs[j]) return fail(LCE_ERR_INVALID_ARG, "%s: two outputs are the same buffer", fn);
     }
+    if ((st = check_residual(fn, residual, ldr, out, ldo, n)) != LCE_OK) return st;
     lce::BlocksForwardArgs a{};
     a.x = x;
     a.weight = weight;
