@@ -38,3 +38,9 @@ def test_only_what_is_missing_is_allocated(blocks):
     assert 0 < room <= 2 * want.scale.numel() + 512
     room = allocated(lambda: lce.lce_quantize_blocks(x, blocks=blocks, scale=given["scale"]))
     assert n * K <= room <= n * K + 2 ** 21
+
+
+@pytest.mark.parametrize("name", ["values", "scale", "values_t", "scale_t"])
+def test_outputs_that_are_no_tensors_are_refused(name):
+    with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
+        lce.lce_quantize_blocks(torch.zeros(4, 130, device=DEV), transposed="row", **{name: [1.0]})

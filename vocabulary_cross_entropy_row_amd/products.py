@@ -106,7 +106,7 @@ def lce_quantize_blocks(x, *, blocks: str | None = "row", transposed: str | None
         raise ValueError("values_t and scale_t go with transposed")
     if scale_dtype is None:
         first = scale if scale is not None else scale_t
-        scale_dtype = E8M0 if first is None else first.dtype
+        scale_dtype = first.dtype if torch.is_tensor(first) else E8M0
     if scale_dtype not in _SCALES:
         raise TypeError(f"scale_dtype must be float8_e8m0fnu or float32 (got {scale_dtype})")
     kind = kind_t = ldv = ldvt = s_row = s_col = st_row = st_col = 0
