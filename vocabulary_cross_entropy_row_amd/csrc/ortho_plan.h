@@ -15,8 +15,8 @@ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
 constexpr int kSide[SHAPES] = {256, 128, 64, 128, 32}, kPerCu[SHAPES] = {1, 2, 2, 1, 2};
 // us of a step of 64 of K with one and two workgroups on a compute unit, and of a tile's start and end.
-// Fitted to the times of all five steps over 260 random shapes (batches of 1 to 16, 32 to 16384 rows and
-// columns) with each shape for each product, replayed from a graph: off by 12% (root mean square), and the
+// Fitted to the times of all five steps over 221 random shapes (batches of 1 to 16, 65 to 16384 rows and
+// columns, fp16's X alone in B X) with each shape for each product, replayed from a graph: off by 12% (root mean square), and the
 // choice that the estimates make 2% slower than the fastest measured one on geometric average.
 constexpr double kStepUs[SHAPES][2] = {{1.03, 0}, {0.65, 0.94}, {0.33, 0.33}, {0.45, 0}, {0.27, 0.57}};
 constexpr double kTileUs[SHAPES] = {12.0, 3.4, 2.1, 4.3, 2.1};

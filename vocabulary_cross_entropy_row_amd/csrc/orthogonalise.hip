@@ -762,7 +762,6 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(oc[u], ot[u], sum, 0, 0, 0);
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int c = wave * 32 + r * 8 + half * 4;
@@ -824,14 +823,15 @@ __global__ __launch_bounds__(512, 2) void apply_short_kernel(Args g) {
     }
 }
 
-// Adds pieces k .. k + N - 1, up to the last, to v; all of their loads are under way at once.
+// Adds pieces k .. k + N - 1, up to the last, to v; all of their loads are under way at once.  The first one ends
+// its range, the others start theirs.
 template <int N>
-__device__ __forceinline__ int add_pieces(const float *p, int size, int first, int first_slot, int k, int last, float (&v)[4]) {
+__device__ __forceinline__ int add_pieces(const float *p, int size, int first, int k, int last, float (&v)[4]) {
     float4 x[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const int i = min(k + u, last);
-        x[u] = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i == first ? first_slot : 2 * i) * size);
+        x[u] = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(2 * i + (i == first ? 1 : 0)) * size);
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
@@ -862,13 +862,12 @@ __global__ __launch_bounds__(256) void fold_kernel(Args g) {
     triangle(tile - z * g.per_batch, ti, fi);
     const int tp = part / ACROSS * kFoldRows, fp = part % ACROSS * 64, t0 = ti * SIDE + tp, f0 = fi * SIDE + fp;
     if (t0 >= g.rows_x || f0 >= g.rows_w) return;   // rows come in 64s
-    const int first_slot = 2 * first + (range_start(units, g.groups, first) <= from ? 1 : 0);
     const int tl = th >> 4, fl = (th & 15) * 4, t = t0 + tl, f = f0 + fl;
     float v[4] = {};
     const float *p = g.part + static_cast<int64_t>(tp + tl) * SIDE + fp + fl;
     int k = first;
-    while (last - k >= 4) k += add_pieces<24>(p, SIDE * SIDE, first, first_slot, k, last, v);
-    if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, first_slot, k, last, v);
+    while (last - k >= 4) k += add_pieces<24>(p, SIDE * SIDE, first, k, last, v);
+    if (k <= last) add_pieces<4>(p, SIDE * SIDE, first, k, last, v);
     gram_values(g, z, t, f, v);
     *reinterpret_cast<uint2 *>(g.o + z * g.ob + static_cast<int64_t>(t) * g.ldo + f) = pack_h4(v);
     if (ti == fi) return;

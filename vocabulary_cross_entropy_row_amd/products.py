@@ -16,7 +16,6 @@ from .head import (LinearGrads, LinearResult, _CODES, _activation, _call_stream,
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _SCALES = {torch.float32: LCE_F32, E8M0: LCE_E8M0}
 BLOCKS = {"row": 0, "tile": 1}
-_MAX_LD = (1 << 24) - 1024   # bytes between the rows of an operand, as the product reads them
 
 
 @dataclass
