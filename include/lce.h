@@ -528,6 +528,7 @@ size_t lce_linear_backward_workspace_bytes(int64_t n, int64_t K, int64_t M);
  * shorter, with a scale for each: of one row (LCE_BLOCKS_ROW, scales [rows,
  * ceil(K / 128)]) or of 128 rows (LCE_BLOCKS_TILE, scales [ceil(rows / 128),
  * ceil(K / 128)]).  Scale (i, b) lies s_row i + s_col b elements from the first.
+ * Workspace queries return 0 for sizes that the calls refuse.
  */
 typedef enum { LCE_BLOCKS_ROW = 0, LCE_BLOCKS_TILE = 1 } lce_blocks;
 

@@ -1023,7 +1023,7 @@ lce_status lce_quantize_blocks(const void *x, int64_t ldx, lce_dtype dtype, int6
 }
 
 size_t lce_linear_blocks_workspace_bytes(int64_t n, int64_t K, int64_t M) {
-    if (n < 0 || K < 1 || M < 1) return 0;
+    if (check_blocks_sizes("lce_linear_blocks_workspace_bytes", n, K, M) != LCE_OK || K > lce::kLinearMaxStride) return 0;
     return lce::linear_blocks_workspace_bytes(n, K, M);
 }
 
@@ -1087,7 +1087,7 @@ lce_status lce_linear_blocks(const void *x, int64_t ldx, const void *scale_x, in
 }
 
 size_t lce_linear_blocks_forward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
-    if (n < 0 || K < 1 || M < 1) return 0;
+    if (check_training_sizes("lce_linear_blocks_forward_workspace_bytes", n, K, M) != LCE_OK) return 0;
     return lce::linear_blocks_forward_workspace_bytes(n, K, M);
 }
 
@@ -1156,7 +1156,7 @@ lce_status lce_linear_blocks_forward(const void *x, int64_t ldx, const void *wei
 }
 
 size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t M) {
-    if (n < 0 || K < 1 || M < 1) return 0;
+    if (check_training_sizes("lce_linear_blocks_backward_workspace_bytes", n, K, M) != LCE_OK) return 0;
     return lce::linear_blocks_backward_workspace_bytes(n, K, M);
 }
 
