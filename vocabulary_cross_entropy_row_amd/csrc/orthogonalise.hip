@@ -23,9 +23,9 @@
 // B, of 64 rows at most, is formed by the workgroups that use it).  Everything is padded with zeros to multiples
 // of 64, so the products meet no edges.
 //
-// 4096 x 16384 in five steps takes 4.9 to 5.2 ms, 0.86 to 0.92 PFLOP/s where a library fp16 product reaches
-// 1.4 to 1.5: a step is X X^T (327 us, 136 tiles on 256 compute units, whose matrix units are busy 40% of the time),
-// A A (92, the same tiles and a quarter of the depth) and B X (554; busy 53% at the 1.77 GHz that
+// 4096 x 16384 in five steps takes 4.9 to 5.0 ms, 0.89 to 0.91 PFLOP/s where a library fp16 product reaches
+// 1.4 to 1.5: a step is X X^T (321 to 332 us, 136 tiles on 256 compute units, whose matrix units are busy 41% of the time),
+// A A (92 to 99, the same tiles and a quarter of the depth) and B X (554 to 569; busy 54% at the 1.7 GHz that
 // their power leaves; 440 of it the main loop, the rest its ends, which read and write 0.7 GB of X).  Small
 // ones are their launches: 256 x 1024, 17 launches, 98 us from a graph, 9 of them for the rest in B X.
 // The steps: tiles chosen for each product, instructions held in place between LDS reads (1003 x 517 x 4 161 ->
@@ -153,8 +153,8 @@ __global__ __launch_bounds__(256) void norm_kernel(LoadArgs a) {
     if (threadIdx.x == 0) a.part[blockIdx.y * kNormGroups + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
-// A workgroup takes 64 x 64 of X: hi, lo and the transposed hi, zeros in the padding (4096 x 16384 bf16: 97 us,
-// 4.8 TB/s of what it reads and writes).
+// A workgroup takes 64 x 64 of X: hi, lo and the transposed hi (and lo, where B X takes it), zeros in the padding
+// (4096 x 16384 bf16: 97 us, 5.5 TB/s of what it reads and writes).
 template <bool BF16>
 __global__ __launch_bounds__(256) void load_kernel(LoadArgs a) {
     __shared__ float tile[64][65];
@@ -706,7 +706,7 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
 }
 
 // Up to 64 rows, B is little work: every workgroup of B X forms the 32 rows of it that it needs, from O and
-// its diagonal, in LDS, instead of a launch that forms it for all (64 x 64 54 -> 42 us; with 128 rows that
+// its diagonal, in LDS, instead of a launch that forms it for all (64 x 64 54 -> 42 us, 48 with the rest of X; with 128 rows that
 // takes longer than the launch, 16 x 128 x 512 71 -> 91).  A workgroup takes 32 rows of X and 256
 // columns, 32 to a wave; everything that it reads is asked for at its start.
 constexpr int kShortRows = 64;
