@@ -99,3 +99,16 @@ def test_every_kernel_without_and_with_the_rest(batch, r, c, steps):
         limit = math.hypot(1.1 * 2.0 ** -8 / math.sqrt(3) * float(want.norm()), 3 * float((like - want).norm()))
         off = float((got[k] - want).norm())
         assert off <= limit, f"matrix {k}: {off:.3g} of {limit:.3g}"
+
+
+@pytest.mark.parametrize("norm", [1e-7, 1e-9, 1e-12, 1e-14])
+@pytest.mark.parametrize("r,c", [(60, 90), (300, 200)])
+def test_gradients_next_to_eps_and_far_below(r, c, norm):
+    G = model.matrix(r, c, 4, device=DEV)
+    G = G * (norm / float(G.norm()))
+    got = lce.lce_orthogonalise(G, eps=1e-7).double()
+    want, like = model.defined(G), model.rounded(G)
+    limit = want.abs() * (2.0 ** -8 + 2.0 ** -20) + 3 * (like - want).abs().max()
+    assert bool(((got - want).abs() <= limit).all())
+    if norm >= 1e-12:   # X's steps of 2^-38 are far below its values of norm / eps / sqrt(r c), 4e-8 at the least
+        assert float((like - want).norm()) <= 2e-3 * float(want.norm())
