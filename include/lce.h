@@ -653,11 +653,11 @@ size_t lce_linear_blocks_backward_workspace_bytes(int64_t n, int64_t K, int64_t 
  * singular values from about 0.002 to 1 to between 0.7 and 1.2.  The products run in fp16
  * with fp32 sums; X is held in two fp16 (22 bits, in steps of 2^-38 at the least, which a G
  * far below eps meets; up to 2^-31 under coefficients that make values grow), the diagonals
- * of A and b A + c A A in fp32.  With five steps of those coefficients the result is off by up to 1.4e-3 of it
- * (Frobenius norm; 2-norm 1.9e-3) before it is rounded to bf16, matrices of few directions
- * included, and by up to 6e-3 below 64 rows.  Coefficients that can take singular
- * values of 0 to 1 past 256 before the last step are refused (LCE_ERR_UNSUPPORTED,
- * whatever g is); short of that no step overflows.
+ * of A and b A + c A A in fp32.  With five steps of those coefficients the result is off
+ * by up to 1.4e-3 of it (Frobenius norm; 2-norm 1.9e-3) before it is rounded to bf16,
+ * matrices of few directions included, and by up to 6e-3 below 64 rows.  Coefficients
+ * that can take singular values of 0 to 1 past 256 before the last step are refused
+ * (LCE_ERR_UNSUPPORTED, whatever g is); short of that no step overflows.
  *   g           device [batch][rows, cols], row stride ldg and g_batch_stride elements
  *               between matrices, dtype F32 or BF16.  A matrix of zeros gives zeros (eps
  *               above 0); one that holds an infinity or a NaN gives NaN, in itself alone.

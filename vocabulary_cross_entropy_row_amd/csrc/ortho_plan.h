@@ -16,8 +16,9 @@ enum { BIG, MID, SMALL, MID_DEEP, FINE, SHAPES };   // FINE: fine_kernel
 constexpr int kSide[SHAPES] = {256, 128, 64, 128, 32}, kPerCu[SHAPES] = {1, 2, 2, 1, 2};
 // us of a step of 64 of K with one and two workgroups on a compute unit, and of a tile's start and end.
 // Fitted to the times of all five steps over 221 random shapes (batches of 1 to 16, 65 to 16384 rows and
-// columns, fp16's X alone in B X) with each shape for each product, replayed from a graph: off by 12% (root mean square), and the
-// choice that the estimates make 2% slower than the fastest measured one on geometric average.
+// columns, fp16's X alone in B X) with each shape for each product, replayed from a graph: off by 12% (root
+// mean square), and the choice that the estimates make 2% slower than the fastest measured one on geometric
+// average.
 constexpr double kStepUs[SHAPES][2] = {{1.03, 0}, {0.65, 0.94}, {0.33, 0.33}, {0.45, 0}, {0.27, 0.57}};
 constexpr double kTileUs[SHAPES] = {12.0, 3.4, 2.1, 4.3, 2.1};
 constexpr double kEven = 1.94;   // a step where workgroups are at different places of K and share less in the caches
@@ -113,7 +114,8 @@ inline Powers powers_of(int64_t r, int steps, double a, double b, double c) {
         x = std::max(x, m);
         o = std::max(o, m * m);
         p = std::max(p, peak_b(b, c, m * m));
-        s.fit = m <= kMaxValue && std::fabs(a) <= kMaxTerm && std::fabs(b) * m * m <= kMaxTerm && std::fabs(c) * m * m * m * m <= kMaxTerm;
+        s.fit = m <= kMaxValue && std::fabs(a) <= kMaxTerm && std::fabs(b) * m * m <= kMaxTerm &&
+                std::fabs(c) * m * m * m * m <= kMaxTerm;
         m = peak(a, b, c, m) * (1.0 + 0x1p-8);   // and what the roundings add
     }
     auto power = [](double v, int most) {

@@ -11,8 +11,9 @@
 //   A, B   their diagonals in fp32 vectors, the rest in fp16.  X approaches orthogonal rows, so A
 //          approaches its diagonal: A = D + O gives A A = O O + (D_t + D_f) O + D^2, and B X = diag X + rest.
 // With these roundings put into the definition (gaussian matrices with even and uneven rows, of 1 to 16
-// directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.4e-3 of the result in the
-// Frobenius norm and 1.9e-3 in the 2-norm from 64 rows on, and by up to 5e-3 and 6e-3 below; the bf16 output rounds at 1.7e-3.
+// directions, and with singular values that fall as 1 / k), five default steps are off by up to 1.4e-3 of the
+// result in the Frobenius norm and 1.9e-3 in the 2-norm from 64 rows on, and by up to 5e-3 and 6e-3 below; the
+// bf16 output rounds at 1.7e-3.
 // Powers of two keep fp16 in range, for the default coefficients X times 2^14 (its values are at most 1.21), O times
 // 2^10 and B times 2^8 (ortho_plan.h).
 //
@@ -403,7 +404,8 @@ __global__ __launch_bounds__(64 * S::NW, S::NW * S::PER_CU / 4) void ortho_kerne
         else if (q < LA + LB)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsB, (lds_ptr)(lds + SA * S::A_BYTES + slot_b * S::B_BYTES + ((q - LA) * S::NW + wave) * 1024), 16,
-                voffB[q < LA ? 0 : q - LA], (kbeg + min(sx, last) - (SYM || kbeg + min(sx, last) < steps_x ? 0 : steps_x)) * kStep, 0, 0);
+                voffB[q < LA ? 0 : q - LA],
+                (kbeg + min(sx, last) - (SYM || kbeg + min(sx, last) < steps_x ? 0 : steps_x)) * kStep, 0, 0);
     };
     auto frag = [&](const unsigned char *tile_at, int q, int kk) {   // 32-row tile q, instruction kk of the step
         const int r = q * 32 + (lane & 31);
@@ -706,8 +708,8 @@ __global__ __launch_bounds__(64 * kFineWaves, 2) void fine_kernel(Args g) {
 }
 
 // Up to 64 rows, B is little work: every workgroup of B X forms the 32 rows of it that it needs, from O and
-// its diagonal, in LDS, instead of a launch that forms it for all (64 x 64 54 -> 42 us, 48 with the rest of X; with 128 rows that
-// takes longer than the launch, 16 x 128 x 512 71 -> 91).  A workgroup takes 32 rows of X and 256
+// its diagonal, in LDS, instead of a launch that forms it for all (64 x 64 54 -> 42 us, 48 with the rest of X;
+// with 128 rows that takes longer than the launch, 16 x 128 x 512 71 -> 91).  A workgroup takes 32 rows of X and 256
 // columns, 32 to a wave; everything that it reads is asked for at its start.
 constexpr int kShortRows = 64;
 constexpr int kShortCols = 256;
